@@ -42,6 +42,9 @@ typedef enum {
     DG_ERR_ARG = 6          /* another argument (a launch override) is invalid     */
 } dg_status;
 
+/* Element types of the calls that take a `dtype`. */
+enum { DG_DTYPE_F32 = 0, DG_DTYPE_F16 = 1, DG_DTYPE_BF16 = 2 };
+
 /* A hipStream_t, kept opaque so that this header needs no HIP include. */
 typedef void* dg_stream;
 
@@ -384,6 +387,47 @@ dg_status dg_quantize_q8_0(const float* w, void* Wq, int64_t N, int64_t K,
                            dg_stream stream);
 
 /* ------------------------------------------------------------------------
+ * RMS norm with the residual's addition, into Q8_1 columns or float rows
+ *
+ *   h[m][k] = T(x[m][k] + res[m][k])      (h = x without res)
+ *   r[m]    = binary32(1 / sqrt(sum_k h[m][k]^2 / K + eps))
+ *   y[m][k] = (h[m][k] * r[m]) * w[k]
+ *
+ * The step between the GEMVs of a decoder layer: the previous GEMV's output
+ * (or the embedding) joins the residual stream and the norm of the sum is the
+ * next GEMV's input.  dg_rmsnorm_q8_1 stores y as the Q8_1 columns that the
+ * quantised GEMVs read, byte for byte what dg_quantize_q8_1 makes of it;
+ * dg_rmsnorm stores it in binary32, binary16 or bfloat16 (the dense GEMVs'
+ * x).  One launch.
+ *
+ * The binary32 sum x + res is rounded once, to the storage type T of x, res
+ * and h, and the norm is that of the rounded values, so that it is the norm of
+ * what h stores.  The sum of squares, the division by K, eps, the root and
+ * the reciprocal are binary64, rounded once to r; the two products are
+ * binary32, then the Q8_1 rules or one rounding to the output type.  Results
+ * are bit-reproducible.  For Q8_1 output the y of a row must be finite.
+ *
+ *   x       device [M][ld] of `dtype`, aligned to the element; K of ld used.
+ *   res     as x, or NULL: no addition.
+ *   h       as x, receives the sum; or NULL (required without res).  h may be
+ *           x or res itself; otherwise no two operands may overlap.
+ *   w       device [K] of `wdtype`, aligned to the element.
+ *   Xq      device, M columns of K/32 Q8_1 blocks (36 bytes each), 4-byte
+ *           aligned (16-byte for the GEMVs that read it).
+ *   y       device [M][ldy] of `ydtype`, aligned to the element; columns K..
+ *           ldy-1 are left as they are (and those of h).
+ *   M       rows, 0 <= M < 2^31.  K: 0 <= K <= 2^26, a multiple of 32 for
+ *           Q8_1.  K <= ld, ldy < 2^31.  M = 0 or K = 0 launches nothing.
+ *   eps     > 0 and finite.
+ * Errors: DG_ERR_ARG (unknown type, eps, h without res), DG_ERR_SHAPE,
+ * DG_ERR_NULL, DG_ERR_MISALIGNED, DG_ERR_HIP.
+ * ------------------------------------------------------------------------ */
+dg_status dg_rmsnorm_q8_1(const void* x, const void* res, void* h, int dtype, const void* w, int wdtype, void* Xq,
+                          int64_t M, int64_t K, int64_t ld, float eps, dg_stream stream);
+dg_status dg_rmsnorm(const void* x, const void* res, void* h, int dtype, const void* w, int wdtype, void* y, int ydtype,
+                     int64_t M, int64_t K, int64_t ld, int64_t ldy, float eps, dg_stream stream);
+
+/* ------------------------------------------------------------------------
  * argmax over rows (greedy sampling), lowest index on ties
  *
  *   idx[r] = min{ c < C : x[r*ld + c] = max_{c'<C} x[r*ld + c'] }
@@ -483,7 +527,6 @@ dg_status dg_gemv_bf16_argmax(const void* W, const void* x, float* y, int64_t* i
  * Errors: DG_ERR_NULL, DG_ERR_MISALIGNED, DG_ERR_SHAPE, DG_ERR_WORKSPACE,
  * DG_ERR_ARG (unknown dtype or op), DG_ERR_HIP.
  * ------------------------------------------------------------------------ */
-enum { DG_DTYPE_F32 = 0, DG_DTYPE_F16 = 1, DG_DTYPE_BF16 = 2 };
 enum { DG_ARG_MAX = 0, DG_ARG_MIN = 1 };
 
 dg_status dg_argcompare_rows(const void* x, int dtype, int op, int64_t* idx, int64_t R, int64_t C,

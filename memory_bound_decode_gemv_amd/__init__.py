@@ -78,6 +78,7 @@ EXPORTED = (
     "dg_gemv_q4_0_tiles", "dg_gemv_q4_0_tiles_ex",
     "dg_q8_0_tiles_bytes", "dg_repack_q8_0_tiles", "dg_gemv_q8_0_tiles_workspace_bytes",
     "dg_gemv_q8_0_tiles", "dg_gemv_q8_0_tiles_ex",
+    "dg_rmsnorm_q8_1", "dg_rmsnorm",
 )
 
 # Size of the library's fixed per-device argmax key array (include/decodegemv.h).
@@ -187,6 +188,11 @@ def _lib():
         getattr(lib, f"dg_gemv_{f}_tiles_ex").argtypes = [P, P, P, I64, I64, I32, P, ctypes.c_size_t,
                                                           ctypes.POINTER(dg_launch), P]
         getattr(lib, f"dg_gemv_{f}_tiles_ex").restype = st
+    F32 = ctypes.c_float
+    lib.dg_rmsnorm_q8_1.argtypes = [P, P, P, I32, P, I32, P, I64, I64, I64, F32, P]
+    lib.dg_rmsnorm_q8_1.restype = st
+    lib.dg_rmsnorm.argtypes = [P, P, P, I32, P, I32, P, I32, I64, I64, I64, I64, F32, P]
+    lib.dg_rmsnorm.restype = st
     _handle = lib
     return lib
 
@@ -224,6 +230,30 @@ def _need(t, dtypes, name):
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _dtype_id(t, name):
+    """The DG_DTYPE_* of a float tensor."""
+    torch = _torch()
+    ids = {torch.float32: DG_DTYPE_F32, torch.float16: DG_DTYPE_F16, torch.bfloat16: DG_DTYPE_BF16}
+    if t.dtype not in ids:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(ids)}")
+    return ids[t.dtype]
+
+
+def _need_here(**tensors):
+    """Raises unless every given tensor is contiguous on the current device: a
+    call runs there, on its current stream."""
+    dev = _torch().cuda.current_device()
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
 def _fits(t, nbytes, name):
@@ -534,6 +564,54 @@ def dg_quantize_q8_0(w, Wq, N, K, stream=None):
         _fits(Wq, int(N) * (int(K) // 32) * 34, "Wq")
     _check(_lib().dg_quantize_q8_0(_ptr(w), _ptr(Wq), int(N), int(K), _stream(stream)), "dg_quantize_q8_0")
     return Wq
+
+
+def _rmsnorm(x, w, out, res, h, eps, M, K, ld, ldy, stream):
+    _need_here(x=x, w=w, out=out, res=res, h=h)
+    dtype, wdtype = _dtype_id(x, "x"), _dtype_id(w, "w")
+    for name, t in (("res", res), ("h", h)):
+        if t is not None and t.dtype != x.dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, x has {x.dtype}")
+    if M is None:
+        M = x.shape[0] if x.dim() == 2 else 1
+    if K is None:
+        K = x.shape[-1]
+    if ld is None:
+        ld = x.shape[-1]
+    M, K, ld = int(M), int(K), int(ld)
+    if M > 0 and K > 0 and ld >= K:
+        need = ((M - 1) * ld + K) * x.element_size()
+        for name, t in (("x", x), ("res", res), ("h", h)):
+            if t is not None:
+                _fits(t, need, name)
+        _fits(w, K * w.element_size(), "w")
+    if ldy is None:   # Q8_1 columns
+        _need(out, (_torch().uint8,), "Xq")
+        if M > 0 and K > 0:
+            _fits(out, M * (K // 32) * 36, "Xq")
+        _check(_lib().dg_rmsnorm_q8_1(_ptr(x), _ptr(res), _ptr(h), dtype, _ptr(w), wdtype, _ptr(out), M, K, ld,
+                                      float(eps), _stream(stream)), "dg_rmsnorm_q8_1")
+        return out
+    ydtype, ldy = _dtype_id(out, "y"), int(ldy)
+    if M > 0 and K > 0 and ldy >= K:
+        _fits(out, ((M - 1) * ldy + K) * out.element_size(), "y")
+    _check(_lib().dg_rmsnorm(_ptr(x), _ptr(res), _ptr(h), dtype, _ptr(w), wdtype, _ptr(out), ydtype, M, K, ld, ldy,
+                             float(eps), _stream(stream)), "dg_rmsnorm")
+    return out
+
+
+def dg_rmsnorm_q8_1(x, w, Xq, res=None, h=None, eps=1e-5, M=None, K=None, ld=None, stream=None):
+    """Xq (uint8, M*K/32*36 bytes) = the Q8_1 columns of the RMS norm of x + res
+    (x: float32, float16 or bfloat16 [M][ld]; w: weights [K]); the sum is stored
+    in h (like x; may be x or res itself)."""
+    return _rmsnorm(x, w, Xq, res, h, eps, M, K, ld, None, stream)
+
+
+def dg_rmsnorm(x, w, y, res=None, h=None, eps=1e-5, M=None, K=None, ld=None, ldy=None, stream=None):
+    """y (float32, float16 or bfloat16 [M][ldy]) = the RMS norm of x + res (as dg_rmsnorm_q8_1)."""
+    if ldy is None:
+        ldy = y.shape[-1]
+    return _rmsnorm(x, w, y, res, h, eps, M, K, ld, ldy, stream)
 
 
 def dg_argmax_workspace_bytes(R, C):

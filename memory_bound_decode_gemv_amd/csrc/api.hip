@@ -135,6 +135,26 @@ dg_status gemv_nf4_checked(const void* codes, const float* absmax, const float* 
     return hip_status(e);
 }
 
+bool dtype_ok(int dtype) { return dtype == DG_DTYPE_F32 || dtype == DG_DTYPE_F16 || dtype == DG_DTYPE_BF16; }
+uintptr_t dtype_size(int dtype) { return dtype == DG_DTYPE_F32 ? 4 : 2; }
+
+// out_kind kRmsNormQ81 (Q8_1 columns) or a DG_DTYPE_* (float rows).
+dg_status rmsnorm_checked(const RmsNorm& a, dg_stream stream) {
+    const bool q81 = a.out_kind == kRmsNormQ81;
+    if (!dtype_ok(a.dtype) || !dtype_ok(a.wdtype) || (!q81 && !dtype_ok(a.out_kind))) return DG_ERR_ARG;
+    if (!(a.eps > 0.0f) || a.eps > 3.4028234e38f) return DG_ERR_ARG;
+    if (a.h && !a.res) return DG_ERR_ARG;
+    if (a.M < 0 || a.M > kI32Max || a.K < 0 || a.K > kQuantMaxK || (q81 && a.K % 32 != 0)) return DG_ERR_SHAPE;
+    if (a.ld < a.K || a.ld > kI32Max || a.ldy < a.K || a.ldy > kI32Max) return DG_ERR_SHAPE;
+    if (a.M == 0 || a.K == 0) return DG_OK;
+    if (!a.x || !a.w || !a.out) return DG_ERR_NULL;
+    const uintptr_t e = dtype_size(a.dtype);
+    if (!aligned(a.x, e) || !aligned(a.res, e) || !aligned(a.h, e) || !aligned(a.w, dtype_size(a.wdtype)) ||
+        !aligned(a.out, q81 ? 4 : dtype_size(a.out_kind)))
+        return DG_ERR_MISALIGNED;
+    return hip_status(launch_rmsnorm(a, (hipStream_t)stream));
+}
+
 }  // namespace
 
 int device_cu_count() {
@@ -346,6 +366,17 @@ dg_status dg_quantize_nf4(const float* w, void* codes, float* absmax, const floa
     if (!w || !codes || !absmax || !table) return DG_ERR_NULL;
     if (!aligned(w, 16) || !aligned(codes, 2) || !aligned(absmax, 4) || !aligned(table, 4)) return DG_ERR_MISALIGNED;
     return hip_status(launch_quantize_nf4(w, codes, absmax, table, N, K, B, (hipStream_t)stream));
+}
+
+dg_status dg_rmsnorm_q8_1(const void* x, const void* res, void* h, int dtype, const void* w, int wdtype, void* Xq,
+                          int64_t M, int64_t K, int64_t ld, float eps, dg_stream stream) {
+    return rmsnorm_checked({x, res, h, dtype, w, wdtype, Xq, kRmsNormQ81, M, K, ld, K, eps}, stream);
+}
+
+dg_status dg_rmsnorm(const void* x, const void* res, void* h, int dtype, const void* w, int wdtype, void* y, int ydtype,
+                     int64_t M, int64_t K, int64_t ld, int64_t ldy, float eps, dg_stream stream) {
+    if (!dtype_ok(ydtype)) return DG_ERR_ARG;
+    return rmsnorm_checked({x, res, h, dtype, w, wdtype, y, ydtype, M, K, ld, ldy, eps}, stream);
 }
 
 size_t dg_argmax_workspace_bytes(int64_t R, int64_t C) { return argmax_workspace_bytes(R, C); }

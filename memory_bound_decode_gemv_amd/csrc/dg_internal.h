@@ -121,6 +121,23 @@ hipError_t launch_quantize_nf4(const float* w, void* codes, float* absmax, const
 hipError_t launch_quantize_q8_1(const float* x, void* Xq, int64_t M, int64_t K, hipStream_t s);
 hipError_t launch_quantize_q4_0(const float* w, void* Wq, int64_t N, int64_t K, hipStream_t s);
 
+// RMS norm of M rows with the residual's addition (res, h may be NULL).
+// out_kind: a DG_DTYPE_* for float rows of stride ldy, or kRmsNormQ81 for
+// Q8_1 columns (K % 32 == 0).
+enum { kRmsNormQ81 = 3 };
+struct RmsNorm {
+    const void *x, *res;
+    void* h;
+    int dtype;
+    const void* w;
+    int wdtype;
+    void* out;
+    int out_kind;
+    int64_t M, K, ld, ldy;
+    float eps;
+};
+hipError_t launch_rmsnorm(const RmsNorm& a, hipStream_t s);
+
 size_t argmax_workspace_bytes(int64_t R, int64_t C);
 hipError_t launch_argmax_rows(const float* x, int64_t* idx, int64_t R, int64_t C, int64_t ld,
                               void* ws, hipStream_t s);

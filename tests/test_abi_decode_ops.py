@@ -1,0 +1,74 @@
+"""Argument checks of the operators around the decode GEMV, on the CPU: every refusal comes back before the HIP
+runtime is touched (fake device addresses, never dereferenced)."""
+import ctypes
+import os
+
+import pytest
+
+P = ctypes.c_void_p
+A = P(0x1000)
+OK, NULL, MISALIGNED, SHAPE, WORKSPACE, ARG = 0, 1, 2, 3, 4, 6
+F32, F16, BF16 = 0, 1, 2
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import memory_bound_decode_gemv_amd as m
+    if not os.path.exists(m.LIB_PATH):
+        from memory_bound_decode_gemv_amd import _build
+        _build.build()
+    return m.raw()
+
+
+@pytest.mark.parametrize("args,expect", [
+    ((A, A, A, 3, A, F32, A, 4, 64, 64, 1e-5), ARG),              # unknown type
+    ((A, A, A, F32, A, -1, A, 4, 64, 64, 1e-5), ARG),
+    ((A, A, A, F32, A, F32, A, 4, 64, 64, 0.0), ARG),             # eps
+    ((A, A, A, F32, A, F32, A, 4, 64, 64, -1.0), ARG),
+    ((A, A, A, F32, A, F32, A, 4, 64, 64, INF), ARG),
+    ((A, A, A, F32, A, F32, A, 4, 64, 64, float("nan")), ARG),
+    ((A, None, A, F32, A, F32, A, 4, 64, 64, 1e-5), ARG),         # a sum to store, without a residual
+    ((A, A, A, F32, A, F32, A, -1, 64, 64, 1e-5), SHAPE),
+    ((A, A, A, F32, A, F32, A, 1 << 31, 64, 64, 1e-5), SHAPE),
+    ((A, A, A, F32, A, F32, A, 4, 48, 64, 1e-5), SHAPE),          # K % 32
+    ((A, A, A, F32, A, F32, A, 4, 64, 63, 1e-5), SHAPE),          # ld < K
+    ((A, A, A, F32, A, F32, A, 4, (1 << 26) + 32, 1 << 27, 1e-5), SHAPE),
+    ((A, A, A, F32, A, F32, A, 4, 64, 1 << 31, 1e-5), SHAPE),
+    ((None, A, A, F32, A, F32, A, 4, 64, 64, 1e-5), NULL),
+    ((A, A, A, F32, None, F32, A, 4, 64, 64, 1e-5), NULL),
+    ((A, A, A, F32, A, F32, None, 4, 64, 64, 1e-5), NULL),
+    ((P(0x1002), A, A, F32, A, F32, A, 4, 64, 64, 1e-5), MISALIGNED),
+    ((A, P(0x1001), A, F16, A, F32, A, 4, 64, 64, 1e-5), MISALIGNED),
+    ((A, A, P(0x1001), BF16, A, F32, A, 4, 64, 64, 1e-5), MISALIGNED),
+    ((A, A, A, F32, P(0x1002), F32, A, 4, 64, 64, 1e-5), MISALIGNED),
+    ((A, A, A, F32, A, F32, P(0x1002), 4, 64, 64, 1e-5), MISALIGNED),
+    ((None, None, None, F32, None, F32, None, 0, 64, 64, 1e-5), OK),
+    ((None, None, None, F32, None, F32, None, 4, 0, 0, 1e-5), OK),
+])
+def test_rmsnorm_q8_1_rejects_before_launch(lib, args, expect):
+    assert lib.dg_rmsnorm_q8_1(*args, None) == expect
+
+
+@pytest.mark.parametrize("args,expect", [
+    ((A, A, A, F32, A, F32, A, 3, 4, 63, 63, 63, 1e-5), ARG),      # Q8_1 is not a float output
+    ((A, A, A, F32, A, F32, A, F32, 4, 63, 63, 62, 1e-5), SHAPE),  # ldy < K
+    ((A, A, A, F32, A, F32, A, F32, 4, 63, 62, 63, 1e-5), SHAPE),
+    ((A, A, A, F32, A, F32, P(0x1001), BF16, 4, 63, 63, 63, 1e-5), MISALIGNED),
+    ((A, A, A, F32, A, F32, P(0x1002), F32, 4, 63, 63, 63, 1e-5), MISALIGNED),
+    ((None, None, None, F32, None, F32, None, F32, 0, 63, 63, 63, 1e-5), OK),
+])
+def test_rmsnorm_rejects_before_launch(lib, args, expect):
+    assert lib.dg_rmsnorm(*args, None) == expect
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    import memory_bound_decode_gemv_amd as dg
+    t = torch.zeros(4, 64)
+    if torch.cuda.is_available():
+        with pytest.raises(ValueError, match="device tensor"):
+            dg._need_here(x=t)
+    with pytest.raises(TypeError):
+        dg._dtype_id(torch.zeros(4, dtype=torch.int32), "x")
+    assert [dg._dtype_id(torch.zeros(1, dtype=d), "x") for d in (torch.float32, torch.float16, torch.bfloat16)] == [0, 1, 2]
