@@ -533,6 +533,55 @@ dg_status dg_argcompare_rows(const void* x, int dtype, int op, int64_t* idx, int
                              int64_t ld, void* ws, size_t ws_bytes, dg_stream stream);
 
 /* ------------------------------------------------------------------------
+ * Sampling: one token per row from a given random number, with temperature,
+ * top-k, top-p and min-p
+ *
+ *   w[c]   = exp((x[r][c] - max_c' x[r][c']) / temperature[r])
+ *   rank   = value descending, then index ascending (-0 equals +0)
+ *   top-k  keeps the first top_k[r] tokens in rank order;
+ *   top-p  keeps the shortest prefix of those whose weight reaches top_p[r]
+ *          times their total, never less than one token;
+ *   min-p  keeps those of them with w >= min_p[r];
+ *   idx[r] = the first kept c, in index order, for which the kept weight up to
+ *          and with c exceeds u[r] times the kept total.
+ *
+ * The tail of a decode step that is not greedy, where dg_argmax_rows is the
+ * tail of one that is.  The random numbers are the caller's, so the same
+ * inputs give the same tokens.  Weights are binary64 and are summed as
+ * integers round(2^F w), F = min(51, 62 - ceil(log2 C)): sums are exact and
+ * the token does not depend on how rows are split or on the batch that a row
+ * is in.  A token with w below 2^-(F+1) is never kept.
+ *
+ *   x        device [R][ld] of `dtype`, aligned to the element.
+ *   u        device float32 [R] in [0, 1); below 0 or NaN counts as 0, 1 and
+ *            above selects the last kept token.
+ *   temperature  device float32 [R], or NULL for 1.  0, a negative number or
+ *            NaN: greedy, exactly dg_argmax_rows (nothing else applies).
+ *   top_k    device int32 [R], or NULL: off.  0, a negative number, or C and
+ *            more: off for the row.
+ *   top_p    device float32 [R], or NULL: off.  1 and above, or NaN: off for
+ *            the row; 0 and below keeps one token.
+ *   min_p    device float32 [R], or NULL: off.  0 and below, or NaN: off for
+ *            the row; above 1 counts as 1.
+ *   idx      device int64 [R], 8-byte aligned.  A row with a NaN gives the
+ *            index of its first NaN, as dg_argmax_rows does.  A row of
+ *            nothing but -infinity gives -1 (0 if greedy).  +infinity
+ *            shares all weight among the infinite ones.
+ *   R, C     0 <= R < 2^31 (0 launches nothing), 1 <= C < 2^31 - 1.
+ *   ld       >= C; elements C..ld-1 of a row are not read.
+ *   ws       device workspace of dg_sample_workspace_bytes(R, C) bytes,
+ *            8-byte aligned; contents on entry do not matter; the call owns
+ *            it until the stream passes the call.  NULL is allowed when the
+ *            required size is 0 (rows of up to 4096).
+ * Errors: DG_ERR_ARG (dtype), DG_ERR_SHAPE, DG_ERR_NULL, DG_ERR_MISALIGNED,
+ * DG_ERR_WORKSPACE, DG_ERR_HIP.
+ * ------------------------------------------------------------------------ */
+size_t dg_sample_workspace_bytes(int64_t R, int64_t C);
+dg_status dg_sample_rows(const void* x, int dtype, const float* u, const float* temperature, const int32_t* top_k,
+                         const float* top_p, const float* min_p, int64_t* idx, int64_t R, int64_t C, int64_t ld,
+                         void* ws, size_t ws_bytes, dg_stream stream);
+
+/* ------------------------------------------------------------------------
  * Launch overrides (measurement and A/B runs)
  *
  * The *_ex variants take a launch configuration instead of the library's

@@ -79,6 +79,7 @@ EXPORTED = (
     "dg_q8_0_tiles_bytes", "dg_repack_q8_0_tiles", "dg_gemv_q8_0_tiles_workspace_bytes",
     "dg_gemv_q8_0_tiles", "dg_gemv_q8_0_tiles_ex",
     "dg_rmsnorm_q8_1", "dg_rmsnorm",
+    "dg_sample_workspace_bytes", "dg_sample_rows",
 )
 
 # Size of the library's fixed per-device argmax key array (include/decodegemv.h).
@@ -193,6 +194,10 @@ def _lib():
     lib.dg_rmsnorm_q8_1.restype = st
     lib.dg_rmsnorm.argtypes = [P, P, P, I32, P, I32, P, I32, I64, I64, I64, I64, F32, P]
     lib.dg_rmsnorm.restype = st
+    lib.dg_sample_workspace_bytes.argtypes = [I64, I64]
+    lib.dg_sample_workspace_bytes.restype = ctypes.c_size_t
+    lib.dg_sample_rows.argtypes = [P, I32, P, P, P, P, P, P, I64, I64, I64, P, ctypes.c_size_t, P]
+    lib.dg_sample_rows.restype = st
     _handle = lib
     return lib
 
@@ -724,4 +729,41 @@ def dg_gemv_bf16_argmax(W, x, idx, y=None, N=None, K=None, ldw=None, ws=None, st
     _need(ws, (torch.uint8, torch.int64), "ws")
     _check(_lib().dg_gemv_bf16_argmax(_ptr(W), _ptr(x), _ptr(y), _ptr(idx), N, K, ldw, _ptr(ws),
                                       ws.numel() * ws.element_size(), _stream(stream)), "dg_gemv_bf16_argmax")
+    return idx
+
+
+def dg_sample_workspace_bytes(R, C):
+    return int(_lib().dg_sample_workspace_bytes(int(R), int(C)))
+
+
+def dg_sample_rows(x, u, idx, R=None, C=None, ld=None, temperature=None, top_k=None, top_p=None, min_p=None, ws=None,
+                   stream=None):
+    """idx[R] (int64) = one token per row of logits x (float32, float16 or bfloat16
+    [R][ld]) drawn with the random numbers u (float32 [R], in [0, 1)) after
+    temperature, top-k, top-p and min-p (float32, int32, float32, float32 [R]
+    each, or None).  ws: a device workspace of dg_sample_workspace_bytes(R, C)
+    bytes; None is allowed when that is 0."""
+    torch = _torch()
+    _need_here(x=x, u=u, idx=idx, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, ws=ws)
+    dtype = _dtype_id(x, "x")
+    if R is None:
+        R = x.shape[0] if x.dim() == 2 else 1
+    if C is None:
+        C = x.shape[-1]
+    if ld is None:
+        ld = x.shape[-1]
+    R, C, ld = int(R), int(C), int(ld)
+    if R > 0 and C > 0 and ld >= C:
+        _fits(x, ((R - 1) * ld + C) * x.element_size(), "x")
+    for name, t, want in (("u", u, torch.float32), ("idx", idx, torch.int64), ("temperature", temperature, torch.float32),
+                          ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
+                          ("min_p", min_p, torch.float32)):
+        if t is None:
+            continue
+        if t.dtype != want:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {want}")
+        _fits(t, max(R, 0) * t.element_size(), name)
+    ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    _check(_lib().dg_sample_rows(_ptr(x), dtype, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                                 _ptr(idx), R, C, ld, _ptr(ws), ws_bytes, _stream(stream)), "dg_sample_rows")
     return idx

@@ -447,4 +447,23 @@ dg_status dg_argmax_rows(const float* x, int64_t* idx, int64_t R, int64_t C, int
     return hip_status(launch_argmax_rows(x, idx, R, C, ld, ws, (hipStream_t)stream));
 }
 
+size_t dg_sample_workspace_bytes(int64_t R, int64_t C) { return sample_workspace_bytes(R, C); }
+
+dg_status dg_sample_rows(const void* x, int dtype, const float* u, const float* temperature, const int32_t* top_k,
+                         const float* top_p, const float* min_p, int64_t* idx, int64_t R, int64_t C, int64_t ld,
+                         void* ws, size_t ws_bytes, dg_stream stream) {
+    if (!dtype_ok(dtype)) return DG_ERR_ARG;
+    if (R < 0 || R > kI32Max || C < 1 || C >= kI32Max || ld < C) return DG_ERR_SHAPE;
+    if (R == 0) return DG_OK;
+    if (!x || !u || !idx) return DG_ERR_NULL;
+    if (!aligned(x, dtype_size(dtype)) || !aligned(idx, 8) || !aligned(u, 4) || !aligned(temperature, 4) ||
+        !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4))
+        return DG_ERR_MISALIGNED;
+    const size_t need = sample_workspace_bytes(R, C);
+    if (need > 0 && (!ws || ws_bytes < need)) return DG_ERR_WORKSPACE;
+    if (ws && !aligned(ws, 8)) return DG_ERR_MISALIGNED;
+    return hip_status(launch_sample_rows({x, dtype, u, temperature, top_k, top_p, min_p, idx, R, C, ld, ws},
+                                         (hipStream_t)stream));
+}
+
 }  // extern "C"

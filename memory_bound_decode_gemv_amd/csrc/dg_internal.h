@@ -148,4 +148,18 @@ hipError_t launch_argcompare_rows(const void* x, int dtype, int op, int64_t* idx
 hipError_t launch_argmax_rows_noalloc(const float* x, int64_t* idx, int64_t R, int64_t C, int64_t ld,
                                       hipStream_t s);
 
+// One token per row from random numbers (the contract of dg_sample_rows).
+struct SampleRows {
+    const void* x;
+    int dtype;
+    const float *u, *temperature;
+    const int32_t* top_k;
+    const float *top_p, *min_p;
+    int64_t* idx;
+    int64_t R, C, ld;
+    void* ws;
+};
+size_t sample_workspace_bytes(int64_t R, int64_t C);
+hipError_t launch_sample_rows(const SampleRows& p, hipStream_t s);
+
 }  // namespace dg

@@ -1,0 +1,825 @@
+// sample.hip -- one token per row from given random numbers: temperature,
+// top-k, top-p and min-p over float32, binary16 or bfloat16 logits.
+//
+// Weights.  w_i = exp((x_i - m) / T) with m the row's maximum, in binary64,
+// held as the integer W_i = round(2^F w_i), F = min(51, 62 - ceil(log2 C)):
+// every sum of them fits 62 bits and is exact, so it does not depend on the
+// order of summation, on the split of a row over workgroups or on the order
+// in which atomics arrive, and the same call gives the same token on any
+// launch shape.  A token with W_i = 0 (below 2^-F of the likeliest) has no
+// part in anything.
+//
+// Rank order is value descending, index ascending, which is the descending
+// order of the 64-bit keys of the argmax (value image, then inverted index).
+// top-k and top-p each keep a prefix of that order, so what they keep together
+// is { key >= threshold } for one threshold key; min-p compares w_i itself.
+// The token is the first kept index whose running sum of W exceeds u times
+// the kept total.
+//
+// Rows of up to kCand elements: one workgroup and one launch, the row's keys
+// in LDS.  Longer rows, four launches:
+//   max     every chunk's largest key and smallest finite value;
+//   hist    (rows with top-k or top-p) counts and masses of kBins equal steps
+//           of m - x over the part of the row's range that has weight: steps
+//           of the value itself, not of its bits, so that a bell of logits
+//           spreads over the bins;
+//   gather  every workgroup reads the bins and finds the ones that the
+//           borders fall into; sums what lies above them for sure, per
+//           sub-chunk, and lists the keys of the border bins;
+//   pick    one workgroup per row resolves the borders within the listed keys
+//           (a radix descent over the key bits that differ), adds the kept
+//           ones to the sub-chunk sums, and finds the sub-chunk and in it the
+//           element that u falls into.
+// A row whose border bins hold more than kCand elements (many equal values)
+// is resolved by the same descent reading the row instead of the list.
+#include "argkey.h"
+#include "dg_device.h"
+#include "dg_internal.h"
+
+// Every kernel computes an element's weight and bin anew; they have to agree
+// to the bit, so no kernel may contract what another does not.
+#pragma clang fp contract(off)
+
+namespace dg {
+namespace {
+
+constexpr int kBins = 512;
+constexpr int kCand = 4096;          // keys that the pick kernel holds in LDS
+constexpr int kSubMin = 2048;        // elements of a sub-chunk, at least
+constexpr int kMaxSubs = 1024;       // sub-chunks of a row, at most
+constexpr int kChunkThreads = 256;
+constexpr int kPickThreads = 1024;
+constexpr int kTargetGroups = 1024;
+constexpr int kBatchRows = 512;      // rows whose workspace exists at once
+constexpr double kLog2e = 1.4426950408889634;
+
+typedef unsigned long long u64;
+
+template <class T>
+struct Logit {
+    __device__ __forceinline__ static float load(const T* p) { return (float)*p; }
+};
+
+struct SampleArgs {
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t* top_k;
+    int64_t* idx;
+    int C;
+    int64_t ld;
+    int F;          // fraction bits of the integer weights
+    int sub;        // elements per sub-chunk
+    int nsub;
+    int G;          // chunks per row
+    int subs_per_chunk;
+};
+
+// The workspace of one row.
+struct RowSpace {
+    u64 key[kMaxSubs];       // per chunk: largest key
+    float low[kMaxSubs];     // per chunk: smallest finite value (+inf if none)
+    u64 mass[kBins];
+    uint32_t count[kBins];
+    uint32_t ncand;
+    uint32_t pad;
+    u64 sum[kMaxSubs];       // per sub-chunk: kept for sure
+    u64 cand[kCand];
+};
+
+__device__ __forceinline__ float key_value(u64 key) {
+    const uint32_t img = (uint32_t)(key >> 32);
+    return __builtin_bit_cast(float, (img & 0x80000000u) ? img ^ 0x80000000u : ~img);
+}
+
+// One row's parameters and what follows from its extremes.
+struct Row {
+    float m;          // maximum
+    float scale;      // bins per unit of m - x
+    double c;         // log2(e) / T
+    double min_p;     // 0: off
+    double p;         // >= 1: off
+    double u;
+    int64_t known;    // the token, when no draw is needed; else -2
+    int k;            // 0: off
+    int F;
+
+    // w as a binary64 number in [0, 1] (0 where the quotient is not a number)
+    __device__ __forceinline__ double weight(float x) const {
+        if (x == m) return 1.0;
+        const double e = exp2(((double)x - (double)m) * c);
+        return e >= 0.0 ? e : 0.0;
+    }
+    // round(2^F w) by the binary64 addition 2^52 + 2^F w (F <= 51)
+    __device__ __forceinline__ u64 fixed(double w) const {
+        const double v = fma(w, (double)(1ull << F), 4503599627370496.0);
+        return __builtin_bit_cast(u64, v) & 0x000FFFFFFFFFFFFFull;
+    }
+    // the step of m - x, larger for smaller x; equal values share a bin
+    __device__ __forceinline__ int bin(float x) const {
+        const float d = x == m ? 0.0f : fminf(m - x, 3.4028234e38f);
+        return (int)fminf(d * scale, (float)(kBins - 1));
+    }
+};
+
+__device__ __forceinline__ Row make_row(const SampleArgs& a, int64_t r, u64 top, float low) {
+    Row q;
+    const uint32_t img = (uint32_t)(top >> 32);
+    const double T = a.temperature ? (double)a.temperature[r] : 1.0;
+    const int k = a.top_k ? a.top_k[r] : 0;
+    const double p = a.top_p ? (double)a.top_p[r] : 1.0;
+    const double mp = a.min_p ? (double)a.min_p[r] : 0.0;
+    const double u = (double)a.u[r];
+    q.m = key_value(top);
+    q.known = -2;
+    if (img == 0xFFFFFFFFu || !(T > 0.0)) q.known = (int64_t)key_index(top);   // a NaN, or greedy
+    else if (q.m == -INFINITY) q.known = -1;                                   // nothing to draw from
+    q.k = k > 0 && k < a.C ? k : 0;
+    q.p = p < 1.0 ? (p > 0.0 ? p : 0.0) : 1.0;
+    q.min_p = mp > 0.0 ? (mp < 1.0 ? mp : 1.0) : 0.0;
+    q.u = u > 0.0 ? (u < 1.0 ? u : 1.0) : 0.0;
+    q.F = a.F;
+    q.c = kLog2e / T;
+    // the range that has weight: down to the smallest value, and no further than W = 0
+    double range = (double)q.m - (double)low;
+    const double reach = (double)(a.F + 1) / q.c;
+    if (reach < range) range = reach;
+    q.scale = range > 0.0 ? fminf((float)((double)kBins / range), 1e30f) : 0.0f;
+    if (q.m == INFINITY) q.scale = 1.0f;   // m - x is 0 or infinite
+    return q;
+}
+
+__device__ __forceinline__ float wave_min_f32(float v) {
+#pragma unroll
+    for (int o = kWave / 2; o >= 1; o >>= 1) v = fminf(v, __shfl_xor(v, o));
+    return v;
+}
+
+__device__ __forceinline__ u64 wave_sum_u64(u64 v) {
+#pragma unroll
+    for (int o = kWave / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+__device__ __forceinline__ u64 wave_scan_u64(u64 v) {   // inclusive
+    const int lane = lane_id();
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const u64 t = __shfl_up(v, o);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+
+// Inclusive sums over the workgroup in thread order; *total = the whole sum.
+template <int THREADS>
+__device__ __forceinline__ u64 block_scan_u64(u64 v, u64* total) {
+    constexpr int kWaves = THREADS / kWave;
+    __shared__ u64 part[kWaves];
+    const int wave = threadIdx.x / kWave;
+    v = wave_scan_u64(v);
+    __syncthreads();   // the array's last use is over
+    if (lane_id() == kWave - 1) part[wave] = v;
+    __syncthreads();
+    u64 before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) before += part[w];
+        all += part[w];
+    }
+    *total = all;
+    return before + v;
+}
+
+// A row's extremes from its chunks (every wave by itself).
+__device__ __forceinline__ void row_extremes(const RowSpace* ws, int G, u64* top, float* low) {
+    u64 t = 0;
+    float l = INFINITY;
+    for (int g = lane_id(); g < G; g += kWave) {
+        t = umax64(t, ws->key[g]);
+        l = fminf(l, ws->low[g]);
+    }
+    *top = wave_max_u64(t);
+    *low = wave_min_f32(l);
+}
+
+// ---- max ----------------------------------------------------------------------
+template <class T>
+__global__ void __launch_bounds__(kChunkThreads)
+k_sample_max(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs a) {
+    const int g = blockIdx.x;
+    const int64_t r = blockIdx.y;
+    RowSpace* ws = spaces + r;
+    const T* row = x + r * a.ld;
+    const int64_t c0 = (int64_t)g * a.subs_per_chunk * a.sub;
+    const int64_t c1 = c0 + (int64_t)a.subs_per_chunk * a.sub < a.C ? c0 + (int64_t)a.subs_per_chunk * a.sub : a.C;
+    uint32_t best = 0u, bidx = 0xFFFFFFFFu;
+    float low = INFINITY;
+    for (int64_t c = c0 + threadIdx.x; c < c1; c += kChunkThreads) {
+        const float v = Logit<T>::load(row + c);
+        const uint32_t img = order_image(v);
+        if (img > best) { best = img; bidx = (uint32_t)c; }
+        if (v > -INFINITY) low = fminf(low, v);
+    }
+    u64 key = wave_max_u64(bidx == 0xFFFFFFFFu ? 0ull : pack_key(best, bidx));
+    low = wave_min_f32(low);
+    __shared__ u64 keys[kChunkThreads / kWave];
+    __shared__ float lows[kChunkThreads / kWave];
+    if (lane_id() == 0) {
+        keys[threadIdx.x / kWave] = key;
+        lows[threadIdx.x / kWave] = low;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < kChunkThreads / kWave; ++w) {
+            key = umax64(key, keys[w]);
+            low = fminf(low, lows[w]);
+        }
+        ws->key[g] = key;
+        ws->low[g] = low;
+    }
+    // the row's bins and list, cleared for the next launches
+    for (int i = g * kChunkThreads + threadIdx.x; i < kBins; i += a.G * kChunkThreads) {
+        ws->mass[i] = 0;
+        ws->count[i] = 0;
+    }
+    if (g == 0 && threadIdx.x == 0) ws->ncand = 0;
+}
+
+// ---- hist ---------------------------------------------------------------------
+template <class T>
+__global__ void __launch_bounds__(kChunkThreads)
+k_sample_hist(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs a) {
+    __shared__ u64 mass[kBins];
+    __shared__ uint32_t count[kBins];
+    const int g = blockIdx.x;
+    const int64_t r = blockIdx.y;
+    RowSpace* ws = spaces + r;
+    u64 top;
+    float low;
+    row_extremes(ws, a.G, &top, &low);
+    const Row q = make_row(a, r, top, low);
+    if (q.known != -2 || (q.k == 0 && q.p >= 1.0)) return;   // workgroup-uniform: nothing to select
+    for (int i = threadIdx.x; i < kBins; i += kChunkThreads) {
+        mass[i] = 0;
+        count[i] = 0;
+    }
+    __syncthreads();
+    const T* row = x + r * a.ld;
+    const int64_t c0 = (int64_t)g * a.subs_per_chunk * a.sub;
+    const int64_t c1 = c0 + (int64_t)a.subs_per_chunk * a.sub < a.C ? c0 + (int64_t)a.subs_per_chunk * a.sub : a.C;
+    for (int64_t c = c0 + threadIdx.x; c < c1; c += kChunkThreads) {
+        const float v = Logit<T>::load(row + c);
+        const u64 W = q.fixed(q.weight(v));
+        if (W) {
+            const int b = q.bin(v);
+            atomicAdd(&mass[b], W);
+            atomicAdd(&count[b], 1u);
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kChunkThreads) {
+        if (count[i]) {
+            atomicAdd(&ws->mass[i], mass[i]);
+            atomicAdd(&ws->count[i], count[i]);
+        }
+    }
+}
+
+// ---- borders ------------------------------------------------------------------
+// What the bins say about the borders of top-k and top-p.
+struct Borders {
+    int sure;              // bins below this are kept whole
+    int kbin;              // the bin of the k-th token, or kBins when top-k is off
+    int p0, p1;            // bins p0..p1 may hold top-p's border (p0 > p1: top-p is off)
+    uint32_t krank;        // its rank within kbin, from 1
+    u64 kmass;             // mass above kbin
+    u64 pmass;             // mass above p0
+    u64 total;             // mass of all bins
+    uint32_t listed;       // elements in the border bins
+};
+
+__device__ __forceinline__ bool border_bin(const Borders& b, int i) { return i == b.kbin || (i >= b.p0 && i <= b.p1); }
+
+// The shortest prefix has mass >= this: ceil(p * total), at least 1.
+__device__ __forceinline__ u64 p_target(double p, u64 total) {
+    const u64 t = (u64)ceil(p * (double)total);
+    return t < 1 ? 1 : (t > total ? total : t);
+}
+
+// Every thread of the workgroup calls this; the first wave scans the bins,
+// eight per lane.
+__device__ __forceinline__ Borders find_borders(const RowSpace* ws, const Row& q) {
+    __shared__ Borders out;
+    constexpr int kPer = kBins / kWave;
+    if (threadIdx.x < kWave) {
+        const int lane = threadIdx.x;
+        u64 mass[kPer], m_in = 0;
+        uint32_t count[kPer], c_in = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            mass[i] = ws->mass[lane * kPer + i];
+            count[i] = ws->count[lane * kPer + i];
+            m_in += mass[i];
+            c_in += count[i];
+        }
+        const u64 m_to = wave_scan_u64(m_in), c_to = wave_scan_u64((u64)c_in);
+        const u64 m_all = __shfl(m_to, kWave - 1), c_all = __shfl(c_to, kWave - 1);
+        Borders b;
+        b.total = m_all;
+        b.kbin = kBins;
+        b.krank = 0;
+        b.kmass = 0;
+        u64 m_low = m_all, m_high = m_all;   // the mass that top-p is a share of, at least and at most
+        if (q.k && (u64)q.k < c_all) {
+            // the lane and the bin in which the count reaches k
+            u64 c = c_to - c_in, m = m_to - m_in;
+            int bin = kBins;
+            u64 rank = 0, above = 0, upto = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if (bin == kBins && c < (u64)q.k && c + count[i] >= (u64)q.k) {
+                    bin = lane * kPer + i;
+                    rank = (u64)q.k - c;
+                    above = m;
+                    upto = m + mass[i];
+                }
+                c += count[i];
+                m += mass[i];
+            }
+            const int src = __ffsll((unsigned long long)__ballot(bin != kBins)) - 1;   // exactly one lane
+            b.kbin = __shfl(bin, src);
+            b.krank = (uint32_t)__shfl(rank, src);
+            b.kmass = __shfl(above, src);
+            m_low = b.kmass;
+            m_high = __shfl(upto, src);
+        }
+        b.p0 = 1;
+        b.p1 = 0;
+        b.pmass = 0;
+        if (q.p < 1.0) {
+            const u64 t[2] = {m_low ? p_target(q.p, m_low) : 1ull, p_target(q.p, m_high)};
+            int bins[2];
+            u64 aboves[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                u64 m = m_to - m_in;
+                int bin = kBins;
+                u64 above = 0;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    if (bin == kBins && m < t[j] && m + mass[i] >= t[j]) {
+                        bin = lane * kPer + i;
+                        above = m;
+                    }
+                    m += mass[i];
+                }
+                const int src = __ffsll((unsigned long long)__ballot(bin != kBins)) - 1;
+                bins[j] = __shfl(bin, src);
+                aboves[j] = __shfl(above, src);
+            }
+            b.p0 = bins[0];
+            b.p1 = bins[1];
+            b.pmass = aboves[0];
+        }
+        b.sure = q.p < 1.0 ? b.p0 : b.kbin;
+        u64 n = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (border_bin(b, lane * kPer + i)) n += count[i];
+        n = wave_sum_u64(n);
+        b.listed = (uint32_t)n;
+        if (lane == 0) out = b;
+    }
+    __syncthreads();
+    return out;
+}
+
+__device__ __forceinline__ Borders no_borders() {
+    Borders b;
+    b.sure = kBins;
+    b.kbin = kBins;
+    b.p0 = 1;
+    b.p1 = 0;
+    b.krank = 0;
+    b.kmass = b.pmass = b.total = 0;
+    b.listed = 0;
+    return b;
+}
+
+// ---- gather -------------------------------------------------------------------
+template <class T>
+__global__ void __launch_bounds__(kChunkThreads)
+k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs a) {
+    __shared__ u64 list[kCand];
+    __shared__ uint32_t n_list, base;
+    const int g = blockIdx.x;
+    const int64_t r = blockIdx.y;
+    RowSpace* ws = spaces + r;
+    u64 top;
+    float low;
+    row_extremes(ws, a.G, &top, &low);
+    const Row q = make_row(a, r, top, low);
+    if (q.known != -2) return;   // workgroup-uniform
+    const Borders b = q.k || q.p < 1.0 ? find_borders(ws, q) : no_borders();
+    const bool listing = b.listed > 0 && b.listed <= (uint32_t)kCand;
+    if (threadIdx.x == 0) n_list = 0;
+    __syncthreads();
+    const T* row = x + r * a.ld;
+    const int s0 = g * a.subs_per_chunk;
+    const int s1 = s0 + a.subs_per_chunk < a.nsub ? s0 + a.subs_per_chunk : a.nsub;
+    for (int s = s0; s < s1; ++s) {
+        const int64_t c0 = (int64_t)s * a.sub;
+        const int64_t c1 = c0 + a.sub < a.C ? c0 + a.sub : a.C;
+        u64 sum = 0;
+        for (int64_t c = c0 + threadIdx.x; c < c1; c += kChunkThreads) {
+            const float v = Logit<T>::load(row + c);
+            const double w = q.weight(v);
+            const u64 W = q.fixed(w);
+            if (W == 0) continue;
+            const int i = q.bin(v);
+            if (i < b.sure) {
+                if (w >= q.min_p) sum += W;
+            } else if (listing && border_bin(b, i)) {
+                const uint32_t at = atomicAdd(&n_list, 1u);
+                if (at < (uint32_t)kCand) list[at] = pack_key(order_image(v), (uint32_t)c);   // at < b.listed
+            }
+        }
+        u64 total;
+        block_scan_u64<kChunkThreads>(sum, &total);
+        if (threadIdx.x == 0) ws->sum[s] = total;
+    }
+    if (!listing) return;   // workgroup-uniform
+    __syncthreads();
+    if (threadIdx.x == 0) base = n_list ? atomicAdd(&ws->ncand, n_list) : 0u;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < n_list && base + i < (uint32_t)kCand; i += kChunkThreads)
+        ws->cand[base + i] = list[i];
+}
+
+// ---- pick ---------------------------------------------------------------------
+struct PickShared {
+    u64 key[kCand];
+    u64 mass[256];
+    uint32_t count[256];
+    u64 sum[kMaxSubs];
+    u64 prefix, left, all_or, all_and;
+    uint32_t hits;
+    int64_t found;
+};
+
+// Calls f(key, w, W) for this thread's share of the border elements: those of
+// the list in LDS, or (row != nullptr) those of the row that lie in a border
+// bin.
+template <class T, class Fn>
+__device__ __forceinline__ void each_listed(const PickShared& s, int n, const T* row, const Row& q, const Borders& b,
+                                            int C, Fn f) {
+    if (row) {
+        for (int64_t c = threadIdx.x; c < C; c += kPickThreads) {
+            const float v = Logit<T>::load(row + c);
+            const double w = q.weight(v);
+            const u64 W = q.fixed(w);
+            if (W && border_bin(b, q.bin(v))) f(pack_key(order_image(v), (uint32_t)c), w, W);
+        }
+    } else {
+        for (int i = threadIdx.x; i < n; i += kPickThreads) {
+            const u64 key = s.key[i];
+            const double w = q.weight(key_value(key));
+            f(key, w, q.fixed(w));
+        }
+    }
+}
+
+// The largest key t such that the border elements with keys in [t, hi] that
+// `take` accepts number (BY_MASS: weigh) at least `want`; 0 when all of them
+// together do not.  `want` >= 1.  A descent over the key digits below the
+// bits that all accepted keys share; every thread returns the same key.
+template <bool BY_MASS, class T, class Take>
+__device__ __forceinline__ u64 select_key(PickShared& s, int n, const T* row, const Row& q, const Borders& b, int C,
+                                          u64 want, Take take) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s.all_or = 0;
+        s.all_and = ~0ull;
+    }
+    __syncthreads();
+    u64 o = 0, n_and = ~0ull;
+    each_listed(s, n, row, q, b, C, [&](u64 key, double, u64) {
+        if (take(key)) {
+            o |= key;
+            n_and &= key;
+        }
+    });
+#pragma unroll
+    for (int d = kWave / 2; d >= 1; d >>= 1) {
+        o |= __shfl_xor(o, d);
+        n_and &= __shfl_xor(n_and, d);
+    }
+    if (lane_id() == 0 && o) {
+        atomicOr(&s.all_or, o);
+        atomicAnd(&s.all_and, n_and);
+    }
+    __syncthreads();
+    if (s.all_or == 0) return 0;   // none accepted
+    const u64 diff = s.all_or ^ s.all_and;
+    int shift = diff ? 64 - __clzll((long long)diff) : 0;   // bits shift.. are shared
+    u64 prefix = shift < 64 ? s.all_and >> shift << shift : 0;
+    while (shift > 0) {
+        const int bits = shift < 8 ? shift : 8;
+        const int next = shift - bits;
+        const u64 mask = shift < 64 ? ~0ull << shift : 0ull;
+        __syncthreads();
+        if (threadIdx.x < 256) {
+            if (BY_MASS) s.mass[threadIdx.x] = 0;
+            else s.count[threadIdx.x] = 0;
+        }
+        __syncthreads();
+        each_listed(s, n, row, q, b, C, [&](u64 key, double, u64 W) {
+            if (take(key) && (key & mask) == prefix) {
+                const int d = (int)((key >> next) & 255u) & ((1 << bits) - 1);
+                if (BY_MASS) atomicAdd(&s.mass[d], W);
+                else atomicAdd(&s.count[d], 1u);
+            }
+        });
+        __syncthreads();
+        if (threadIdx.x < kWave) {   // digits from the top, four per lane
+            const int lane = threadIdx.x;
+            u64 v[4], in = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = 255 - (lane * 4 + i);
+                v[i] = BY_MASS ? s.mass[d] : (u64)s.count[d];
+                in += v[i];
+            }
+            u64 at = wave_scan_u64(in) - in;
+            int digit = -1;
+            u64 above = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (digit < 0 && at < want && at + v[i] >= want) {
+                    digit = 255 - (lane * 4 + i);
+                    above = at;
+                }
+                at += v[i];
+            }
+            const u64 hit = __ballot(digit >= 0);
+            if (hit == 0) {
+                if (lane == 0) s.hits = 0;
+            } else {
+                const int src = __ffsll((unsigned long long)hit) - 1;
+                const int dg = __shfl(digit, src);
+                const u64 ab = __shfl(above, src);
+                if (lane == 0) {
+                    s.hits = 1;
+                    s.prefix = prefix | ((u64)dg << next);
+                    s.left = want - ab;
+                }
+            }
+        }
+        __syncthreads();
+        if (!s.hits) return 0;   // fewer than wanted (only at the first digit)
+        prefix = s.prefix;
+        want = s.left;
+        shift = next;
+    }
+    return prefix;
+}
+
+// Resolves a row whose border elements are in s.key[0..n) or in `row`, and
+// writes its token.  whole: the list is the whole row (nothing was summed).
+template <class T>
+__device__ __forceinline__ void pick_token(PickShared& s, int n, bool from_row, const T* row, const Row& q,
+                                           const Borders& b, const SampleArgs& a, bool whole, int64_t r) {
+    const T* scan = from_row ? row : nullptr;
+    const int C = a.C;
+    u64 threshold = 0;
+    u64 kkey = 0;
+    u64 total = b.total;
+    if (b.kbin < kBins) {
+        const int kbin = b.kbin;
+        auto in_kbin = [&](u64 key) { return q.bin(key_value(key)) == kbin; };
+        kkey = select_key<false>(s, n, scan, q, b, C, (u64)b.krank, in_kbin);
+        threshold = kkey;
+        if (q.p < 1.0) {   // the mass that top-k keeps
+            u64 part = 0;
+            each_listed(s, n, scan, q, b, C, [&](u64 key, double, u64 W) {
+                if (in_kbin(key) && key >= kkey) part += W;
+            });
+            u64 all;
+            block_scan_u64<kPickThreads>(part, &all);
+            total = b.kmass + all;
+        }
+    }
+    if (q.p < 1.0) {
+        const int p0 = b.p0, p1 = b.p1;
+        const u64 target = p_target(q.p, total);
+        auto in_reach = [&](u64 key) {
+            const int i = q.bin(key_value(key));
+            return i >= p0 && i <= p1 && key >= kkey;
+        };
+        const u64 pkey = select_key<true>(s, n, scan, q, b, C, target > b.pmass ? target - b.pmass : 1ull, in_reach);
+        if (pkey > threshold) threshold = pkey;
+    }
+
+    // the part of the row that u falls into
+    u64 before = 0, kept = 0;   // kept mass before it; of the whole row
+    int64_t c0 = 0, c1 = C;
+    if (!whole) {
+        __syncthreads();
+        if (from_row) {
+            // a wave's 64 consecutive elements lie in one sub-chunk
+            for (int64_t base = (int64_t)(threadIdx.x / kWave) * kWave; base < C; base += kPickThreads) {
+                const int64_t c = base + lane_id();
+                u64 add = 0;
+                if (c < C) {
+                    const float v = Logit<T>::load(row + c);
+                    const double w = q.weight(v);
+                    const u64 W = q.fixed(w);
+                    if (W && w >= q.min_p && border_bin(b, q.bin(v)) && q.bin(v) >= b.sure &&
+                        pack_key(order_image(v), (uint32_t)c) >= threshold)
+                        add = W;
+                }
+                add = wave_sum_u64(add);
+                if (add && lane_id() == 0) atomicAdd(&s.sum[base / a.sub], add);
+            }
+        } else {
+            for (int i = threadIdx.x; i < n; i += kPickThreads) {
+                const u64 key = s.key[i];
+                const double w = q.weight(key_value(key));
+                if (key >= threshold && w >= q.min_p) atomicAdd(&s.sum[min(key_index(key) / (uint32_t)a.sub, (uint32_t)kMaxSubs - 1)], q.fixed(w));
+            }
+        }
+        __syncthreads();
+        const u64 mine = (int)threadIdx.x < a.nsub ? s.sum[threadIdx.x] : 0ull;
+        const u64 upto = block_scan_u64<kPickThreads>(mine, &kept);
+        u64 t = (u64)(q.u * (double)kept);
+        if (t >= kept) t = kept - 1;
+        if (upto > t && upto - mine <= t) {   // exactly one thread
+            s.found = threadIdx.x;
+            s.left = upto - mine;
+        }
+        __syncthreads();
+        before = s.left;
+        c0 = s.found * a.sub;
+        c1 = c0 + a.sub < C ? c0 + a.sub : C;
+    }
+    const int64_t per = (c1 - c0 + kPickThreads - 1) / kPickThreads;   // consecutive elements per thread
+    auto kept_weight = [&](int64_t c) -> u64 {
+        const float v = Logit<T>::load(row + c);
+        const double w = q.weight(v);
+        return w >= q.min_p && pack_key(order_image(v), (uint32_t)c) >= threshold ? q.fixed(w) : 0ull;
+    };
+    const int64_t a0 = c0 + per * threadIdx.x;
+    const int64_t a1 = a0 + per < c1 ? a0 + per : c1;
+    u64 mine = 0;
+    for (int64_t c = a0; c < a1; ++c) mine += kept_weight(c);
+    u64 all;
+    const u64 upto = block_scan_u64<kPickThreads>(mine, &all);
+    if (whole) kept = all;
+    u64 t = (u64)(q.u * (double)kept);
+    if (t >= kept) t = kept - 1;
+    if (before + upto > t && before + upto - mine <= t) {   // exactly one thread
+        u64 at = before + upto - mine;
+        for (int64_t c = a0; c < a1; ++c) {
+            at += kept_weight(c);
+            if (at > t) {
+                a.idx[r] = c;
+                break;
+            }
+        }
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kPickThreads)
+k_sample_pick(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs a) {
+    __shared__ PickShared s;
+    const int64_t r = blockIdx.x;
+    RowSpace* ws = spaces + r;
+    u64 top;
+    float low;
+    row_extremes(ws, a.G, &top, &low);
+    const Row q = make_row(a, r, top, low);
+    if (q.known != -2) {   // workgroup-uniform
+        if (threadIdx.x == 0) a.idx[r] = q.known;
+        return;
+    }
+    const Borders b = q.k || q.p < 1.0 ? find_borders(ws, q) : no_borders();
+    const bool from_row = b.listed > (uint32_t)kCand;
+    const int n = from_row ? 0 : (int)min(ws->ncand, (uint32_t)kCand);   // b.listed of them
+    for (int i = threadIdx.x; i < n; i += kPickThreads) s.key[i] = ws->cand[i];
+    if ((int)threadIdx.x < a.nsub) s.sum[threadIdx.x] = ws->sum[threadIdx.x];
+    if (threadIdx.x == 0) s.found = 0;
+    __syncthreads();
+    pick_token<T>(s, n, from_row, x + r * a.ld, q, b, a, false, r);
+}
+
+// A row of at most kCand elements: every element is listed, in one bin.
+template <class T>
+__global__ void __launch_bounds__(kPickThreads)
+k_sample_row(const T* __restrict__ x, SampleArgs a) {
+    __shared__ PickShared s;
+    __shared__ u64 keys[kPickThreads / kWave];
+    const int64_t r = blockIdx.x;
+    const T* row = x + r * a.ld;
+    u64 top = 0;
+    for (int c = threadIdx.x; c < a.C; c += kPickThreads) {
+        const u64 key = pack_key(order_image(Logit<T>::load(row + c)), (uint32_t)c);
+        s.key[c] = key;
+        top = umax64(top, key);
+    }
+    top = wave_max_u64(top);
+    if (lane_id() == 0) keys[threadIdx.x / kWave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPickThreads / kWave; ++w) top = umax64(top, keys[w]);
+    Row q = make_row(a, r, top, 0.0f);
+    if (q.known != -2) {   // workgroup-uniform
+        if (threadIdx.x == 0) a.idx[r] = q.known;
+        return;
+    }
+    q.scale = 0.0f;
+    Borders b = no_borders();
+    if (q.k) {
+        b.kbin = 0;
+        b.krank = (uint32_t)q.k;
+    }
+    if (q.p < 1.0) {
+        b.p0 = 0;
+        b.p1 = 0;
+        u64 mass = 0;
+        for (int c = threadIdx.x; c < a.C; c += kPickThreads) mass += q.fixed(q.weight(key_value(s.key[c])));
+        block_scan_u64<kPickThreads>(mass, &b.total);
+    }
+    pick_token<T>(s, a.C, false, row, q, b, a, true, r);
+}
+
+// ---- host ---------------------------------------------------------------------
+SampleArgs plan_rows(int64_t R, int64_t C) {
+    SampleArgs a{};
+    a.C = (int)C;
+    int bits = 0;
+    while (((int64_t)1 << bits) < C) ++bits;
+    a.F = 62 - bits < 51 ? 62 - bits : 51;
+    int64_t sub = (C + kMaxSubs - 1) / kMaxSubs;
+    sub = (sub + kSubMin - 1) / kSubMin * kSubMin;
+    a.sub = (int)sub;
+    a.nsub = (int)((C + sub - 1) / sub);
+    int64_t G = (kTargetGroups + R - 1) / R;
+    if (G > a.nsub) G = a.nsub;
+    a.subs_per_chunk = (int)((a.nsub + G - 1) / G);
+    a.G = (a.nsub + a.subs_per_chunk - 1) / a.subs_per_chunk;
+    return a;
+}
+
+template <class T>
+hipError_t launch_sample(const SampleRows& p, hipStream_t s) {
+    const T* x = (const T*)p.x;
+    if (p.C <= kCand) {
+        SampleArgs a = plan_rows(p.R, p.C);
+        a.ld = p.ld;
+        a.u = p.u; a.temperature = p.temperature; a.top_k = p.top_k; a.top_p = p.top_p; a.min_p = p.min_p;
+        a.idx = p.idx;
+        hipLaunchKernelGGL((k_sample_row<T>), dim3((unsigned)p.R), dim3(kPickThreads), 0, s, x, a);
+        return hipGetLastError();
+    }
+    RowSpace* ws = (RowSpace*)p.ws;
+    for (int64_t r0 = 0; r0 < p.R; r0 += kBatchRows) {
+        const int64_t rn = p.R - r0 < kBatchRows ? p.R - r0 : kBatchRows;
+        SampleArgs a = plan_rows(rn, p.C);
+        a.ld = p.ld;
+        a.u = p.u + r0;
+        a.temperature = p.temperature ? p.temperature + r0 : nullptr;
+        a.top_k = p.top_k ? p.top_k + r0 : nullptr;
+        a.top_p = p.top_p ? p.top_p + r0 : nullptr;
+        a.min_p = p.min_p ? p.min_p + r0 : nullptr;
+        a.idx = p.idx + r0;
+        const T* xr = x + r0 * p.ld;
+        const dim3 chunks((unsigned)a.G, (unsigned)rn);
+        hipLaunchKernelGGL((k_sample_max<T>), chunks, dim3(kChunkThreads), 0, s, xr, ws, a);
+        if (p.top_k || p.top_p)
+            hipLaunchKernelGGL((k_sample_hist<T>), chunks, dim3(kChunkThreads), 0, s, xr, ws, a);
+        hipLaunchKernelGGL((k_sample_gather<T>), chunks, dim3(kChunkThreads), 0, s, xr, ws, a);
+        hipLaunchKernelGGL((k_sample_pick<T>), dim3((unsigned)rn), dim3(kPickThreads), 0, s, xr, ws, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+size_t sample_workspace_bytes(int64_t R, int64_t C) {
+    if (R <= 0 || C <= kCand) return 0;
+    return (size_t)(R < kBatchRows ? R : kBatchRows) * sizeof(RowSpace);
+}
+
+hipError_t launch_sample_rows(const SampleRows& p, hipStream_t s) {
+    switch (p.dtype) {
+        case DG_DTYPE_F32: return launch_sample<float>(p, s);
+        case DG_DTYPE_F16: return launch_sample<_Float16>(p, s);
+        case DG_DTYPE_BF16: return launch_sample<__bf16>(p, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace dg

@@ -72,3 +72,37 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(TypeError):
         dg._dtype_id(torch.zeros(4, dtype=torch.int32), "x")
     assert [dg._dtype_id(torch.zeros(1, dtype=d), "x") for d in (torch.float32, torch.float16, torch.bfloat16)] == [0, 1, 2]
+
+
+@pytest.mark.parametrize("args,expect", [
+    ((A, 3, A, A, A, A, A, A, 4, 100, 100, None, 0), ARG),
+    ((A, F32, A, A, A, A, A, A, -1, 100, 100, None, 0), SHAPE),
+    ((A, F32, A, A, A, A, A, A, 1 << 31, 100, 100, None, 0), SHAPE),
+    ((A, F32, A, A, A, A, A, A, 4, 0, 100, None, 0), SHAPE),
+    ((A, F32, A, A, A, A, A, A, 4, (1 << 31) - 1, 1 << 31, A, 1 << 40), SHAPE),
+    ((A, F32, A, A, A, A, A, A, 4, 100, 99, None, 0), SHAPE),
+    ((None, F32, A, A, A, A, A, A, 4, 100, 100, None, 0), NULL),
+    ((A, F32, None, A, A, A, A, A, 4, 100, 100, None, 0), NULL),
+    ((A, F32, A, A, A, A, A, None, 4, 100, 100, None, 0), NULL),
+    ((P(0x1002), F32, A, A, A, A, A, A, 4, 100, 100, None, 0), MISALIGNED),
+    ((P(0x1001), BF16, A, A, A, A, A, A, 4, 100, 100, None, 0), MISALIGNED),
+    ((A, F32, P(0x1002), A, A, A, A, A, 4, 100, 100, None, 0), MISALIGNED),
+    ((A, F32, A, P(0x1002), A, A, A, A, 4, 100, 100, None, 0), MISALIGNED),
+    ((A, F32, A, A, P(0x1002), A, A, A, 4, 100, 100, None, 0), MISALIGNED),
+    ((A, F32, A, A, A, P(0x1002), A, A, 4, 100, 100, None, 0), MISALIGNED),
+    ((A, F32, A, A, A, A, P(0x1002), A, 4, 100, 100, None, 0), MISALIGNED),
+    ((A, F32, A, A, A, A, A, P(0x1004), 4, 100, 100, None, 0), MISALIGNED),
+    ((A, F32, A, A, A, A, A, A, 4, 5000, 5000, None, 1 << 30), WORKSPACE),
+    ((A, F32, A, A, A, A, A, A, 4, 5000, 5000, A, 1000), WORKSPACE),
+    ((A, F32, A, A, A, A, A, A, 4, 5000, 5000, P(0x1004), 1 << 30), MISALIGNED),
+    ((None, F32, None, None, None, None, None, None, 0, 100, 100, None, 0), OK),
+])
+def test_sample_rows_rejects_before_launch(lib, args, expect):
+    assert lib.dg_sample_rows(*args, None) == expect
+
+
+def test_sample_workspace(lib):
+    f = lib.dg_sample_workspace_bytes
+    assert f(0, 128256) == 0 and f(-1, 128256) == 0 and f(7, 4096) == 0
+    one = f(1, 4097)
+    assert one > 0 and f(3, 128256) == 3 * one and f(512, 4097) == 512 * one == f(100000, 4097)
