@@ -307,6 +307,48 @@ dg_status dg_gemv_q8_0_tiles(const void* Wt, const void* Xq, float* Y, int64_t N
                              void* ws, size_t ws_bytes, dg_stream stream);
 
 /* ------------------------------------------------------------------------
+ * The gated feed-forward product: gate and up projections, the activation and
+ * their product in one launch, M = 1..24 activation columns
+ *
+ *   Y[m][n] = act(G[m][n]) * U[m][n],   G = Wg X, U = Wu X
+ *
+ * The first half of a decoder layer's gated feed-forward block, whose two
+ * matrices read the same columns.  G and U are the sums of the GEMV of the
+ * same format (exact int32 block sums, exact binary16 scale products, fp32
+ * sums over blocks in an order that the shape fixes); the activation and the
+ * product are fp32.  Results are bit-reproducible.
+ *
+ *   DG_ACT_SILU       act(g) = g / (1 + exp(-g))
+ *   DG_ACT_GELU       act(g) = g/2 (1 + erf(g / sqrt 2))
+ *   DG_ACT_GELU_TANH  act(g) = g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))
+ *   DG_ACT_RELU       act(g) = max(g, 0)
+ *
+ *   Wg, Wu  device, N rows each, as Wq of dg_gemv_q4_0 / dg_gemv_q8_0, or (the
+ *           tiled calls) as Wt of dg_gemv_q4_0_tiles / dg_gemv_q8_0_tiles;
+ *           16-byte aligned.  They may be the same matrix.
+ *   Xq, Y, N, K, M  as for dg_gemv_q4_0.  K = 0 gives Y = 0.
+ *   ws      (tiled calls) device workspace of at least
+ *           dg_gemv_*_tiles_glu_workspace_bytes(N, K, M) bytes (0: ws may be
+ *           NULL), with the rules of dg_gemv_q4_0_tiles: zero-filled once when
+ *           allocated, left zero where it matters by every call; the same
+ *           workspace serves both kinds of call in turn.
+ * Errors: DG_ERR_ARG (act), DG_ERR_SHAPE, DG_ERR_NULL, DG_ERR_MISALIGNED,
+ * DG_ERR_WORKSPACE, DG_ERR_HIP.
+ * ------------------------------------------------------------------------ */
+enum { DG_ACT_SILU = 0, DG_ACT_GELU = 1, DG_ACT_GELU_TANH = 2, DG_ACT_RELU = 3 };
+
+dg_status dg_gemv_q4_0_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
+                           int act, dg_stream stream);
+dg_status dg_gemv_q8_0_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
+                           int act, dg_stream stream);
+size_t dg_gemv_q4_0_tiles_glu_workspace_bytes(int64_t N, int64_t K, int M);
+size_t dg_gemv_q8_0_tiles_glu_workspace_bytes(int64_t N, int64_t K, int M);
+dg_status dg_gemv_q4_0_tiles_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
+                                 int act, void* ws, size_t ws_bytes, dg_stream stream);
+dg_status dg_gemv_q8_0_tiles_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
+                                 int act, void* ws, size_t ws_bytes, dg_stream stream);
+
+/* ------------------------------------------------------------------------
  * NF4 weights (4-bit codes into a 16-entry float table, per-block absmax)
  * x bfloat16 activations, one column
  *

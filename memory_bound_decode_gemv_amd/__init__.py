@@ -44,6 +44,10 @@ DG_DTYPE_F16 = 1
 DG_DTYPE_BF16 = 2
 DG_ARG_MAX = 0
 DG_ARG_MIN = 1
+DG_ACT_SILU = 0
+DG_ACT_GELU = 1
+DG_ACT_GELU_TANH = 2
+DG_ACT_RELU = 3
 
 DG_VARIANT_DENSE_WIDE = 1
 DG_VARIANT_DENSE_XREG = 2
@@ -80,6 +84,9 @@ EXPORTED = (
     "dg_gemv_q8_0_tiles", "dg_gemv_q8_0_tiles_ex",
     "dg_rmsnorm_q8_1", "dg_rmsnorm",
     "dg_sample_workspace_bytes", "dg_sample_rows",
+    "dg_gemv_q4_0_glu", "dg_gemv_q8_0_glu",
+    "dg_gemv_q4_0_tiles_glu_workspace_bytes", "dg_gemv_q8_0_tiles_glu_workspace_bytes",
+    "dg_gemv_q4_0_tiles_glu", "dg_gemv_q8_0_tiles_glu",
 )
 
 # Size of the library's fixed per-device argmax key array (include/decodegemv.h).
@@ -198,6 +205,13 @@ def _lib():
     lib.dg_sample_workspace_bytes.restype = ctypes.c_size_t
     lib.dg_sample_rows.argtypes = [P, I32, P, P, P, P, P, P, I64, I64, I64, P, ctypes.c_size_t, P]
     lib.dg_sample_rows.restype = st
+    for f in ("q4_0", "q8_0"):
+        getattr(lib, f"dg_gemv_{f}_glu").argtypes = [P, P, P, P, I64, I64, I32, I32, P]
+        getattr(lib, f"dg_gemv_{f}_glu").restype = st
+        getattr(lib, f"dg_gemv_{f}_tiles_glu_workspace_bytes").argtypes = [I64, I64, I32]
+        getattr(lib, f"dg_gemv_{f}_tiles_glu_workspace_bytes").restype = ctypes.c_size_t
+        getattr(lib, f"dg_gemv_{f}_tiles_glu").argtypes = [P, P, P, P, I64, I64, I32, I32, P, ctypes.c_size_t, P]
+        getattr(lib, f"dg_gemv_{f}_tiles_glu").restype = st
     _handle = lib
     return lib
 
@@ -486,6 +500,68 @@ def dg_gemv_q8_0_tiles(Wt, Xq, Y, N, K, M, ws=None, launch=None, stream=None):
 def dg_gemv_q8_0(Wq, Xq, Y, N, K, M, launch=None, stream=None):
     """Y[M][N] (float32) from Q8_0 weight bytes and Q8_1 activation bytes (uint8 tensors)."""
     return _gemv_quant("dg_gemv_q8_0", 34, Wq, Xq, Y, N, K, M, launch, stream)
+
+
+_ACTS = {"silu": DG_ACT_SILU, "gelu": DG_ACT_GELU, "gelu_tanh": DG_ACT_GELU_TANH, "relu": DG_ACT_RELU}
+
+
+def _gemv_glu(fmt, tiles, Wg, Wu, Xq, Y, N, K, M, act, ws, stream):
+    torch = _torch()
+    _need_here(Wg=Wg, Wu=Wu, Xq=Xq, Y=Y, ws=ws)
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {tuple(_ACTS)}, not {act!r}")
+    for name, t, want in (("Wg", Wg, torch.uint8), ("Wu", Wu, torch.uint8), ("Xq", Xq, torch.uint8),
+                          ("Y", Y, torch.float32), ("ws", ws, torch.uint8)):
+        if t is not None and t.dtype != want:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {want}")
+    N, K, M = int(N), int(K), int(M)
+    lib = _lib()
+    if N > 0 and K > 0 and M > 0:
+        rows = (N + 15) // 16 * 16 if tiles else N
+        need = rows * (K // 32) * (18 if fmt == "q4_0" else 34)
+        _fits(Wg, need, "Wg")
+        _fits(Wu, need, "Wu")
+        _fits(Xq, M * (K // 32) * 36, "Xq")
+    if N > 0 and M > 0:
+        _fits(Y, M * N * 4, "Y")
+    args = (_ptr(Wg), _ptr(Wu), _ptr(Xq), _ptr(Y), N, K, M, _ACTS[act])
+    if tiles:
+        name = f"dg_gemv_{fmt}_tiles_glu"
+        args += (_ptr(ws), ws.numel() if ws is not None else 0)
+    else:
+        name = f"dg_gemv_{fmt}_glu"
+    _check(getattr(lib, name)(*args, _stream(stream)), name)
+    return Y
+
+
+def dg_gemv_q4_0_glu(Wg, Wu, Xq, Y, N, K, M, act="silu", stream=None):
+    """Y[M][N] (float32) = act(Wg X) * (Wu X) from two matrices of Q4_0 bytes and
+    Q8_1 activation bytes (uint8 tensors); act: "silu", "gelu", "gelu_tanh" or "relu"."""
+    return _gemv_glu("q4_0", False, Wg, Wu, Xq, Y, N, K, M, act, None, stream)
+
+
+def dg_gemv_q8_0_glu(Wg, Wu, Xq, Y, N, K, M, act="silu", stream=None):
+    """As dg_gemv_q4_0_glu, from Q8_0 bytes."""
+    return _gemv_glu("q8_0", False, Wg, Wu, Xq, Y, N, K, M, act, None, stream)
+
+
+def dg_gemv_q4_0_tiles_glu_workspace_bytes(N, K, M):
+    return int(_lib().dg_gemv_q4_0_tiles_glu_workspace_bytes(int(N), int(K), int(M)))
+
+
+def dg_gemv_q8_0_tiles_glu_workspace_bytes(N, K, M):
+    return int(_lib().dg_gemv_q8_0_tiles_glu_workspace_bytes(int(N), int(K), int(M)))
+
+
+def dg_gemv_q4_0_tiles_glu(Wg, Wu, Xq, Y, N, K, M, act="silu", ws=None, stream=None):
+    """As dg_gemv_q4_0_glu, from the tiled copies (workspace as for dg_gemv_q4_0_tiles, of
+    dg_gemv_q4_0_tiles_glu_workspace_bytes(N, K, M) bytes)."""
+    return _gemv_glu("q4_0", True, Wg, Wu, Xq, Y, N, K, M, act, ws, stream)
+
+
+def dg_gemv_q8_0_tiles_glu(Wg, Wu, Xq, Y, N, K, M, act="silu", ws=None, stream=None):
+    """As dg_gemv_q4_0_tiles_glu, from the tiled Q8_0 copies."""
+    return _gemv_glu("q8_0", True, Wg, Wu, Xq, Y, N, K, M, act, ws, stream)
 
 
 def dg_gemv_nf4(codes, absmax, table, x, y, N=None, K=None, B=64, launch=None, stream=None):

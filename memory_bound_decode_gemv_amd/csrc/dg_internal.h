@@ -110,6 +110,24 @@ hipError_t launch_q4_res(int M, int unroll, const void* Wq, const void* Xq, floa
 hipError_t launch_q8_res(int M, int unroll, const void* Wq, const void* Xq, float* Y, int N, int K, int grid,
                          hipStream_t s);
 
+// The gated products Y = act(gate X) * (up X): the operands of dg_gemv_*_glu.
+struct GluMatrices {
+    const void *gate, *up;
+    int act;   // DG_ACT_*
+};
+// Row-major: rows in units (M * ceil(K / 4096) <= 8, K <= 16384), or pairs of
+// row tiles on the matrix cores (any shape of the contract).
+hipError_t launch_gemv_glu(bool q8, const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M,
+                           hipStream_t s);
+hipError_t launch_units_glu(bool q8, int K, int M, int depth, const GluMatrices& w, const void* Xq, float* Y, int N,
+                            int grid, int block, hipStream_t s);
+hipError_t launch_mfma_glu(bool q8, int M, const GluMatrices& w, const void* Xq, float* Y, int N, int K,
+                           hipStream_t s);
+// In 16-row tiles; tiles_glu_config gives the workspace bytes that a call needs.
+bool tiles_glu_config(bool q8, int N, int K, int M, size_t* ws_bytes);
+hipError_t launch_tiles_glu(bool q8, int M, const GluMatrices& w, const void* Xq, float* Y, void* ws, int N, int K,
+                            hipStream_t s);
+
 hipError_t launch_quantize_q8_0(const float* w, void* Wq, int64_t N, int64_t K, hipStream_t s);
 
 // NF4 x bfloat16, one column (K <= 32768; B in {32, 64, 128, 256}; K % (4B) == 0),

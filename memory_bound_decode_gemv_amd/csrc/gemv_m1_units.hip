@@ -18,7 +18,13 @@
 // back has landed (loads complete in issue order; the workgroup's copy of
 // the activation column is issued before the first unit and the outputs are
 // stored after the last wait).
+//
+// The gated product (GLU) is the same kernel with rows of 2 S units: a wave
+// streams the units of gate row n, then those of up row n, through the same
+// buffers, and stores act(gate) * up.  Both matrices meet the activation pairs
+// that already sit in registers.
 #include "dg_internal.h"
+#include "glu.h"
 #include "q4_common.h"
 
 namespace dg {
@@ -95,10 +101,13 @@ __device__ __forceinline__ void copy_unit(const uint8_t* __restrict__ row, int s
     }
 }
 
-template <class F, int S, int MC, int DEPTH>
+template <class F, int S, int MC, int DEPTH, bool GLU>
 __global__ void __launch_bounds__(256)
-k_units(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* __restrict__ Y, int N, int K) {
+k_units(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* __restrict__ Y, int N, int K,
+        GluArgs<GLU> glu_args) {
     using G = UnitGeom<F>;
+    constexpr int H = GLU ? 2 : 1;   // weight rows per output: (gate and) the row
+    constexpr int U = H * S;         // units per output
     static_assert(DEPTH >= 2 && DEPTH <= 4, "pipeline depth");
     static_assert(G::kC * (DEPTH - 1) <= 63, "wait count exceeds the vmcnt field");
     static_assert(MC >= 1 && (MC * S <= 8 || (S == 1 && MC <= 12)), "activation pairs held in registers");
@@ -123,16 +132,20 @@ k_units(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
     int irow = row0, is = 0, islot = 0;
     auto issue = [&]() {
         if (irow < N) {
-            copy_unit<F>(Wq + (size_t)irow * row_bytes, is, npairs, bufs + islot * G::kBufBytes, lane);
+            if constexpr (GLU)
+                copy_unit<F>((is < S ? Wq : glu_args.Wu) + (size_t)irow * row_bytes, is < S ? is : is - S, npairs,
+                             bufs + islot * G::kBufBytes, lane);
+            else
+                copy_unit<F>(Wq + (size_t)irow * row_bytes, is, npairs, bufs + islot * G::kBufBytes, lane);
             islot = islot + 1 == DEPTH ? 0 : islot + 1;
-            if (++is == S) { is = 0; irow += rstride; }
+            if (++is == U) { is = 0; irow += rstride; }
         }
     };
 #pragma unroll
     for (int d = 0; d < DEPTH - 1; ++d) issue();
 
     {   // this wave's column copies have landed once only its issued units can be outstanding
-        const int units = row0 < N ? ((N - 1 - row0) / rstride + 1) * S : 0;   // wave-uniform
+        const int units = row0 < N ? ((N - 1 - row0) / rstride + 1) * U : 0;   // wave-uniform
         wait_ahead<G::kC, DEPTH>(units < DEPTH - 1 ? units : DEPTH - 1);
         lds_barrier();
     }
@@ -150,50 +163,62 @@ k_units(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
         }
     }
 
-    float out[MC];
+    float out[H][MC];
 #pragma unroll
-    for (int m = 0; m < MC; ++m) out[m] = 0.0f;
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int m = 0; m < MC; ++m) out[h][m] = 0.0f;
+    // the outputs held by the lanes, `count` of them, from row out_row0 on
+    auto store = [&](int out_row, int count) {
+        if (lane < count) {
+#pragma unroll
+            for (int m = 0; m < MC; ++m) {
+                float v = out[0][m];
+                if constexpr (GLU) v = glu(glu_args.act, v, out[1][m]);
+                Y[(int64_t)m * N + out_row + (int64_t)lane * rstride] = v;
+            }
+        }
+    };
     int nout = 0;
     int out_row0 = row0;
     int slot = 0;
     for (int row = row0; row < N; row += rstride) {
         // units left after the last one of this row (wave-uniform)
         const int rows_after = __builtin_amdgcn_readfirstlane((N - 1 - row) / rstride);
-        float acc[MC];
 #pragma unroll
-        for (int m = 0; m < MC; ++m) acc[m] = 0.0f;
+        for (int h = 0; h < H; ++h) {
+            float acc[MC];
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            issue();
-            const int after = rows_after * S + (S - 1 - s);
-            wait_ahead<G::kC, DEPTH>(after < DEPTH - 1 ? after : DEPTH - 1);
-            const int p = s * kWave + lane;
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(bufs + slot * G::kBufBytes) +
-                                (p < npairs ? lane : 0) * F::kPairDwords;
-            F::template pairs<MC>(w, act[s], acc);
-            slot = slot + 1 == DEPTH ? 0 : slot + 1;
-        }
+            for (int m = 0; m < MC; ++m) acc[m] = 0.0f;
 #pragma unroll
-        for (int m = 0; m < MC; ++m) {
-            const float r = wave_sum_f32(acc[m]);   // wave-uniform
-            if (lane == nout) out[m] = r;
+            for (int s = 0; s < S; ++s) {
+                issue();
+                const int after = rows_after * U + (U - 1 - h * S - s);
+                wait_ahead<G::kC, DEPTH>(after < DEPTH - 1 ? after : DEPTH - 1);
+                const int p = s * kWave + lane;
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(bufs + slot * G::kBufBytes) +
+                                    (p < npairs ? lane : 0) * F::kPairDwords;
+                F::template pairs<MC>(w, act[s], acc);
+                slot = slot + 1 == DEPTH ? 0 : slot + 1;
+            }
+#pragma unroll
+            for (int m = 0; m < MC; ++m) {
+                const float r = wave_sum_f32(acc[m]);   // wave-uniform
+                if (lane == nout) out[h][m] = r;
+            }
         }
         if (++nout == kWave) {
-#pragma unroll
-            for (int m = 0; m < MC; ++m) Y[(int64_t)m * N + out_row0 + (int64_t)lane * rstride] = out[m];
+            store(out_row0, kWave);
             nout = 0;
             out_row0 = row + rstride;
         }
     }
-    if (lane < nout) {
-#pragma unroll
-        for (int m = 0; m < MC; ++m) Y[(int64_t)m * N + out_row0 + (int64_t)lane * rstride] = out[m];
-    }
+    store(out_row0, nout);
 }
 
-template <class F>
+template <class F, bool GLU>
 hipError_t launch_units(int K, int M, int depth, const void* Wq, const void* Xq, float* Y, int N, int grid, int block,
-                        hipStream_t s) {
+                        GluArgs<GLU> ga, hipStream_t s) {
     using G = UnitGeom<F>;
     if (!block) block = 256;
     if (block > 256) return hipErrorInvalidValue;   // compiled for <= 256 threads
@@ -216,7 +241,7 @@ hipError_t launch_units(int K, int M, int depth, const void* Wq, const void* Xq,
     const uint8_t* x = (const uint8_t*)Xq;
 #define DG_SMD(SS, MM, DD)                                                                                 \
     if (S == SS && M == MM && depth == DD) {                                                               \
-        hipLaunchKernelGGL((k_units<F, SS, MM, DD>), dim3(grid), dim3(block), lds, s, w, x, Y, N, K);  \
+        hipLaunchKernelGGL((k_units<F, SS, MM, DD, GLU>), dim3(grid), dim3(block), lds, s, w, x, Y, N, K, ga); \
         return hipGetLastError();                                                                          \
     }
 #define DG_SM(SS, MM) DG_SMD(SS, MM, 2) DG_SMD(SS, MM, 3) DG_SMD(SS, MM, 4)
@@ -236,12 +261,33 @@ hipError_t launch_units(int K, int M, int depth, const void* Wq, const void* Xq,
 
 hipError_t launch_q4_units(int K, int M, int depth, const void* Wq, const void* Xq, float* Y, int N, int grid,
                            int block, hipStream_t s) {
-    return launch_units<UnitsQ4_0>(K, M, depth, Wq, Xq, Y, N, grid, block, s);
+    return launch_units<UnitsQ4_0, false>(K, M, depth, Wq, Xq, Y, N, grid, block, {}, s);
 }
 
 hipError_t launch_q8_units(int K, int M, int depth, const void* Wq, const void* Xq, float* Y, int N, int grid,
                            int block, hipStream_t s) {
-    return launch_units<UnitsQ8_0>(K, M, depth, Wq, Xq, Y, N, grid, block, s);
+    return launch_units<UnitsQ8_0, false>(K, M, depth, Wq, Xq, Y, N, grid, block, {}, s);
+}
+
+hipError_t launch_units_glu(bool q8, int K, int M, int depth, const GluMatrices& w, const void* Xq, float* Y, int N,
+                            int grid, int block, hipStream_t s) {
+    const GluArgs<true> ga = {(const uint8_t*)w.up, w.act};
+    return q8 ? launch_units<UnitsQ8_0, true>(K, M, depth, w.gate, Xq, Y, N, grid, block, ga, s)
+              : launch_units<UnitsQ4_0, true>(K, M, depth, w.gate, Xq, Y, N, grid, block, ga, s);
+}
+
+// The gated products over row-major weights, both matrices in one launch: the
+// columns are staged once for both, no sum leaves the chip before the product,
+// and of two GEMVs and an elementwise kernel two launches are gone.
+hipError_t launch_gemv_glu(bool q8, const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M,
+                           hipStream_t s) {
+    const int S = (K / 64 + kWave - 1) / kWave;
+    if (S <= 4 && M <= 4 && M * S <= 8) {
+        int grid, block;
+        units_default_grid(N, M, grid, block);
+        return launch_units_glu(q8, K, M, 0, w, Xq, Y, N, grid, block, s);
+    }
+    return launch_mfma_glu(q8, M, w, Xq, Y, N, K, s);
 }
 
 }  // namespace dg

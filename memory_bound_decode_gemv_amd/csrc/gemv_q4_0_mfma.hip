@@ -1,6 +1,7 @@
 // gemv_q4_0_mfma.hip -- Q4_0 x Q8_1 for 2..24 activation columns on the int8
 // matrix cores (the small-batch kernel of "The kernel that waited for itself").
 #include "dg_internal.h"
+#include "glu.h"
 #include "mfma_formats.h"
 
 namespace dg {
@@ -61,6 +62,9 @@ using namespace mfma;
 // complete for all.
 // Outputs: the KS partial results of a row tile meet in LDS and are added in
 // the fixed order 0..KS-1 (deterministic).
+// The gated product (GLU) gives a workgroup RT/2 row tiles of two matrices:
+// even tiles are the gate's, odd ones the up matrix's same rows.  The up sums
+// then go through LDS to the gate's wave, which stores act(gate) * up.
 // ---------------------------------------------------------------------------
 template <class WF, int CB, int MP, int RT, int KS>
 struct MfmaGeom {
@@ -193,11 +197,13 @@ __device__ __forceinline__ void wait_iterations_ahead(int q) {
     else wait_vmcnt<(DEPTH > 1 ? (DEPTH - 1) * COPIES : 0)>();
 }
 
-template <class WF, int CB, int MP, int RT, int KS, int DEPTH>
+template <class WF, int CB, int MP, int RT, int KS, int DEPTH, bool GLU>
 __global__ void __launch_bounds__(64 * RT * KS)
 k_qmfma(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* __restrict__ Y,
-        int N, int K, int M) {
+        int N, int K, int M, GluArgs<GLU> glu_args) {
     using G = MfmaGeom<WF, CB, MP, RT, KS>;
+    static_assert(!GLU || RT % 2 == 0, "gate and up tiles in pairs");
+    constexpr int RN = GLU ? RT / 2 : RT;      // row tiles of the output per workgroup
     constexpr bool TAIL = MP == 17;                // column 16 on the vector unit (below)
     constexpr int NT = TAIL ? 1 : G::kNT;          // 16-column matrix-core tiles
     constexpr int GB = RT * KS >= 12 ? 4 : 8;   // blocks per operand group
@@ -214,7 +220,7 @@ k_qmfma(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
     const size_t row_bytes = (size_t)nblk * WF::kBlockBytes;
     const int nchunks = (nblk + CB - 1) / CB;
     const int iters = (nchunks + KS - 1) / KS;
-    const int ngroups = (N + 16 * RT - 1) / (16 * RT);
+    const int ngroups = (N + 16 * RN - 1) / (16 * RN);
     // A-operand column of this lane in column tile t: 16t + rn, or, for the
     // MFMA rows past MP (MP = 4, 8, 24), a column of the same tile re-read
     // (16t + rn % (MP - 16t)); those results are dropped
@@ -223,12 +229,16 @@ k_qmfma(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
     auto abuf = [&](int d) { return lds + d * G::kStageBytes + G::kW * G::kWBufBytes; };
     const uint32_t dwidth = g == 0 ? 16u : 0u;   // lane group 0 feeds d4 to k-slot 0 of the scale products
 
+    const bool up = GLU && (tile & 1);         // wave-uniform
+    const uint8_t* __restrict__ Wt = Wq;
+    if constexpr (GLU) Wt = up ? glu_args.Wu : Wq;
+
     const uint32_t xlast = (uint32_t)M * nblk * kQ81Bytes - 16;   // the columns' last 16 bytes
     uint32_t aoff[G::kCa];
     act_offsets<WF, CB, MP, RT, KS>(nblk, M, wave, lane, aoff);
 
     for (int grp = blockIdx.x; grp < ngroups; grp += gridDim.x) {   // workgroup-uniform
-        const int n0 = (grp * RT + tile) * 16;
+        const int n0 = (grp * RN + (GLU ? tile >> 1 : tile)) * 16;
         const int n0c = n0 < N ? n0 : N - 1;   // tiles past N re-read row N - 1
         uint32_t woff[G::kCw];
         weight_offsets<WF, CB, MP, RT, KS>((uint32_t)row_bytes, N - 1 - n0c, lane, woff);
@@ -236,7 +246,7 @@ k_qmfma(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
 #pragma unroll
         for (int d = 0; d < DEPTH - 1; ++d)
             if (d < iters) {
-                copy_weights<WF, CB, G::kCw>(Wq, row_bytes, n0c, nchunks, d * KS + part, woff, wbuf(d));
+                copy_weights<WF, CB, G::kCw>(Wt, row_bytes, n0c, nchunks, d * KS + part, woff, wbuf(d));
                 copy_acts<CB, KS, G::kCa>(Xq, xlast, nchunks, d, wave, aoff, abuf(d));
             }
 
@@ -255,7 +265,7 @@ k_qmfma(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
             if (ahead < iters) {
                 int aslot = slot + DEPTH - 1;
                 if (aslot >= DEPTH) aslot -= DEPTH;
-                copy_weights<WF, CB, G::kCw>(Wq, row_bytes, n0c, nchunks, ahead * KS + part, woff, wbuf(aslot));
+                copy_weights<WF, CB, G::kCw>(Wt, row_bytes, n0c, nchunks, ahead * KS + part, woff, wbuf(aslot));
                 copy_acts<CB, KS, G::kCa>(Xq, xlast, nchunks, ahead, wave, aoff, abuf(aslot));
             }
             const int left = iters - 1 - it;
@@ -368,7 +378,28 @@ k_qmfma(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
                 }
             }
         }
-        if (part == 0) {
+        if constexpr (GLU) {
+            float* const red = reinterpret_cast<float*>(lds);   // a slot per wave; no other wave reads an up wave's
+            float* const tred = red + G::kW * NT * 4 * 64;
+            if constexpr (KS == 1) lds_barrier();   // every wave is done reading the buffers
+            if (part == 0 && up) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) red[((wave * NT + t) * 4 + r) * 64 + lane] = acc[t][r];
+                if constexpr (TAIL) tred[wave * 64 + lane] = tacc;
+            }
+            lds_barrier();
+            if (part == 0 && !up) {   // the up tile's first wave is KS further on
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[t][r] = glu(glu_args.act, acc[t][r], red[(((wave + KS) * NT + t) * 4 + r) * 64 + lane]);
+                if constexpr (TAIL) tacc = glu(glu_args.act, tacc, tred[(wave + KS) * 64 + lane]);
+            }
+        }
+        if (part == 0 && !up) {
             const int n = n0 + rn;
             if (n < N) {
 #pragma unroll
@@ -386,15 +417,17 @@ k_qmfma(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
     }
 }
 
-template <class WF, int CB, int MP, int RT, int KS, int DEPTH>
-hipError_t launch_mfma_cfg(const void* Wq, const void* Xq, float* Y, int N, int K, int M, int grid, hipStream_t s) {
+template <class WF, int CB, int MP, int RT, int KS, int DEPTH, bool GLU = false>
+hipError_t launch_mfma_cfg(const void* Wq, const void* Xq, float* Y, int N, int K, int M, int grid, hipStream_t s,
+                           GluArgs<GLU> ga = {}) {
     const size_t lds = mfma_lds_bytes<WF, CB, MP, RT, KS, DEPTH>();
     if (lds > device_max_lds_per_block()) return hipErrorInvalidValue;
     if ((K >> 5) % CB != 0 || K > (1 << 26)) return hipErrorInvalidValue;   // whole chunks, 32-bit offsets
-    const int groups = (N + 16 * RT - 1) / (16 * RT);
+    constexpr int kRows = 16 * (GLU ? RT / 2 : RT);
+    const int groups = (N + kRows - 1) / kRows;
     const int g = grid ? grid : groups;
-    hipLaunchKernelGGL((k_qmfma<WF, CB, MP, RT, KS, DEPTH>), dim3(g), dim3(64 * RT * KS), lds, s,
-                       (const uint8_t*)Wq, (const uint8_t*)Xq, Y, N, K, M);
+    hipLaunchKernelGGL((k_qmfma<WF, CB, MP, RT, KS, DEPTH, GLU>), dim3(g), dim3(64 * RT * KS), lds, s,
+                       (const uint8_t*)Wq, (const uint8_t*)Xq, Y, N, K, M, ga);
     return hipGetLastError();
 }
 
@@ -481,6 +514,22 @@ hipError_t launch_qmfma(int M, int unroll, const void* Wq, const void* Xq, float
     return launch_mfma_mp<WF, 24>(RT, KS, DEPTH, CB, Wq, Xq, Y, N, K, M, grid, s);
 }
 
+// The gated product: one pair of row tiles per workgroup, K in four parts.
+template <class WF, int MP>
+hipError_t launch_glu_mp(const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M, hipStream_t s) {
+    const GluArgs<true> ga = {(const uint8_t*)w.up, w.act};
+    return launch_mfma_cfg<WF, 8, MP, 2, 4, 2, true>(w.gate, Xq, Y, N, K, M, 0, s, ga);
+}
+
+template <class WF>
+hipError_t launch_qmfma_glu(const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M, hipStream_t s) {
+    if (M <= 4) return launch_glu_mp<WF, 4>(w, Xq, Y, N, K, M, s);
+    if (M <= 8) return launch_glu_mp<WF, 8>(w, Xq, Y, N, K, M, s);
+    if (M <= 16) return launch_glu_mp<WF, 16>(w, Xq, Y, N, K, M, s);
+    if (M == 17) return launch_glu_mp<WF, 17>(w, Xq, Y, N, K, M, s);
+    return launch_glu_mp<WF, 24>(w, Xq, Y, N, K, M, s);
+}
+
 }  // namespace
 
 hipError_t launch_q4_mfma(int M, int unroll, const void* Wq, const void* Xq, float* Y, int N, int K, int grid,
@@ -491,6 +540,11 @@ hipError_t launch_q4_mfma(int M, int unroll, const void* Wq, const void* Xq, flo
 hipError_t launch_q8_mfma(int M, int unroll, const void* Wq, const void* Xq, float* Y, int N, int K, int grid,
                           hipStream_t s) {
     return launch_qmfma<FmtQ8_0>(M, unroll, Wq, Xq, Y, N, K, grid, s);
+}
+
+hipError_t launch_mfma_glu(bool q8, int M, const GluMatrices& w, const void* Xq, float* Y, int N, int K,
+                           hipStream_t s) {
+    return q8 ? launch_qmfma_glu<FmtQ8_0>(w, Xq, Y, N, K, M, s) : launch_qmfma_glu<FmtQ4_0>(w, Xq, Y, N, K, M, s);
 }
 
 }  // namespace dg

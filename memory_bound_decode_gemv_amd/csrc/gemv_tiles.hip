@@ -55,7 +55,14 @@
 // Workgroup i of a row group takes range i % KP: with the hardware's
 // round-robin placement, the workgroups on one XCD read the same activation
 // range, so each XCD's L2 holds only its part of the columns.
+//
+// The gated product (GLU) is the same kernel with the row tiles of a workgroup
+// in pairs, an even wave row on the gate matrix's tile and the odd one after
+// it on the up matrix's same tile: 2 T tiles in all.  Everything up to the
+// tile sums is unchanged (the activation columns in LDS serve both), then the
+// up sums go through LDS to the gate's wave, which stores act(gate) * up.
 #include "dg_internal.h"
+#include "glu.h"
 #include "mfma_formats.h"
 
 namespace dg {
@@ -291,49 +298,67 @@ __device__ __forceinline__ void bind_group(u32x4 (&w)[L]) {
     else asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]), "+v"(w[4])::"memory");
 }
 
-// Stores the tile's outputs (unscaled).  The full tile adds its even- and
-// odd-block sums; the pair tile's sit in lane groups g and g + 2 (output rows
-// m' and m' + 8).  All 64 lanes of the wave call this.
+// The tile's outputs, scaled: out[j][r] of column 16 j + ... as stored below.
+// The full tile adds its even- and odd-block sums; the pair tile's sit in lane
+// groups g and g + 2 (output rows m' and m' + 8).  All 64 lanes call this.
 template <class TF, int MP>
-__device__ __forceinline__ void store_tile(const f32x4 (&acc)[TileSet<MP>::kNA], float* __restrict__ Y, int N, int M,
-                                           int t, int g, int rn) {
-    constexpr float kUnscale = TF::kUnscale;
+struct TileOut {
     using TS = TileSet<MP>;
-    const int n = t * 16 + rn;
-    f32x4 pr = {0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (TS::kPair) {
+    float full[TS::kFull ? 4 : 1], pair[TS::kPair ? 4 : 1];
+    __device__ __forceinline__ explicit TileOut(const f32x4 (&acc)[TS::kNA]) {
+        if constexpr (TS::kFull) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) pr[r] = acc[TS::kPairAcc][r] + __shfl_xor(acc[TS::kPairAcc][r], 32);
-    }
-    if (n >= N) return;
-    if constexpr (TS::kFull) {
+            for (int r = 0; r < 4; ++r) full[r] = (acc[0][r] + acc[1][r]) * TF::kUnscale;
+        }
+        if constexpr (TS::kPair) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int m = g * 4 + r;
-            if (m < M) Y[(size_t)m * N + n] = (acc[0][r] + acc[1][r]) * kUnscale;
+            for (int r = 0; r < 4; ++r)
+                pair[r] = (acc[TS::kPairAcc][r] + __shfl_xor(acc[TS::kPairAcc][r], 32)) * TF::kUnscale;
         }
     }
-    if constexpr (TS::kPair) {
-        if (g < 2) {
+    __device__ __forceinline__ void gate(int act, const TileOut& up) {
+        if constexpr (TS::kFull) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) full[r] = glu(act, full[r], up.full[r]);
+        }
+        if constexpr (TS::kPair) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) pair[r] = glu(act, pair[r], up.pair[r]);
+        }
+    }
+    __device__ __forceinline__ void store(float* __restrict__ Y, int N, int M, int t, int g, int rn) const {
+        const int n = t * 16 + rn;
+        if (n >= N) return;
+        if constexpr (TS::kFull) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int m = TS::kC0 + g * 4 + r;
-                if (m < M) Y[(size_t)m * N + n] = pr[r] * kUnscale;
+                const int m = g * 4 + r;
+                if (m < M) Y[(size_t)m * N + n] = full[r];
+            }
+        }
+        if constexpr (TS::kPair) {
+            if (g < 2) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int m = TS::kC0 + g * 4 + r;
+                    if (m < M) Y[(size_t)m * N + n] = pair[r];
+                }
             }
         }
     }
-}
+};
 
 // ---------------------------------------------------------------------------
 // The GEMV.  MP = 8 (M <= 8: one pair tile), 16 (one full tile) or 24 (a
 // full tile and a pair tile); columns past M re-read column M - 1, their
 // results dropped.
 // ---------------------------------------------------------------------------
-template <class TF, int MP, int RT, int KW, int D>
+template <class TF, int MP, int RT, int KW, int D, bool GLU>
 __global__ void __launch_bounds__(64 * RT * KW)
 k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* __restrict__ Y,
            uint32_t* __restrict__ tickets, f32x4* __restrict__ part, int N, int K, int M, int KP, int spw,
-           int cs_slots, uint32_t cs_magic, int CS, int groups, int pre) {
+           int cs_slots, uint32_t cs_magic, int CS, int groups, int pre, GluArgs<GLU> glu_args) {
+    static_assert(!GLU || RT % 2 == 0, "gate and up tiles in pairs");
     using TS = TileSet<MP>;
     constexpr int NA = TS::kNA;
     constexpr int W = RT * KW;
@@ -374,8 +399,10 @@ k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* _
     const int spk = (ns + KW - 1) / KW;
     const int w0 = kw * spk;                       // the wave's part: groups w0 .. w0 + cnt - 1 of the range
     const int cnt = max(0, min(spk, ns - w0));     // wave-uniform
-    const int t = grp * RT + rt;
+    const int t = GLU ? grp * (RT / 2) + (rt >> 1) : grp * RT + rt;
     const int tc = t < T ? t : T - 1;
+    const bool up = GLU && (rt & 1);   // wave-uniform
+    if constexpr (GLU) Wt = up ? glu_args.Wu : Wt;
     constexpr int kGroupBytes = TF::kGroupBytes;
     constexpr int L = TF::kCodeLoads + 1;   // 16-byte loads per lane and group
     const uint8_t* const wbase = Wt + ((size_t)tc * S + s0 + (cnt > 0 ? w0 : 0)) * kGroupBytes;
@@ -492,9 +519,11 @@ k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* _
                 }
         }
     }
-    if (KP == 1) {
-        if (kw == 0 && t < T) store_tile<TF, MP>(acc, Y, N, M, t, g, rn);
-        return;
+    if constexpr (!GLU) {
+        if (KP == 1) {
+            if (kw == 0 && t < T) TileOut<TF, MP>(acc).store(Y, N, M, t, g, rn);
+            return;
+        }
     }
 
     // KP ranges: partial tile sums to the workspace, then a ticket.  Every
@@ -506,46 +535,70 @@ k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* _
     // invalidate on this chip, both of whole caches) measured 15-140 us per
     // call, and are not needed when every shared access is atomic.
     const int slot = grp * CS + cs;   // this slice's ticket counter and partial sums
-    float* const mine = reinterpret_cast<float*>(part + (((size_t)slot * KP + kp) * RT + rt) * NA * kWave);
-    if (kw == 0) {
+    if (!GLU || KP > 1) {
+        float* const mine = reinterpret_cast<float*>(part + (((size_t)slot * KP + kp) * RT + rt) * NA * kWave);
+        if (kw == 0) {
 #pragma unroll
-        for (int a = 0; a < NA; ++a)
+            for (int a = 0; a < NA; ++a)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                __hip_atomic_store(mine + (a * kWave + lane) * 4 + r, acc[a][r], __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's partial sums are stored
-    __syncthreads();
-    if (threadIdx.x == 0)
-        last_ticket = __hip_atomic_fetch_add(tickets + slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                      (uint32_t)(KP - 1);
-    __syncthreads();
-    if (!last_ticket) return;   // workgroup-uniform
-    if (kw == 0 && t < T) {
-        f32x4 sum[NA];
-        for (int k2 = 0; k2 < KP; ++k2) {
-            const float* const src =
-                reinterpret_cast<const float*>(part + (((size_t)slot * KP + k2) * RT + rt) * NA * kWave);
+                for (int r = 0; r < 4; ++r)
+                    __hip_atomic_store(mine + (a * kWave + lane) * 4 + r, acc[a][r], __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's partial sums are stored
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last_ticket = __hip_atomic_fetch_add(tickets + slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                          (uint32_t)(KP - 1);
+        __syncthreads();
+        if (!last_ticket) return;   // workgroup-uniform
+        if (kw == 0 && t < T) {
+            f32x4 sum[NA];
+            for (int k2 = 0; k2 < KP; ++k2) {
+                const float* const src =
+                    reinterpret_cast<const float*>(part + (((size_t)slot * KP + k2) * RT + rt) * NA * kWave);
 #pragma unroll
-            for (int a = 0; a < NA; ++a) {
-                f32x4 v = acc[a];
-                if (k2 != kp) {
+                for (int a = 0; a < NA; ++a) {
+                    f32x4 v = acc[a];
+                    if (k2 != kp) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[r] = __hip_atomic_load(src + (a * kWave + lane) * 4 + r, __ATOMIC_RELAXED,
-                                                 __HIP_MEMORY_SCOPE_AGENT);
-                }
-                if (k2 == 0) sum[a] = v;
-                else {
+                        for (int r = 0; r < 4; ++r)
+                            v[r] = __hip_atomic_load(src + (a * kWave + lane) * 4 + r, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT);
+                    }
+                    if (k2 == 0) sum[a] = v;
+                    else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) sum[a][r] += v[r];
+                        for (int r = 0; r < 4; ++r) sum[a][r] += v[r];
+                    }
                 }
             }
+            if constexpr (GLU) {
+#pragma unroll
+                for (int a = 0; a < NA; ++a) acc[a] = sum[a];
+            } else {
+                TileOut<TF, MP>(sum).store(Y, N, M, t, g, rn);
+            }
         }
-        store_tile<TF, MP>(sum, Y, N, M, t, g, rn);
+        if (threadIdx.x == 0) __hip_atomic_store(tickets + slot, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (threadIdx.x == 0) __hip_atomic_store(tickets + slot, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if constexpr (GLU) {   // the up sums to the gate's wave, which stores the tile's outputs
+        f32x4* red = reinterpret_cast<f32x4*>(lds);   // a slot per wave; only a pair's waves use those of kw = 0
+        if constexpr (KW == 1) lds_barrier();         // every wave is done with the activation copies
+        if (kw == 0 && up) {
+#pragma unroll
+            for (int a = 0; a < NA; ++a) red[(wave * NA + a) * kWave + lane] = acc[a];
+        }
+        lds_barrier();
+        if (kw == 0 && !up && t < T) {
+            f32x4 us[NA];
+#pragma unroll
+            for (int a = 0; a < NA; ++a) us[a] = red[((wave + KW) * NA + a) * kWave + lane];
+            TileOut<TF, MP> out(acc);
+            out.gate(glu_args.act, TileOut<TF, MP>(us));
+            out.store(Y, N, M, t, g, rn);
+        }
+    }
 }
 
 // f32x4 accumulators per lane for M columns (TileSet<MP>::kNA).
@@ -582,7 +635,8 @@ bool tiles_built(int RT, int KW, int D) {
     return false;
 }
 
-bool tiles_plan(int N, int K, int M, int RT, int KW, int D, int KP, int CS, TilesPlan& p) {
+// T: row tiles (of both matrices, for a gated product).
+bool tiles_plan(int T, int K, int M, int RT, int KW, int D, int KP, int CS, TilesPlan& p) {
     const int S = K >> 8;
     if (S < 1 || KP < 1 || KP > kTilesMaxKP || !tiles_built(RT, KW, D)) return false;
     if (CS < 1 || CS > kTilesMaxCS) return false;
@@ -601,7 +655,7 @@ bool tiles_plan(int N, int K, int M, int RT, int KW, int D, int KP, int CS, Tile
     const size_t act = (size_t)((M * p.cs_slots + kWave - 1) / kWave) * 1024 + (pair ? (size_t)p.cs_slots * 16 : 0);
     const size_t red = (size_t)RT * KW * NA * kWave * 16;
     p.lds = act > red ? act : red;
-    p.groups = ((N + 15) / 16 + RT - 1) / RT;
+    p.groups = (T + RT - 1) / RT;
     if (p.KP > 1 && p.groups * CS > kTicketSlots) return false;   // one ticket counter per row group and slice
     // LDS of one workgroup; the quotient by the column stride (a multiply-high
     // by ceil(2^32 / stride)) is exact for strides below 2^14 and slots below 2^18
@@ -643,7 +697,7 @@ void tiles_default(bool q8, int N, int K, int M, int& RT, int& KW, int& D, int& 
     TilesPlan p;
     CS = 0;
     for (int c : cand)
-        if (c > 0 && tiles_plan(N, K, M, 1, 4, 2, 1, c, p)) {
+        if (c > 0 && tiles_plan(T, K, M, 1, 4, 2, 1, c, p)) {
             CS = c;
             break;
         }
@@ -674,20 +728,22 @@ void tiles_default(bool q8, int N, int K, int M, int& RT, int& KW, int& D, int& 
     const int Mh = (M + CS - 1) / CS;
     const size_t fit = 150 * 1024;   // the columns of one range in LDS
     while (KP < kTilesMaxKP && KP < S && (size_t)Mh * ((S + KP - 1) / KP) * kGroupSlots * 16 > fit) KP *= 2;
+    // few columns: the pair tile's zero column takes LDS as well
+    while (KP < kTilesMaxKP && KP < S && !tiles_plan(T, K, M, 4, 2, 2, KP, CS, p)) KP *= 2;
     RT = KP * CS >= 4 ? 4 : 2;
     KW = KP * CS >= 4 ? 2 : 4;
 }
 
-template <class TF, int MP, int RT, int KW, int D>
+template <class TF, int MP, int RT, int KW, int D, bool GLU = false>
 hipError_t launch_tiles_cfg(const TilesPlan& p, const void* Wt, const void* Xq, float* Y, void* ws, int N, int K,
-                            int M, hipStream_t s) {
+                            int M, hipStream_t s, GluArgs<GLU> ga = {}) {
     uint32_t* tickets = reinterpret_cast<uint32_t*>(ws);
     f32x4* part = reinterpret_cast<f32x4*>(reinterpret_cast<uint8_t*>(ws) + kTicketBytes);
     const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) + (uint64_t)p.cs_slots - 1) / (uint64_t)p.cs_slots);
     const int grid = p.CS == 1 ? p.groups * p.KP : (p.groups * p.KP + 7) / 8 * 8 * p.CS;
-    hipLaunchKernelGGL((k_tiles<TF, MP, RT, KW, D>), dim3(grid), dim3(64 * RT * KW), p.lds, s, (const uint8_t*)Wt,
+    hipLaunchKernelGGL((k_tiles<TF, MP, RT, KW, D, GLU>), dim3(grid), dim3(64 * RT * KW), p.lds, s, (const uint8_t*)Wt,
                        (const uint8_t*)Xq, Y, tickets, part, N, K, M, p.KP, p.spw, p.cs_slots, magic, p.CS,
-                       p.groups, p.pre);
+                       p.groups, p.pre, ga);
     return hipGetLastError();
 }
 
@@ -719,6 +775,27 @@ hipError_t launch_tiles_fmt(const TilesPlan& p, const void* Wt, const void* Xq, 
     if (p.Mh <= 8) return launch_tiles_mp<TF, 8>(p, Wt, Xq, Y, ws, N, K, M, s);
     if (p.Mh <= 16) return launch_tiles_mp<TF, 16>(p, Wt, Xq, Y, ws, N, K, M, s);
     return launch_tiles_mp<TF, 24>(p, Wt, Xq, Y, ws, N, K, M, s);
+}
+
+// The gated product's configurations: pairs of row tiles over KW parts of K.
+template <class TF, int MP>
+hipError_t launch_tiles_glu_mp(const TilesPlan& p, const GluMatrices& w, const void* Xq, float* Y, void* ws, int N,
+                               int K, int M, hipStream_t s) {
+    const GluArgs<true> ga = {(const uint8_t*)w.up, w.act};
+#define DG_TG(RR, WW, DD)                                                                                   \
+    if (p.RT == RR && p.KW == WW && p.D == DD)                                                              \
+        return launch_tiles_cfg<TF, MP, RR, WW, DD, true>(p, w.gate, Xq, Y, ws, N, K, M, s, ga);
+    DG_TG(2, 4, 2) DG_TG(2, 8, 2) DG_TG(4, 2, 2) DG_TG(4, 4, 2)
+#undef DG_TG
+    return hipErrorInvalidValue;
+}
+
+template <class TF>
+hipError_t launch_tiles_glu_fmt(const TilesPlan& p, const GluMatrices& w, const void* Xq, float* Y, void* ws, int N,
+                                int K, int M, hipStream_t s) {
+    if (p.Mh <= 8) return launch_tiles_glu_mp<TF, 8>(p, w, Xq, Y, ws, N, K, M, s);
+    if (p.Mh <= 16) return launch_tiles_glu_mp<TF, 16>(p, w, Xq, Y, ws, N, K, M, s);
+    return launch_tiles_glu_mp<TF, 24>(p, w, Xq, Y, ws, N, K, M, s);
 }
 
 }  // namespace
@@ -759,7 +836,7 @@ static bool tiles_resolve(bool q8, int N, int K, int M, int unroll, TilesPlan& p
     }
     const int late = D >= 10;   // D + 10: the other prologue order (measurements only)
     if (late) D -= 10;
-    const bool ok = tiles_plan(N, K, M, RT, KW, D, KP, CS, p);
+    const bool ok = tiles_plan((N + 15) / 16, K, M, RT, KW, D, KP, CS, p);
     p.pre = !late;
     return ok;
 }
@@ -777,6 +854,33 @@ hipError_t launch_tiles(bool q8, int M, int unroll, const void* Wt, const void* 
     if (!tiles_resolve(q8, N, K, M, unroll, p) || p.lds > device_max_lds_per_block()) return hipErrorInvalidValue;
     return q8 ? launch_tiles_fmt<TilesQ8_0>(p, Wt, Xq, Y, ws, N, K, M, s)
               : launch_tiles_fmt<TilesQ4_0>(p, Wt, Xq, Y, ws, N, K, M, s);
+}
+
+// The gated product's plan: that of a GEMV over the row tiles of both
+// matrices, one row tile per workgroup becoming a pair over 8 parts of K.
+static bool tiles_glu_resolve(bool q8, int N, int K, int M, TilesPlan& p) {
+    const int T2 = 2 * ((N + 15) / 16);
+    int RT, KW, D, KP, CS;
+    tiles_default(q8, 16 * T2, K, M, RT, KW, D, KP, CS);
+    if (RT == 1) RT = 2;
+    const bool ok = tiles_plan(T2, K, M, RT, KW, D, KP, CS, p);
+    p.pre = 1;
+    return ok;
+}
+
+bool tiles_glu_config(bool q8, int N, int K, int M, size_t* ws_bytes) {
+    TilesPlan p;
+    if (N <= 0 || K <= 0 || M <= 0 || M > 24 || !tiles_glu_resolve(q8, N, K, M, p)) return false;
+    *ws_bytes = tiles_ws_bytes(p);
+    return true;
+}
+
+hipError_t launch_tiles_glu(bool q8, int M, const GluMatrices& w, const void* Xq, float* Y, void* ws, int N, int K,
+                            hipStream_t s) {
+    TilesPlan p;
+    if (!tiles_glu_resolve(q8, N, K, M, p) || p.lds > device_max_lds_per_block()) return hipErrorInvalidValue;
+    return q8 ? launch_tiles_glu_fmt<TilesQ8_0>(p, w, Xq, Y, ws, N, K, M, s)
+              : launch_tiles_glu_fmt<TilesQ4_0>(p, w, Xq, Y, ws, N, K, M, s);
 }
 
 }  // namespace dg

@@ -106,3 +106,40 @@ def test_sample_workspace(lib):
     assert f(0, 128256) == 0 and f(-1, 128256) == 0 and f(7, 4096) == 0
     one = f(1, 4097)
     assert one > 0 and f(3, 128256) == 3 * one and f(512, 4097) == 512 * one == f(100000, 4097)
+
+
+@pytest.mark.parametrize("args,expect", [
+    ((A, A, A, A, 4, 256, 1, 4), ARG),                # unknown activation
+    ((A, A, A, A, 4, 256, 1, -1), ARG),
+    ((A, A, A, A, 4, 100, 1, 0), SHAPE),              # K % 256
+    ((A, A, A, A, 4, 256, 25, 0), SHAPE),
+    ((A, A, A, A, 4, 256, -1, 0), SHAPE),
+    ((A, A, A, A, -1, 256, 1, 0), SHAPE),
+    ((A, A, A, A, 1 << 31, 256, 1, 0), SHAPE),
+    ((A, A, A, A, 4, (1 << 26) + 256, 1, 0), SHAPE),
+    ((None, A, A, A, 4, 256, 1, 0), NULL),
+    ((A, None, A, A, 4, 256, 1, 0), NULL),
+    ((A, A, None, A, 4, 256, 1, 0), NULL),
+    ((A, A, A, None, 4, 256, 1, 0), NULL),
+    ((P(0x1008), A, A, A, 4, 256, 1, 0), MISALIGNED),
+    ((A, P(0x1008), A, A, 4, 256, 1, 0), MISALIGNED),
+    ((A, A, P(0x1004), A, 4, 256, 1, 0), MISALIGNED),
+    ((A, A, A, P(0x1002), 4, 256, 1, 0), MISALIGNED),
+    ((None, None, None, None, 0, 256, 1, 0), OK),
+    ((None, None, None, None, 4, 256, 0, 0), OK),
+])
+def test_gemv_glu_rejects_before_launch(lib, args, expect):
+    for f in ("q4_0", "q8_0"):
+        assert getattr(lib, f"dg_gemv_{f}_glu")(*args, None) == expect
+        assert getattr(lib, f"dg_gemv_{f}_tiles_glu")(*args, None, 0, None) == expect
+
+
+def test_gemv_tiles_glu_workspace(lib):
+    need = lib.dg_gemv_q4_0_tiles_glu_workspace_bytes(64, 28672, 24)
+    assert need > 0 and lib.dg_gemv_q4_0_tiles_glu_workspace_bytes(14336, 4096, 16) == 0
+    assert lib.dg_gemv_q4_0_tiles_glu_workspace_bytes(64, 100, 24) == 0
+    assert lib.dg_gemv_q8_0_tiles_glu_workspace_bytes(0, 4096, 24) == 0
+    f = lib.dg_gemv_q4_0_tiles_glu
+    assert f(A, A, A, A, 64, 28672, 24, 0, None, 0, None) == WORKSPACE
+    assert f(A, A, A, A, 64, 28672, 24, 0, A, need - 1, None) == WORKSPACE
+    assert f(A, A, A, A, 64, 28672, 24, 0, P(0x1008), need, None) == MISALIGNED
