@@ -251,28 +251,51 @@ def _need(t, dtypes, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _here(t, name):
+    """The current device's index, on which tensor t has to be: a call runs there, on its current stream."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    cur = _torch().cuda.current_device()
+    if dev != cur:
+        raise ValueError(f"{name} is on device {dev}, the current device is {cur}")
+    return dev
+
+
+def _arg(name, t, dev, dtype, nbytes):
+    """The address of operand t (None: None), a contiguous tensor of `dtype` on device dev that spans at least nbytes."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        where = f"on device {t.get_device()}" if t.is_cuda else "a host tensor"
+        raise ValueError(f"{name} is {where}, the call runs on device {dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.nbytes < nbytes:
+        raise ValueError(f"{name} holds {t.nbytes} bytes but the call touches {nbytes}")
+    return t.data_ptr()
+
+
+_float_ids = {}   # torch dtype -> DG_DTYPE_*
+
+
 def _dtype_id(t, name):
     """The DG_DTYPE_* of a float tensor."""
-    torch = _torch()
-    ids = {torch.float32: DG_DTYPE_F32, torch.float16: DG_DTYPE_F16, torch.bfloat16: DG_DTYPE_BF16}
-    if t.dtype not in ids:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(ids)}")
-    return ids[t.dtype]
+    if not _float_ids:
+        torch = _torch()
+        _float_ids.update({torch.float32: DG_DTYPE_F32, torch.float16: DG_DTYPE_F16, torch.bfloat16: DG_DTYPE_BF16})
+    if t.dtype not in _float_ids:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(_float_ids)}")
+    return _float_ids[t.dtype]
 
 
-def _need_here(**tensors):
-    """Raises unless every given tensor is contiguous on the current device: a
-    call runs there, on its current stream."""
-    dev = _torch().cuda.current_device()
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a device tensor")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _stream_here(stream, dev):
+    """The handle of `stream`, or of the current stream of device dev."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _fits(t, nbytes, name):
@@ -507,30 +530,21 @@ _ACTS = {"silu": DG_ACT_SILU, "gelu": DG_ACT_GELU, "gelu_tanh": DG_ACT_GELU_TANH
 
 def _gemv_glu(fmt, tiles, Wg, Wu, Xq, Y, N, K, M, act, ws, stream):
     torch = _torch()
-    _need_here(Wg=Wg, Wu=Wu, Xq=Xq, Y=Y, ws=ws)
+    dev = _here(Y, "Y")
     if act not in _ACTS:
         raise ValueError(f"act must be one of {tuple(_ACTS)}, not {act!r}")
-    for name, t, want in (("Wg", Wg, torch.uint8), ("Wu", Wu, torch.uint8), ("Xq", Xq, torch.uint8),
-                          ("Y", Y, torch.float32), ("ws", ws, torch.uint8)):
-        if t is not None and t.dtype != want:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {want}")
     N, K, M = int(N), int(K), int(M)
-    lib = _lib()
-    if N > 0 and K > 0 and M > 0:
-        rows = (N + 15) // 16 * 16 if tiles else N
-        need = rows * (K // 32) * (18 if fmt == "q4_0" else 34)
-        _fits(Wg, need, "Wg")
-        _fits(Wu, need, "Wu")
-        _fits(Xq, M * (K // 32) * 36, "Xq")
-    if N > 0 and M > 0:
-        _fits(Y, M * N * 4, "Y")
-    args = (_ptr(Wg), _ptr(Wu), _ptr(Xq), _ptr(Y), N, K, M, _ACTS[act])
+    blocks = K // 32 if N > 0 and K > 0 and M > 0 else 0
+    weights = ((N + 15) // 16 * 16 if tiles else N) * blocks * (18 if fmt == "q4_0" else 34)
+    args = (_arg("Wg", Wg, dev, torch.uint8, weights), _arg("Wu", Wu, dev, torch.uint8, weights),
+            _arg("Xq", Xq, dev, torch.uint8, M * blocks * 36),
+            _arg("Y", Y, dev, torch.float32, M * N * 4 if N > 0 and M > 0 else 0), N, K, M, _ACTS[act])
     if tiles:
         name = f"dg_gemv_{fmt}_tiles_glu"
-        args += (_ptr(ws), ws.numel() if ws is not None else 0)
+        args += (_arg("ws", ws, dev, torch.uint8, 0), ws.nbytes if ws is not None else 0)
     else:
         name = f"dg_gemv_{fmt}_glu"
-    _check(getattr(lib, name)(*args, _stream(stream)), name)
+    _check(getattr(_lib(), name)(*args, _stream_here(stream, dev)), name)
     return Y
 
 
@@ -648,11 +662,8 @@ def dg_quantize_q8_0(w, Wq, N, K, stream=None):
 
 
 def _rmsnorm(x, w, out, res, h, eps, M, K, ld, ldy, stream):
-    _need_here(x=x, w=w, out=out, res=res, h=h)
+    dev = _here(x, "x")
     dtype, wdtype = _dtype_id(x, "x"), _dtype_id(w, "w")
-    for name, t in (("res", res), ("h", h)):
-        if t is not None and t.dtype != x.dtype:
-            raise TypeError(f"{name} has dtype {t.dtype}, x has {x.dtype}")
     if M is None:
         M = x.shape[0] if x.dim() == 2 else 1
     if K is None:
@@ -660,24 +671,18 @@ def _rmsnorm(x, w, out, res, h, eps, M, K, ld, ldy, stream):
     if ld is None:
         ld = x.shape[-1]
     M, K, ld = int(M), int(K), int(ld)
-    if M > 0 and K > 0 and ld >= K:
-        need = ((M - 1) * ld + K) * x.element_size()
-        for name, t in (("x", x), ("res", res), ("h", h)):
-            if t is not None:
-                _fits(t, need, name)
-        _fits(w, K * w.element_size(), "w")
-    if ldy is None:   # Q8_1 columns
-        _need(out, (_torch().uint8,), "Xq")
-        if M > 0 and K > 0:
-            _fits(out, M * (K // 32) * 36, "Xq")
-        _check(_lib().dg_rmsnorm_q8_1(_ptr(x), _ptr(res), _ptr(h), dtype, _ptr(w), wdtype, _ptr(out), M, K, ld,
-                                      float(eps), _stream(stream)), "dg_rmsnorm_q8_1")
+    live = M > 0 and K > 0
+    span = ((M - 1) * ld + K) * x.element_size() if live and ld >= K else 0
+    xa, ra, ha = (_arg(name, t, dev, x.dtype, span) for name, t in (("x", x), ("res", res), ("h", h)))
+    wa = _arg("w", w, dev, w.dtype, K * w.element_size() if live else 0)
+    st = _stream_here(stream, dev)
+    if ldy is None:
+        oa = _arg("Xq", out, dev, _torch().uint8, M * (K // 32) * 36 if live else 0)
+        _check(_lib().dg_rmsnorm_q8_1(xa, ra, ha, dtype, wa, wdtype, oa, M, K, ld, eps, st), "dg_rmsnorm_q8_1")
         return out
     ydtype, ldy = _dtype_id(out, "y"), int(ldy)
-    if M > 0 and K > 0 and ldy >= K:
-        _fits(out, ((M - 1) * ldy + K) * out.element_size(), "y")
-    _check(_lib().dg_rmsnorm(_ptr(x), _ptr(res), _ptr(h), dtype, _ptr(w), wdtype, _ptr(out), ydtype, M, K, ld, ldy,
-                             float(eps), _stream(stream)), "dg_rmsnorm")
+    oa = _arg("y", out, dev, out.dtype, ((M - 1) * ldy + K) * out.element_size() if live and ldy >= K else 0)
+    _check(_lib().dg_rmsnorm(xa, ra, ha, dtype, wa, wdtype, oa, ydtype, M, K, ld, ldy, eps, st), "dg_rmsnorm")
     return out
 
 
@@ -820,7 +825,7 @@ def dg_sample_rows(x, u, idx, R=None, C=None, ld=None, temperature=None, top_k=N
     each, or None).  ws: a device workspace of dg_sample_workspace_bytes(R, C)
     bytes; None is allowed when that is 0."""
     torch = _torch()
-    _need_here(x=x, u=u, idx=idx, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, ws=ws)
+    dev = _here(x, "x")
     dtype = _dtype_id(x, "x")
     if R is None:
         R = x.shape[0] if x.dim() == 2 else 1
@@ -829,17 +834,12 @@ def dg_sample_rows(x, u, idx, R=None, C=None, ld=None, temperature=None, top_k=N
     if ld is None:
         ld = x.shape[-1]
     R, C, ld = int(R), int(C), int(ld)
-    if R > 0 and C > 0 and ld >= C:
-        _fits(x, ((R - 1) * ld + C) * x.element_size(), "x")
-    for name, t, want in (("u", u, torch.float32), ("idx", idx, torch.int64), ("temperature", temperature, torch.float32),
-                          ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
-                          ("min_p", min_p, torch.float32)):
-        if t is None:
-            continue
-        if t.dtype != want:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {want}")
-        _fits(t, max(R, 0) * t.element_size(), name)
-    ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
-    _check(_lib().dg_sample_rows(_ptr(x), dtype, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
-                                 _ptr(idx), R, C, ld, _ptr(ws), ws_bytes, _stream(stream)), "dg_sample_rows")
+    n, f32 = max(R, 0), torch.float32
+    xa = _arg("x", x, dev, x.dtype, ((R - 1) * ld + C) * x.element_size() if R > 0 and ld >= C > 0 else 0)
+    _check(_lib().dg_sample_rows(xa, dtype, _arg("u", u, dev, f32, n * 4),
+                                 _arg("temperature", temperature, dev, f32, n * 4),
+                                 _arg("top_k", top_k, dev, torch.int32, n * 4), _arg("top_p", top_p, dev, f32, n * 4),
+                                 _arg("min_p", min_p, dev, f32, n * 4), _arg("idx", idx, dev, torch.int64, n * 8), R,
+                                 C, ld, _arg("ws", ws, dev, torch.uint8, 0), ws.nbytes if ws is not None else 0,
+                                 _stream_here(stream, dev)), "dg_sample_rows")
     return idx

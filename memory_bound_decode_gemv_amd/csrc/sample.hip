@@ -60,6 +60,41 @@ struct Logit {
     __device__ __forceinline__ static float load(const T* p) { return (float)*p; }
 };
 
+constexpr int kPer = 8;   // elements per thread of the chunk kernels: kChunkThreads of them fill a shortest sub-chunk
+static_assert(kPer * kChunkThreads == kSubMin, "one load step per shortest sub-chunk");
+
+// This thread's kPer elements of the kSubMin from c0 on (those at C and past
+// it as -infinity, which has no weight): consecutive ones in one or two
+// 16-byte loads where the row is 16-byte aligned, else a coalesced stride
+// apart.  element(i, vec) is the offset of the i-th from c0.
+template <class T>
+struct Share {
+    float v[kPer];
+    __device__ __forceinline__ static int element(int i, bool vec) {
+        return vec ? (int)threadIdx.x * kPer + i : i * kChunkThreads + (int)threadIdx.x;
+    }
+    __device__ __forceinline__ void load(const T* __restrict__ row, int64_t c0, int64_t C, bool vec) {
+        constexpr int kVecs = kPer * sizeof(T) / 16;
+        if (vec && c0 + element(kPer - 1, true) < C) {
+            union {
+                u32x4 q[kVecs];
+                T e[kPer];
+            } b;
+            const u32x4* p = reinterpret_cast<const u32x4*>(row + c0 + element(0, true));
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) b.q[i] = p[i];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) v[i] = (float)b.e[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int64_t c = c0 + element(i, vec);
+                v[i] = c < C ? Logit<T>::load(row + c) : -INFINITY;
+            }
+        }
+    }
+};
+
 struct SampleArgs {
     const float *u, *temperature, *top_p, *min_p;
     const int32_t* top_k;
@@ -71,6 +106,7 @@ struct SampleArgs {
     int nsub;
     int G;          // chunks per row
     int subs_per_chunk;
+    bool vec;       // rows are 16-byte aligned
 };
 
 // The workspace of one row.
@@ -102,11 +138,28 @@ struct Row {
     int k;            // 0: off
     int F;
 
-    // w as a binary64 number in [0, 1] (0 where the quotient is not a number)
+    // w = 2^t, t = (x - m) log2(e) / T, as a binary64 number in [0, 1] (0 where
+    // t is not a number): t = n + f with n an integer and |f| <= 1/2, and
+    // 2^f = sum (f ln 2)^k / k!, whose terms past k = 12 are below 2^-52.
     __device__ __forceinline__ double weight(float x) const {
-        if (x == m) return 1.0;
-        const double e = exp2(((double)x - (double)m) * c);
-        return e >= 0.0 ? e : 0.0;
+        const double d = x == m ? 0.0 : (double)x - (double)m;
+        const double t = fmax(d * c, -1100.0);
+        const double n = rint(t);
+        const double f = t - n;
+        double e = 2.5678435993488196e-11;   // (ln 2)^k / k!, k = 12 .. 0
+        e = fma(e, f, 4.44553827187081e-10);
+        e = fma(e, f, 7.054911620801121e-09);
+        e = fma(e, f, 1.0178086009239696e-07);
+        e = fma(e, f, 1.3215486790144305e-06);
+        e = fma(e, f, 1.5252733804059838e-05);
+        e = fma(e, f, 1.5403530393381606e-04);
+        e = fma(e, f, 1.3333558146428441e-03);
+        e = fma(e, f, 9.618129107628477e-03);
+        e = fma(e, f, 5.5504108664821576e-02);
+        e = fma(e, f, 2.402265069591007e-01);
+        e = fma(e, f, 6.931471805599453e-01);
+        e = fma(e, f, 1.0);
+        return ldexp(e, (int)n);
     }
     // round(2^F w) by the binary64 addition 2^52 + 2^F w (F <= 51)
     __device__ __forceinline__ u64 fixed(double w) const {
@@ -153,21 +206,35 @@ __device__ __forceinline__ float wave_min_f32(float v) {
     return v;
 }
 
-__device__ __forceinline__ u64 wave_sum_u64(u64 v) {
-#pragma unroll
-    for (int o = kWave / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+// Inclusive sums over the wave, on DPP moves (lanes without a source receive 0).
+__device__ __forceinline__ u64 wave_scan_u64(u64 v) {
+    v += dpp_key<kDppRowShr1, 0xF>(v);
+    v += dpp_key<kDppRowShr2, 0xF>(v);
+    v += dpp_key<kDppRowShr4, 0xF>(v);
+    v += dpp_key<kDppRowShr8, 0xF>(v);
+    v += dpp_key<kDppRowBcast15, 0xA>(v);
+    v += dpp_key<kDppRowBcast31, 0xC>(v);
     return v;
 }
 
-__device__ __forceinline__ u64 wave_scan_u64(u64 v) {   // inclusive
-    const int lane = lane_id();
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const u64 t = __shfl_up(v, o);
-        if (lane >= o) v += t;
-    }
+__device__ __forceinline__ u64 wave_or_u64(u64 v) {   // in lane 63
+    v |= dpp_key<kDppRowShr1, 0xF>(v);
+    v |= dpp_key<kDppRowShr2, 0xF>(v);
+    v |= dpp_key<kDppRowShr4, 0xF>(v);
+    v |= dpp_key<kDppRowShr8, 0xF>(v);
+    v |= dpp_key<kDppRowBcast15, 0xA>(v);
+    v |= dpp_key<kDppRowBcast31, 0xC>(v);
     return v;
 }
+
+// A lane's value in every lane (the lane is the same in all of them).
+__device__ __forceinline__ u64 lane_u64(u64 v, int src) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, src);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), src);
+    return ((u64)hi << 32) | lo;
+}
+
+__device__ __forceinline__ u64 wave_sum_u64(u64 v) { return lane_u64(wave_scan_u64(v), kWave - 1); }
 
 // Inclusive sums over the workgroup in thread order; *total = the whole sum.
 template <int THREADS>
@@ -213,13 +280,17 @@ k_sample_max(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs 
     const int64_t c1 = c0 + (int64_t)a.subs_per_chunk * a.sub < a.C ? c0 + (int64_t)a.subs_per_chunk * a.sub : a.C;
     uint32_t best = 0u, bidx = 0xFFFFFFFFu;
     float low = INFINITY;
-    for (int64_t c = c0 + threadIdx.x; c < c1; c += kChunkThreads) {
-        const float v = Logit<T>::load(row + c);
-        const uint32_t img = order_image(v);
-        if (img > best) { best = img; bidx = (uint32_t)c; }
-        if (v > -INFINITY) low = fminf(low, v);
+    for (int64_t c = c0; c < c1; c += kSubMin) {
+        Share<T> e;
+        e.load(row, c, a.C, a.vec);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {   // a thread's elements in increasing order
+            const uint32_t img = order_image(e.v[i]);
+            if (img > best) { best = img; bidx = (uint32_t)(c + Share<T>::element(i, a.vec)); }
+            if (e.v[i] > -INFINITY) low = fminf(low, e.v[i]);
+        }
     }
-    u64 key = wave_max_u64(bidx == 0xFFFFFFFFu ? 0ull : pack_key(best, bidx));
+    u64 key = wave_max_u64(pack_key(best, bidx));
     low = wave_min_f32(low);
     __shared__ u64 keys[kChunkThreads / kWave];
     __shared__ float lows[kChunkThreads / kWave];
@@ -267,21 +338,29 @@ k_sample_hist(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
     const T* row = x + r * a.ld;
     const int64_t c0 = (int64_t)g * a.subs_per_chunk * a.sub;
     const int64_t c1 = c0 + (int64_t)a.subs_per_chunk * a.sub < a.C ? c0 + (int64_t)a.subs_per_chunk * a.sub : a.C;
-    for (int64_t c = c0 + threadIdx.x; c < c1; c += kChunkThreads) {
-        const float v = Logit<T>::load(row + c);
-        const u64 W = q.fixed(q.weight(v));
-        if (W) {
-            const int b = q.bin(v);
-            atomicAdd(&mass[b], W);
-            atomicAdd(&count[b], 1u);
+    // top-k needs the counts, top-p the masses.  Counting alone takes no
+    // weights: elements without weight are in the last bin, behind all others.
+    const bool by_mass = q.p < 1.0, by_count = q.k > 0;
+    for (int64_t c = c0; c < c1; c += kSubMin) {
+        Share<T> e;
+        e.load(row, c, a.C, a.vec);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const float v = e.v[i];
+            if (v > -INFINITY) {
+                const int b = q.bin(v);
+                if (by_mass) {
+                    const u64 W = q.fixed(q.weight(v));
+                    if (W) atomicAdd(&mass[b], W);
+                }
+                if (by_count) atomicAdd(&count[b], 1u);
+            }
         }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kChunkThreads) {
-        if (count[i]) {
-            atomicAdd(&ws->mass[i], mass[i]);
-            atomicAdd(&ws->count[i], count[i]);
-        }
+        if (mass[i]) atomicAdd(&ws->mass[i], mass[i]);
+        if (count[i]) atomicAdd(&ws->count[i], count[i]);
     }
 }
 
@@ -294,8 +373,7 @@ struct Borders {
     uint32_t krank;        // its rank within kbin, from 1
     u64 kmass;             // mass above kbin
     u64 pmass;             // mass above p0
-    u64 total;             // mass of all bins
-    uint32_t listed;       // elements in the border bins
+    u64 total;             // mass of all bins (0 without top-p)
 };
 
 __device__ __forceinline__ bool border_bin(const Borders& b, int i) { return i == b.kbin || (i >= b.p0 && i <= b.p1); }
@@ -310,20 +388,20 @@ __device__ __forceinline__ u64 p_target(double p, u64 total) {
 // eight per lane.
 __device__ __forceinline__ Borders find_borders(const RowSpace* ws, const Row& q) {
     __shared__ Borders out;
-    constexpr int kPer = kBins / kWave;
+    constexpr int kLaneBins = kBins / kWave;
     if (threadIdx.x < kWave) {
         const int lane = threadIdx.x;
-        u64 mass[kPer], m_in = 0;
-        uint32_t count[kPer], c_in = 0;
+        u64 mass[kLaneBins], m_in = 0;
+        uint32_t count[kLaneBins], c_in = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            mass[i] = ws->mass[lane * kPer + i];
-            count[i] = ws->count[lane * kPer + i];
+        for (int i = 0; i < kLaneBins; ++i) {
+            mass[i] = ws->mass[lane * kLaneBins + i];
+            count[i] = ws->count[lane * kLaneBins + i];
             m_in += mass[i];
             c_in += count[i];
         }
         const u64 m_to = wave_scan_u64(m_in), c_to = wave_scan_u64((u64)c_in);
-        const u64 m_all = __shfl(m_to, kWave - 1), c_all = __shfl(c_to, kWave - 1);
+        const u64 m_all = lane_u64(m_to, kWave - 1), c_all = lane_u64(c_to, kWave - 1);
         Borders b;
         b.total = m_all;
         b.kbin = kBins;
@@ -336,9 +414,9 @@ __device__ __forceinline__ Borders find_borders(const RowSpace* ws, const Row& q
             int bin = kBins;
             u64 rank = 0, above = 0, upto = 0;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
+            for (int i = 0; i < kLaneBins; ++i) {
                 if (bin == kBins && c < (u64)q.k && c + count[i] >= (u64)q.k) {
-                    bin = lane * kPer + i;
+                    bin = lane * kLaneBins + i;
                     rank = (u64)q.k - c;
                     above = m;
                     upto = m + mass[i];
@@ -347,11 +425,11 @@ __device__ __forceinline__ Borders find_borders(const RowSpace* ws, const Row& q
                 m += mass[i];
             }
             const int src = __ffsll((unsigned long long)__ballot(bin != kBins)) - 1;   // exactly one lane
-            b.kbin = __shfl(bin, src);
-            b.krank = (uint32_t)__shfl(rank, src);
-            b.kmass = __shfl(above, src);
+            b.kbin = __builtin_amdgcn_readlane(bin, src);
+            b.krank = (uint32_t)lane_u64(rank, src);
+            b.kmass = lane_u64(above, src);
             m_low = b.kmass;
-            m_high = __shfl(upto, src);
+            m_high = lane_u64(upto, src);
         }
         b.p0 = 1;
         b.p1 = 0;
@@ -366,28 +444,22 @@ __device__ __forceinline__ Borders find_borders(const RowSpace* ws, const Row& q
                 int bin = kBins;
                 u64 above = 0;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
+                for (int i = 0; i < kLaneBins; ++i) {
                     if (bin == kBins && m < t[j] && m + mass[i] >= t[j]) {
-                        bin = lane * kPer + i;
+                        bin = lane * kLaneBins + i;
                         above = m;
                     }
                     m += mass[i];
                 }
                 const int src = __ffsll((unsigned long long)__ballot(bin != kBins)) - 1;
-                bins[j] = __shfl(bin, src);
-                aboves[j] = __shfl(above, src);
+                bins[j] = __builtin_amdgcn_readlane(bin, src);
+                aboves[j] = lane_u64(above, src);
             }
             b.p0 = bins[0];
             b.p1 = bins[1];
             b.pmass = aboves[0];
         }
         b.sure = q.p < 1.0 ? b.p0 : b.kbin;
-        u64 n = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (border_bin(b, lane * kPer + i)) n += count[i];
-        n = wave_sum_u64(n);
-        b.listed = (uint32_t)n;
         if (lane == 0) out = b;
     }
     __syncthreads();
@@ -402,7 +474,6 @@ __device__ __forceinline__ Borders no_borders() {
     b.p1 = 0;
     b.krank = 0;
     b.kmass = b.pmass = b.total = 0;
-    b.listed = 0;
     return b;
 }
 
@@ -421,7 +492,7 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
     const Row q = make_row(a, r, top, low);
     if (q.known != -2) return;   // workgroup-uniform
     const Borders b = q.k || q.p < 1.0 ? find_borders(ws, q) : no_borders();
-    const bool listing = b.listed > 0 && b.listed <= (uint32_t)kCand;
+    const bool listing = b.kbin < kBins || b.p0 <= b.p1;
     if (threadIdx.x == 0) n_list = 0;
     __syncthreads();
     const T* row = x + r * a.ld;
@@ -431,17 +502,21 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
         const int64_t c0 = (int64_t)s * a.sub;
         const int64_t c1 = c0 + a.sub < a.C ? c0 + a.sub : a.C;
         u64 sum = 0;
-        for (int64_t c = c0 + threadIdx.x; c < c1; c += kChunkThreads) {
-            const float v = Logit<T>::load(row + c);
-            const double w = q.weight(v);
-            const u64 W = q.fixed(w);
-            if (W == 0) continue;
-            const int i = q.bin(v);
-            if (i < b.sure) {
-                if (w >= q.min_p) sum += W;
-            } else if (listing && border_bin(b, i)) {
-                const uint32_t at = atomicAdd(&n_list, 1u);
-                if (at < (uint32_t)kCand) list[at] = pack_key(order_image(v), (uint32_t)c);   // at < b.listed
+        for (int64_t c = c0; c < c1; c += kSubMin) {
+            Share<T> e;
+            e.load(row, c, a.C, a.vec);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const float v = e.v[i];
+                const int bin = q.bin(v);
+                if (bin < b.sure) {
+                    const double w = q.weight(v);
+                    if (w >= q.min_p) sum += q.fixed(w);
+                } else if (listing && border_bin(b, bin) && q.fixed(q.weight(v))) {
+                    const uint32_t at = atomicAdd(&n_list, 1u);
+                    if (at < (uint32_t)kCand)
+                        list[at] = pack_key(order_image(v), (uint32_t)(c + Share<T>::element(i, a.vec)));
+                }
             }
         }
         u64 total;
@@ -450,6 +525,7 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
     }
     if (!listing) return;   // workgroup-uniform
     __syncthreads();
+    // past kCand in one workgroup or in all of them: the pick reads the row
     if (threadIdx.x == 0) base = n_list ? atomicAdd(&ws->ncand, n_list) : 0u;
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < n_list && base + i < (uint32_t)kCand; i += kChunkThreads)
@@ -462,7 +538,7 @@ struct PickShared {
     u64 mass[256];
     uint32_t count[256];
     u64 sum[kMaxSubs];
-    u64 prefix, left, all_or, all_and;
+    u64 prefix, left, some_set, some_clear, found_key;
     uint32_t hits;
     int64_t found;
 };
@@ -489,40 +565,35 @@ __device__ __forceinline__ void each_listed(const PickShared& s, int n, const T*
     }
 }
 
-// The largest key t such that the border elements with keys in [t, hi] that
-// `take` accepts number (BY_MASS: weigh) at least `want`; 0 when all of them
-// together do not.  `want` >= 1.  A descent over the key digits below the
-// bits that all accepted keys share; every thread returns the same key.
+// The largest key t such that the border elements with keys of at least t
+// that `take` accepts number (BY_MASS: weigh) at least `want`; 0 when all of
+// them together do not.  `want` >= 1.  A descent over the key's digits of up
+// to eight bits below the bits that all accepted keys share, until one key is
+// left; every thread returns the same key.
 template <bool BY_MASS, class T, class Take>
 __device__ __forceinline__ u64 select_key(PickShared& s, int n, const T* row, const Row& q, const Borders& b, int C,
                                           u64 want, Take take) {
     __syncthreads();
-    if (threadIdx.x == 0) {
-        s.all_or = 0;
-        s.all_and = ~0ull;
-    }
+    if (threadIdx.x == 0) s.some_set = s.some_clear = 0;
     __syncthreads();
-    u64 o = 0, n_and = ~0ull;
+    u64 set = 0, clear = 0;
     each_listed(s, n, row, q, b, C, [&](u64 key, double, u64) {
         if (take(key)) {
-            o |= key;
-            n_and &= key;
+            set |= key;
+            clear |= ~key;
         }
     });
-#pragma unroll
-    for (int d = kWave / 2; d >= 1; d >>= 1) {
-        o |= __shfl_xor(o, d);
-        n_and &= __shfl_xor(n_and, d);
-    }
-    if (lane_id() == 0 && o) {
-        atomicOr(&s.all_or, o);
-        atomicAnd(&s.all_and, n_and);
+    set = wave_or_u64(set);
+    clear = wave_or_u64(clear);
+    if (lane_id() == kWave - 1 && (set | clear)) {
+        atomicOr(&s.some_set, set);
+        atomicOr(&s.some_clear, clear);
     }
     __syncthreads();
-    if (s.all_or == 0) return 0;   // none accepted
-    const u64 diff = s.all_or ^ s.all_and;
+    if ((s.some_set | s.some_clear) == 0) return 0;   // none accepted
+    const u64 diff = s.some_set & s.some_clear;
     int shift = diff ? 64 - __clzll((long long)diff) : 0;   // bits shift.. are shared
-    u64 prefix = shift < 64 ? s.all_and >> shift << shift : 0;
+    u64 prefix = shift < 64 ? s.some_set >> shift << shift : 0;
     while (shift > 0) {
         const int bits = shift < 8 ? shift : 8;
         const int next = shift - bits;
@@ -530,14 +601,14 @@ __device__ __forceinline__ u64 select_key(PickShared& s, int n, const T* row, co
         __syncthreads();
         if (threadIdx.x < 256) {
             if (BY_MASS) s.mass[threadIdx.x] = 0;
-            else s.count[threadIdx.x] = 0;
+            s.count[threadIdx.x] = 0;
         }
         __syncthreads();
         each_listed(s, n, row, q, b, C, [&](u64 key, double, u64 W) {
             if (take(key) && (key & mask) == prefix) {
                 const int d = (int)((key >> next) & 255u) & ((1 << bits) - 1);
                 if (BY_MASS) atomicAdd(&s.mass[d], W);
-                else atomicAdd(&s.count[d], 1u);
+                atomicAdd(&s.count[d], 1u);
             }
         });
         __syncthreads();
@@ -566,20 +637,29 @@ __device__ __forceinline__ u64 select_key(PickShared& s, int n, const T* row, co
                 if (lane == 0) s.hits = 0;
             } else {
                 const int src = __ffsll((unsigned long long)hit) - 1;
-                const int dg = __shfl(digit, src);
-                const u64 ab = __shfl(above, src);
+                const int dg = __builtin_amdgcn_readlane(digit, src);
+                const u64 ab = lane_u64(above, src);
                 if (lane == 0) {
-                    s.hits = 1;
+                    s.hits = s.count[dg];
                     s.prefix = prefix | ((u64)dg << next);
                     s.left = want - ab;
                 }
             }
         }
         __syncthreads();
-        if (!s.hits) return 0;   // fewer than wanted (only at the first digit)
+        const uint32_t hits = s.hits;
+        if (hits == 0) return 0;   // fewer than wanted (only at the first digit)
         prefix = s.prefix;
         want = s.left;
         shift = next;
+        if (hits == 1 && shift > 0) {   // one key has this prefix: the rest of its bits
+            const u64 found = ~0ull << shift;
+            each_listed(s, n, row, q, b, C, [&](u64 key, double, u64) {
+                if (take(key) && (key & found) == prefix) s.found_key = key;
+            });
+            __syncthreads();
+            return s.found_key;
+        }
     }
     return prefix;
 }
@@ -704,8 +784,9 @@ k_sample_pick(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
         return;
     }
     const Borders b = q.k || q.p < 1.0 ? find_borders(ws, q) : no_borders();
-    const bool from_row = b.listed > (uint32_t)kCand;
-    const int n = from_row ? 0 : (int)min(ws->ncand, (uint32_t)kCand);   // b.listed of them
+    const uint32_t listed = ws->ncand;
+    const bool from_row = listed > (uint32_t)kCand;
+    const int n = from_row ? 0 : (int)listed;
     for (int i = threadIdx.x; i < n; i += kPickThreads) s.key[i] = ws->cand[i];
     if ((int)threadIdx.x < a.nsub) s.sum[threadIdx.x] = ws->sum[threadIdx.x];
     if (threadIdx.x == 0) s.found = 0;
@@ -754,9 +835,20 @@ k_sample_row(const T* __restrict__ x, SampleArgs a) {
 }
 
 // ---- host ---------------------------------------------------------------------
-SampleArgs plan_rows(int64_t R, int64_t C) {
+// The arguments for rows r0 .. r0 + R - 1.
+SampleArgs plan_rows(const SampleRows& p, int64_t r0, int64_t R) {
+    const int64_t C = p.C;
     SampleArgs a{};
+    a.u = p.u + r0;
+    a.temperature = p.temperature ? p.temperature + r0 : nullptr;
+    a.top_k = p.top_k ? p.top_k + r0 : nullptr;
+    a.top_p = p.top_p ? p.top_p + r0 : nullptr;
+    a.min_p = p.min_p ? p.min_p + r0 : nullptr;
+    a.idx = p.idx + r0;
+    a.ld = p.ld;
     a.C = (int)C;
+    const int size = p.dtype == DG_DTYPE_F32 ? 4 : 2;
+    a.vec = (uintptr_t)p.x % 16 == 0 && p.ld * size % 16 == 0;
     int bits = 0;
     while (((int64_t)1 << bits) < C) ++bits;
     a.F = 62 - bits < 51 ? 62 - bits : 51;
@@ -775,24 +867,13 @@ template <class T>
 hipError_t launch_sample(const SampleRows& p, hipStream_t s) {
     const T* x = (const T*)p.x;
     if (p.C <= kCand) {
-        SampleArgs a = plan_rows(p.R, p.C);
-        a.ld = p.ld;
-        a.u = p.u; a.temperature = p.temperature; a.top_k = p.top_k; a.top_p = p.top_p; a.min_p = p.min_p;
-        a.idx = p.idx;
-        hipLaunchKernelGGL((k_sample_row<T>), dim3((unsigned)p.R), dim3(kPickThreads), 0, s, x, a);
+        hipLaunchKernelGGL((k_sample_row<T>), dim3((unsigned)p.R), dim3(kPickThreads), 0, s, x, plan_rows(p, 0, p.R));
         return hipGetLastError();
     }
     RowSpace* ws = (RowSpace*)p.ws;
     for (int64_t r0 = 0; r0 < p.R; r0 += kBatchRows) {
         const int64_t rn = p.R - r0 < kBatchRows ? p.R - r0 : kBatchRows;
-        SampleArgs a = plan_rows(rn, p.C);
-        a.ld = p.ld;
-        a.u = p.u + r0;
-        a.temperature = p.temperature ? p.temperature + r0 : nullptr;
-        a.top_k = p.top_k ? p.top_k + r0 : nullptr;
-        a.top_p = p.top_p ? p.top_p + r0 : nullptr;
-        a.min_p = p.min_p ? p.min_p + r0 : nullptr;
-        a.idx = p.idx + r0;
+        const SampleArgs a = plan_rows(p, r0, rn);
         const T* xr = x + r0 * p.ld;
         const dim3 chunks((unsigned)a.G, (unsigned)rn);
         hipLaunchKernelGGL((k_sample_max<T>), chunks, dim3(kChunkThreads), 0, s, xr, ws, a);

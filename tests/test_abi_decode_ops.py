@@ -62,16 +62,29 @@ def test_rmsnorm_rejects_before_launch(lib, args, expect):
     assert lib.dg_rmsnorm(*args, None) == expect
 
 
-def test_binding_refuses_host_tensors():
+def test_binding_checks_operands():
+    """Host tensors, other types, strided tensors and ones smaller than the call touches are refused."""
     import torch
     import memory_bound_decode_gemv_amd as dg
     t = torch.zeros(4, 64)
-    if torch.cuda.is_available():
+    for call in (lambda: dg.dg_rmsnorm(t, t[0], t), lambda: dg.dg_rmsnorm_q8_1(t, t[0], t),
+                 lambda: dg.dg_sample_rows(t, t[0], t), lambda: dg.dg_gemv_q4_0_glu(t, t, t, t, 4, 256, 1)):
         with pytest.raises(ValueError, match="device tensor"):
-            dg._need_here(x=t)
+            call()
     with pytest.raises(TypeError):
         dg._dtype_id(torch.zeros(4, dtype=torch.int32), "x")
     assert [dg._dtype_id(torch.zeros(1, dtype=d), "x") for d in (torch.float32, torch.float16, torch.bfloat16)] == [0, 1, 2]
+    host = t.get_device()   # -1: the checks of one operand, without a device
+    assert dg._arg("x", t, host, torch.float32, 4 * 64 * 4) == t.data_ptr()
+    assert dg._arg("x", None, host, torch.float32, 1000) is None
+    with pytest.raises(ValueError, match="holds 1024 bytes but the call touches 1025"):
+        dg._arg("x", t, host, torch.float32, 1025)
+    with pytest.raises(TypeError, match="float32, expected torch.float16"):
+        dg._arg("x", t, host, torch.float16, 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        dg._arg("x", t[:, :5], host, torch.float32, 0)
+    with pytest.raises(ValueError, match="host tensor"):
+        dg._arg("x", t, 0, torch.float32, 0)
 
 
 @pytest.mark.parametrize("args,expect", [
