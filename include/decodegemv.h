@@ -327,13 +327,10 @@ dg_status dg_gemv_q8_0_tiles(const void* Wt, const void* Xq, float* Y, int64_t N
  *           tiled calls) as Wt of dg_gemv_q4_0_tiles / dg_gemv_q8_0_tiles;
  *           16-byte aligned.  They may be the same matrix.
  *   Xq, Y, N, K, M  as for dg_gemv_q4_0.  K = 0 gives Y = 0.
- *   ws      (tiled calls) device workspace of at least
- *           dg_gemv_*_tiles_glu_workspace_bytes(N, K, M) bytes (0: ws may be
- *           NULL), with the rules of dg_gemv_q4_0_tiles: zero-filled once when
- *           allocated, left zero where it matters by every call; the same
- *           workspace serves both kinds of call in turn.
+ * No workspace: the tiled calls take columns that do not fit a workgroup's LDS
+ * at once in passes over K.
  * Errors: DG_ERR_ARG (act), DG_ERR_SHAPE, DG_ERR_NULL, DG_ERR_MISALIGNED,
- * DG_ERR_WORKSPACE, DG_ERR_HIP.
+ * DG_ERR_HIP.
  * ------------------------------------------------------------------------ */
 enum { DG_ACT_SILU = 0, DG_ACT_GELU = 1, DG_ACT_GELU_TANH = 2, DG_ACT_RELU = 3 };
 
@@ -341,12 +338,10 @@ dg_status dg_gemv_q4_0_glu(const void* Wg, const void* Wu, const void* Xq, float
                            int act, dg_stream stream);
 dg_status dg_gemv_q8_0_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
                            int act, dg_stream stream);
-size_t dg_gemv_q4_0_tiles_glu_workspace_bytes(int64_t N, int64_t K, int M);
-size_t dg_gemv_q8_0_tiles_glu_workspace_bytes(int64_t N, int64_t K, int M);
 dg_status dg_gemv_q4_0_tiles_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
-                                 int act, void* ws, size_t ws_bytes, dg_stream stream);
+                                 int act, dg_stream stream);
 dg_status dg_gemv_q8_0_tiles_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
-                                 int act, void* ws, size_t ws_bytes, dg_stream stream);
+                                 int act, dg_stream stream);
 
 /* ------------------------------------------------------------------------
  * NF4 weights (4-bit codes into a 16-entry float table, per-block absmax)

@@ -85,7 +85,6 @@ EXPORTED = (
     "dg_rmsnorm_q8_1", "dg_rmsnorm",
     "dg_sample_workspace_bytes", "dg_sample_rows",
     "dg_gemv_q4_0_glu", "dg_gemv_q8_0_glu",
-    "dg_gemv_q4_0_tiles_glu_workspace_bytes", "dg_gemv_q8_0_tiles_glu_workspace_bytes",
     "dg_gemv_q4_0_tiles_glu", "dg_gemv_q8_0_tiles_glu",
 )
 
@@ -208,9 +207,7 @@ def _lib():
     for f in ("q4_0", "q8_0"):
         getattr(lib, f"dg_gemv_{f}_glu").argtypes = [P, P, P, P, I64, I64, I32, I32, P]
         getattr(lib, f"dg_gemv_{f}_glu").restype = st
-        getattr(lib, f"dg_gemv_{f}_tiles_glu_workspace_bytes").argtypes = [I64, I64, I32]
-        getattr(lib, f"dg_gemv_{f}_tiles_glu_workspace_bytes").restype = ctypes.c_size_t
-        getattr(lib, f"dg_gemv_{f}_tiles_glu").argtypes = [P, P, P, P, I64, I64, I32, I32, P, ctypes.c_size_t, P]
+        getattr(lib, f"dg_gemv_{f}_tiles_glu").argtypes = [P, P, P, P, I64, I64, I32, I32, P]
         getattr(lib, f"dg_gemv_{f}_tiles_glu").restype = st
     _handle = lib
     return lib
@@ -528,7 +525,7 @@ def dg_gemv_q8_0(Wq, Xq, Y, N, K, M, launch=None, stream=None):
 _ACTS = {"silu": DG_ACT_SILU, "gelu": DG_ACT_GELU, "gelu_tanh": DG_ACT_GELU_TANH, "relu": DG_ACT_RELU}
 
 
-def _gemv_glu(fmt, tiles, Wg, Wu, Xq, Y, N, K, M, act, ws, stream):
+def _gemv_glu(fmt, tiles, Wg, Wu, Xq, Y, N, K, M, act, stream):
     torch = _torch()
     dev = _here(Y, "Y")
     if act not in _ACTS:
@@ -539,11 +536,7 @@ def _gemv_glu(fmt, tiles, Wg, Wu, Xq, Y, N, K, M, act, ws, stream):
     args = (_arg("Wg", Wg, dev, torch.uint8, weights), _arg("Wu", Wu, dev, torch.uint8, weights),
             _arg("Xq", Xq, dev, torch.uint8, M * blocks * 36),
             _arg("Y", Y, dev, torch.float32, M * N * 4 if N > 0 and M > 0 else 0), N, K, M, _ACTS[act])
-    if tiles:
-        name = f"dg_gemv_{fmt}_tiles_glu"
-        args += (_arg("ws", ws, dev, torch.uint8, 0), ws.nbytes if ws is not None else 0)
-    else:
-        name = f"dg_gemv_{fmt}_glu"
+    name = f"dg_gemv_{fmt}{'_tiles' if tiles else ''}_glu"
     _check(getattr(_lib(), name)(*args, _stream_here(stream, dev)), name)
     return Y
 
@@ -551,31 +544,22 @@ def _gemv_glu(fmt, tiles, Wg, Wu, Xq, Y, N, K, M, act, ws, stream):
 def dg_gemv_q4_0_glu(Wg, Wu, Xq, Y, N, K, M, act="silu", stream=None):
     """Y[M][N] (float32) = act(Wg X) * (Wu X) from two matrices of Q4_0 bytes and
     Q8_1 activation bytes (uint8 tensors); act: "silu", "gelu", "gelu_tanh" or "relu"."""
-    return _gemv_glu("q4_0", False, Wg, Wu, Xq, Y, N, K, M, act, None, stream)
+    return _gemv_glu("q4_0", False, Wg, Wu, Xq, Y, N, K, M, act, stream)
 
 
 def dg_gemv_q8_0_glu(Wg, Wu, Xq, Y, N, K, M, act="silu", stream=None):
     """As dg_gemv_q4_0_glu, from Q8_0 bytes."""
-    return _gemv_glu("q8_0", False, Wg, Wu, Xq, Y, N, K, M, act, None, stream)
+    return _gemv_glu("q8_0", False, Wg, Wu, Xq, Y, N, K, M, act, stream)
 
 
-def dg_gemv_q4_0_tiles_glu_workspace_bytes(N, K, M):
-    return int(_lib().dg_gemv_q4_0_tiles_glu_workspace_bytes(int(N), int(K), int(M)))
+def dg_gemv_q4_0_tiles_glu(Wg, Wu, Xq, Y, N, K, M, act="silu", stream=None):
+    """As dg_gemv_q4_0_glu, from the tiled copies."""
+    return _gemv_glu("q4_0", True, Wg, Wu, Xq, Y, N, K, M, act, stream)
 
 
-def dg_gemv_q8_0_tiles_glu_workspace_bytes(N, K, M):
-    return int(_lib().dg_gemv_q8_0_tiles_glu_workspace_bytes(int(N), int(K), int(M)))
-
-
-def dg_gemv_q4_0_tiles_glu(Wg, Wu, Xq, Y, N, K, M, act="silu", ws=None, stream=None):
-    """As dg_gemv_q4_0_glu, from the tiled copies (workspace as for dg_gemv_q4_0_tiles, of
-    dg_gemv_q4_0_tiles_glu_workspace_bytes(N, K, M) bytes)."""
-    return _gemv_glu("q4_0", True, Wg, Wu, Xq, Y, N, K, M, act, ws, stream)
-
-
-def dg_gemv_q8_0_tiles_glu(Wg, Wu, Xq, Y, N, K, M, act="silu", ws=None, stream=None):
-    """As dg_gemv_q4_0_tiles_glu, from the tiled Q8_0 copies."""
-    return _gemv_glu("q8_0", True, Wg, Wu, Xq, Y, N, K, M, act, ws, stream)
+def dg_gemv_q8_0_tiles_glu(Wg, Wu, Xq, Y, N, K, M, act="silu", stream=None):
+    """As dg_gemv_q8_0_glu, from the tiled copies."""
+    return _gemv_glu("q8_0", True, Wg, Wu, Xq, Y, N, K, M, act, stream)
 
 
 def dg_gemv_nf4(codes, absmax, table, x, y, N=None, K=None, B=64, launch=None, stream=None):

@@ -115,16 +115,15 @@ size_t tiles_workspace_checked(bool q8, int64_t N, int64_t K, int M) {
 
 bool act_ok(int act) { return act >= DG_ACT_SILU && act <= DG_ACT_RELU; }
 
-// tiles: the tiled copies, with a workspace (ws, ws_bytes).
+// tiles: the tiled copies.
 dg_status gemv_glu_checked(bool q8, bool tiles, const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N,
-                           int64_t K, int M, int act, void* ws, size_t ws_bytes, dg_stream stream) {
+                           int64_t K, int M, int act, dg_stream stream) {
     if (!act_ok(act)) return DG_ERR_ARG;
     if (N < 0 || N > kI32Max || K < 0 || K > kQuantMaxK || K % 256 != 0 || M < 0 || M > 24) return DG_ERR_SHAPE;
     if (N == 0 || M == 0) return DG_OK;
     if (!Y || (K > 0 && (!Wg || !Wu || !Xq))) return DG_ERR_NULL;
     if (!aligned(Y, 4)) return DG_ERR_MISALIGNED;
-    if (K > 0 && (!aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(Xq, 16) || !aligned(ws, 16)))
-        return DG_ERR_MISALIGNED;
+    if (K > 0 && (!aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(Xq, 16))) return DG_ERR_MISALIGNED;
     if (K == 0) {   // empty sums: act(0) * 0 = 0
         const int64_t n = N * (int64_t)M;
         hipLaunchKernelGGL(k_fill_zero_f32, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, (hipStream_t)stream, Y,
@@ -132,17 +131,8 @@ dg_status gemv_glu_checked(bool q8, bool tiles, const void* Wg, const void* Wu, 
         return hip_status(hipGetLastError());
     }
     const GluMatrices w = {Wg, Wu, act};
-    if (!tiles) return hip_status(launch_gemv_glu(q8, w, Xq, Y, (int)N, (int)K, M, (hipStream_t)stream));
-    size_t need = 0;
-    if (!tiles_glu_config(q8, (int)N, (int)K, M, &need)) return DG_ERR_SHAPE;
-    if (need > 0 && (!ws || ws_bytes < need)) return DG_ERR_WORKSPACE;
-    return hip_status(launch_tiles_glu(q8, M, w, Xq, Y, ws, (int)N, (int)K, (hipStream_t)stream));
-}
-
-size_t tiles_glu_workspace_checked(bool q8, int64_t N, int64_t K, int M) {
-    size_t need = 0;
-    if (N <= 0 || N > kI32Max || K <= 0 || K > kQuantMaxK || K % 256 != 0 || M <= 0 || M > 24) return 0;
-    return tiles_glu_config(q8, (int)N, (int)K, M, &need) ? need : 0;
+    return hip_status(tiles ? launch_tiles_glu(q8, M, w, Xq, Y, (int)N, (int)K, (hipStream_t)stream)
+                            : launch_gemv_glu(q8, w, Xq, Y, (int)N, (int)K, M, (hipStream_t)stream));
 }
 
 bool nf4_block_ok(int B) { return B == 32 || B == 64 || B == 128 || B == 256; }
@@ -500,29 +490,22 @@ dg_status dg_sample_rows(const void* x, int dtype, const float* u, const float* 
 
 dg_status dg_gemv_q4_0_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
                            int act, dg_stream stream) {
-    return gemv_glu_checked(false, false, Wg, Wu, Xq, Y, N, K, M, act, nullptr, 0, stream);
+    return gemv_glu_checked(false, false, Wg, Wu, Xq, Y, N, K, M, act, stream);
+}
+
+dg_status dg_gemv_q4_0_tiles_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
+                                 int act, dg_stream stream) {
+    return gemv_glu_checked(false, true, Wg, Wu, Xq, Y, N, K, M, act, stream);
 }
 
 dg_status dg_gemv_q8_0_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
                            int act, dg_stream stream) {
-    return gemv_glu_checked(true, false, Wg, Wu, Xq, Y, N, K, M, act, nullptr, 0, stream);
-}
-
-size_t dg_gemv_q4_0_tiles_glu_workspace_bytes(int64_t N, int64_t K, int M) {
-    return tiles_glu_workspace_checked(false, N, K, M);
-}
-size_t dg_gemv_q8_0_tiles_glu_workspace_bytes(int64_t N, int64_t K, int M) {
-    return tiles_glu_workspace_checked(true, N, K, M);
-}
-
-dg_status dg_gemv_q4_0_tiles_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
-                                 int act, void* ws, size_t ws_bytes, dg_stream stream) {
-    return gemv_glu_checked(false, true, Wg, Wu, Xq, Y, N, K, M, act, ws, ws_bytes, stream);
+    return gemv_glu_checked(true, false, Wg, Wu, Xq, Y, N, K, M, act, stream);
 }
 
 dg_status dg_gemv_q8_0_tiles_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
-                                 int act, void* ws, size_t ws_bytes, dg_stream stream) {
-    return gemv_glu_checked(true, true, Wg, Wu, Xq, Y, N, K, M, act, ws, ws_bytes, stream);
+                                 int act, dg_stream stream) {
+    return gemv_glu_checked(true, true, Wg, Wu, Xq, Y, N, K, M, act, stream);
 }
 
 }  // extern "C"

@@ -123,9 +123,8 @@ hipError_t launch_units_glu(bool q8, int K, int M, int depth, const GluMatrices&
                             int grid, int block, hipStream_t s);
 hipError_t launch_mfma_glu(bool q8, int M, const GluMatrices& w, const void* Xq, float* Y, int N, int K,
                            hipStream_t s);
-// In 16-row tiles; tiles_glu_config gives the workspace bytes that a call needs.
-bool tiles_glu_config(bool q8, int N, int K, int M, size_t* ws_bytes);
-hipError_t launch_tiles_glu(bool q8, int M, const GluMatrices& w, const void* Xq, float* Y, void* ws, int N, int K,
+// In 16-row tiles.
+hipError_t launch_tiles_glu(bool q8, int M, const GluMatrices& w, const void* Xq, float* Y, int N, int K,
                             hipStream_t s);
 
 hipError_t launch_quantize_q8_0(const float* w, void* Wq, int64_t N, int64_t K, hipStream_t s);

@@ -351,11 +351,12 @@ struct TileOut {
 // ---------------------------------------------------------------------------
 // The GEMV.  MP = 8 (M <= 8: one pair tile), 16 (one full tile) or 24 (a
 // full tile and a pair tile); columns past M re-read column M - 1, their
-// results dropped.
+// results dropped.  A gated product is one range of K per row group (KP = 1,
+// no workspace), in passes.
 // ---------------------------------------------------------------------------
 template <class TF, int MP, int RT, int KW, int D, bool GLU>
-__global__ void __launch_bounds__(64 * RT * KW)
-k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* __restrict__ Y,
+__device__ __forceinline__ void
+tiles_body(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* __restrict__ Y,
            uint32_t* __restrict__ tickets, f32x4* __restrict__ part, int N, int K, int M, int KP, int spw,
            int cs_slots, uint32_t cs_magic, int CS, int groups, int pre, GluArgs<GLU> glu_args) {
     static_assert(!GLU || RT % 2 == 0, "gate and up tiles in pairs");
@@ -363,7 +364,6 @@ k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* _
     constexpr int NA = TS::kNA;
     constexpr int W = RT * KW;
     extern __shared__ u32x4 tiles_lds[];
-    __shared__ int last_ticket;
     uint8_t* const lds = reinterpret_cast<uint8_t*>(tiles_lds);
     const int lane = lane_id();
     const int wave = wave_in_block();
@@ -396,18 +396,32 @@ k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* _
     }
     const int s0 = kp * spw;                       // first group of the workgroup's range
     const int ns = min(spw, S - s0);               // groups in the range (>= 1)
-    const int spk = (ns + KW - 1) / KW;
-    const int w0 = kw * spk;                       // the wave's part: groups w0 .. w0 + cnt - 1 of the range
-    const int cnt = max(0, min(spk, ns - w0));     // wave-uniform
     const int t = GLU ? grp * (RT / 2) + (rt >> 1) : grp * RT + rt;
     const int tc = t < T ? t : T - 1;
     const bool up = GLU && (rt & 1);   // wave-uniform
     if constexpr (GLU) Wt = up ? glu_args.Wu : Wt;
     constexpr int kGroupBytes = TF::kGroupBytes;
     constexpr int L = TF::kCodeLoads + 1;   // 16-byte loads per lane and group
-    const uint8_t* const wbase = Wt + ((size_t)tc * S + s0 + (cnt > 0 ? w0 : 0)) * kGroupBytes;
-    const int last = cnt > 0 ? cnt - 1 : 0;
 
+    f32x4 acc[NA];
+#pragma unroll
+    for (int a = 0; a < NA; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // The range in one pass, or (GLU) in passes of glu_args.spp groups whose
+    // columns take the same LDS in turn.
+    int p0 = 0;   // the pass's first group within the range
+    do {
+    int np = ns;  // its groups
+    if constexpr (GLU) {
+        np = min(glu_args.spp, ns - p0);
+        if (p0 > 0) lds_barrier();   // every wave is done with the columns of the pass before
+    }
+    const int sp = s0 + p0;
+    const int spk = (np + KW - 1) / KW;
+    const int w0 = kw * spk;                       // the wave's part: groups w0 .. w0 + cnt - 1 of the pass
+    const int cnt = max(0, min(spk, np - w0));     // wave-uniform
+    const uint8_t* const wbase = Wt + ((size_t)tc * S + sp + (cnt > 0 ? w0 : 0)) * kGroupBytes;
+    const int last = cnt > 0 ? cnt - 1 : 0;
     // (1) the activation columns of the range, copied into LDS by DMA, and a
     // wait for them; then (2) the first D groups of this wave's weights (past
     // its part: its last group again, never used).  The wait is the builtin
@@ -421,9 +435,9 @@ k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* _
     // weights issued before the wait (pre = 0, kept for measurements) they
     // start when all D have.  Measured 2-16% faster on most shapes.
     {
-        const int used = ns * kGroupSlots;
+        const int used = np * kGroupSlots;
         const int copies = (M * cs_slots + kWave - 1) / kWave;
-        const uint8_t* const xr = Xq + (size_t)s0 * kGroupBlocks * kQ81Bytes;
+        const uint8_t* const xr = Xq + (size_t)sp * kGroupBlocks * kQ81Bytes;
         for (int j = wave; j < copies; j += W) {
             const uint32_t q = (uint32_t)(j * kWave + lane);
             const uint32_t m = __umulhi(q, cs_magic);          // q / cs_slots
@@ -466,10 +480,6 @@ k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* _
         al.ps = pc + (hi ? (uint32_t)kQ81Bytes : 0u);
         al.sel = hi ? 0x01000C0Cu : 0x0C0C0100u;
     }
-    f32x4 acc[NA];
-#pragma unroll
-    for (int a = 0; a < NA; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
     // D groups per round; the loads of the next round are issued right after
     // each group's products, with no branch between them, so the compiler's
     // waits count exactly the D - 1 groups still in flight.  The last round
@@ -499,6 +509,8 @@ k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* _
                 tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(w0 + i) * kGroupBlocks, g, acc);
         }
     }
+    if constexpr (GLU) p0 += glu_args.spp;
+    } while (GLU && p0 < ns);
 
     // the KW parts of each tile, added in the order 0..KW-1
     if constexpr (KW > 1) {
@@ -519,69 +531,6 @@ k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* _
                 }
         }
     }
-    if constexpr (!GLU) {
-        if (KP == 1) {
-            if (kw == 0 && t < T) TileOut<TF, MP>(acc).store(Y, N, M, t, g, rn);
-            return;
-        }
-    }
-
-    // KP ranges: partial tile sums to the workspace, then a ticket.  Every
-    // access to the workspace is an agent-scope atomic (device-coherent loads
-    // and stores, sc1 on gfx950), and each wave waits for its stores to
-    // complete before the workgroup takes its ticket; the workgroup that draws
-    // the last ticket issues its loads only after the ticket has returned.
-    // Agent-scope release and acquire fences (an L2 write-back and an L2
-    // invalidate on this chip, both of whole caches) measured 15-140 us per
-    // call, and are not needed when every shared access is atomic.
-    const int slot = grp * CS + cs;   // this slice's ticket counter and partial sums
-    if (!GLU || KP > 1) {
-        float* const mine = reinterpret_cast<float*>(part + (((size_t)slot * KP + kp) * RT + rt) * NA * kWave);
-        if (kw == 0) {
-#pragma unroll
-            for (int a = 0; a < NA; ++a)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    __hip_atomic_store(mine + (a * kWave + lane) * 4 + r, acc[a][r], __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-        }
-        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's partial sums are stored
-        __syncthreads();
-        if (threadIdx.x == 0)
-            last_ticket = __hip_atomic_fetch_add(tickets + slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                          (uint32_t)(KP - 1);
-        __syncthreads();
-        if (!last_ticket) return;   // workgroup-uniform
-        if (kw == 0 && t < T) {
-            f32x4 sum[NA];
-            for (int k2 = 0; k2 < KP; ++k2) {
-                const float* const src =
-                    reinterpret_cast<const float*>(part + (((size_t)slot * KP + k2) * RT + rt) * NA * kWave);
-#pragma unroll
-                for (int a = 0; a < NA; ++a) {
-                    f32x4 v = acc[a];
-                    if (k2 != kp) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            v[r] = __hip_atomic_load(src + (a * kWave + lane) * 4 + r, __ATOMIC_RELAXED,
-                                                     __HIP_MEMORY_SCOPE_AGENT);
-                    }
-                    if (k2 == 0) sum[a] = v;
-                    else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) sum[a][r] += v[r];
-                    }
-                }
-            }
-            if constexpr (GLU) {
-#pragma unroll
-                for (int a = 0; a < NA; ++a) acc[a] = sum[a];
-            } else {
-                TileOut<TF, MP>(sum).store(Y, N, M, t, g, rn);
-            }
-        }
-        if (threadIdx.x == 0) __hip_atomic_store(tickets + slot, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
     if constexpr (GLU) {   // the up sums to the gate's wave, which stores the tile's outputs
         f32x4* red = reinterpret_cast<f32x4*>(lds);   // a slot per wave; only a pair's waves use those of kw = 0
         if constexpr (KW == 1) lds_barrier();         // every wave is done with the activation copies
@@ -598,7 +547,80 @@ k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* _
             out.gate(glu_args.act, TileOut<TF, MP>(us));
             out.store(Y, N, M, t, g, rn);
         }
+        return;
     }
+    if (KP == 1) {
+        if (kw == 0 && t < T) TileOut<TF, MP>(acc).store(Y, N, M, t, g, rn);
+        return;
+    }
+
+    // KP ranges: partial tile sums to the workspace, then a ticket.  Every
+    // access to the workspace is an agent-scope atomic (device-coherent loads
+    // and stores, sc1 on gfx950), and each wave waits for its stores to
+    // complete before the workgroup takes its ticket; the workgroup that draws
+    // the last ticket issues its loads only after the ticket has returned.
+    // Agent-scope release and acquire fences (an L2 write-back and an L2
+    // invalidate on this chip, both of whole caches) measured 15-140 us per
+    // call, and are not needed when every shared access is atomic.
+    __shared__ int last_ticket;
+    const int slot = grp * CS + cs;   // this slice's ticket counter and partial sums
+    float* const mine = reinterpret_cast<float*>(part + (((size_t)slot * KP + kp) * RT + rt) * NA * kWave);
+    if (kw == 0) {
+#pragma unroll
+        for (int a = 0; a < NA; ++a)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                __hip_atomic_store(mine + (a * kWave + lane) * 4 + r, acc[a][r], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's partial sums are stored
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last_ticket = __hip_atomic_fetch_add(tickets + slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                      (uint32_t)(KP - 1);
+    __syncthreads();
+    if (!last_ticket) return;   // workgroup-uniform
+    if (kw == 0 && t < T) {
+        f32x4 sum[NA];
+        for (int k2 = 0; k2 < KP; ++k2) {
+            const float* const src =
+                reinterpret_cast<const float*>(part + (((size_t)slot * KP + k2) * RT + rt) * NA * kWave);
+#pragma unroll
+            for (int a = 0; a < NA; ++a) {
+                f32x4 v = acc[a];
+                if (k2 != kp) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[r] = __hip_atomic_load(src + (a * kWave + lane) * 4 + r, __ATOMIC_RELAXED,
+                                                 __HIP_MEMORY_SCOPE_AGENT);
+                }
+                if (k2 == 0) sum[a] = v;
+                else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sum[a][r] += v[r];
+                }
+            }
+        }
+        TileOut<TF, MP>(sum).store(Y, N, M, t, g, rn);
+    }
+    if (threadIdx.x == 0) __hip_atomic_store(tickets + slot, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <class TF, int MP, int RT, int KW, int D>
+__global__ void __launch_bounds__(64 * RT * KW)
+k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* __restrict__ Y,
+           uint32_t* __restrict__ tickets, f32x4* __restrict__ part, int N, int K, int M, int KP, int spw,
+           int cs_slots, uint32_t cs_magic, int CS, int groups, int pre) {
+    tiles_body<TF, MP, RT, KW, D, false>(Wt, Xq, Y, tickets, part, N, K, M, KP, spw, cs_slots, cs_magic, CS, groups,
+                                         pre, {});
+}
+
+template <class TF, int MP, int RT, int KW, int D>
+__global__ void __launch_bounds__(64 * RT * KW)
+k_glu_tiles(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ Xq, float* __restrict__ Y, int N, int K, int M,
+            int cs_slots, uint32_t cs_magic, int CS, int groups, GluArgs<true> glu_args) {
+    tiles_body<TF, MP, RT, KW, D, true>(Wg, Xq, Y, nullptr, nullptr, N, K, M, 1, K >> 8, cs_slots, cs_magic, CS,
+                                        groups, 1, glu_args);
 }
 
 // f32x4 accumulators per lane for M columns (TileSet<MP>::kNA).
@@ -635,8 +657,7 @@ bool tiles_built(int RT, int KW, int D) {
     return false;
 }
 
-// T: row tiles (of both matrices, for a gated product).
-bool tiles_plan(int T, int K, int M, int RT, int KW, int D, int KP, int CS, TilesPlan& p) {
+bool tiles_plan(int N, int K, int M, int RT, int KW, int D, int KP, int CS, TilesPlan& p) {
     const int S = K >> 8;
     if (S < 1 || KP < 1 || KP > kTilesMaxKP || !tiles_built(RT, KW, D)) return false;
     if (CS < 1 || CS > kTilesMaxCS) return false;
@@ -655,7 +676,7 @@ bool tiles_plan(int T, int K, int M, int RT, int KW, int D, int KP, int CS, Tile
     const size_t act = (size_t)((M * p.cs_slots + kWave - 1) / kWave) * 1024 + (pair ? (size_t)p.cs_slots * 16 : 0);
     const size_t red = (size_t)RT * KW * NA * kWave * 16;
     p.lds = act > red ? act : red;
-    p.groups = (T + RT - 1) / RT;
+    p.groups = ((N + 15) / 16 + RT - 1) / RT;
     if (p.KP > 1 && p.groups * CS > kTicketSlots) return false;   // one ticket counter per row group and slice
     // LDS of one workgroup; the quotient by the column stride (a multiply-high
     // by ceil(2^32 / stride)) is exact for strides below 2^14 and slots below 2^18
@@ -697,7 +718,7 @@ void tiles_default(bool q8, int N, int K, int M, int& RT, int& KW, int& D, int& 
     TilesPlan p;
     CS = 0;
     for (int c : cand)
-        if (c > 0 && tiles_plan(T, K, M, 1, 4, 2, 1, c, p)) {
+        if (c > 0 && tiles_plan(N, K, M, 1, 4, 2, 1, c, p)) {
             CS = c;
             break;
         }
@@ -728,22 +749,20 @@ void tiles_default(bool q8, int N, int K, int M, int& RT, int& KW, int& D, int& 
     const int Mh = (M + CS - 1) / CS;
     const size_t fit = 150 * 1024;   // the columns of one range in LDS
     while (KP < kTilesMaxKP && KP < S && (size_t)Mh * ((S + KP - 1) / KP) * kGroupSlots * 16 > fit) KP *= 2;
-    // few columns: the pair tile's zero column takes LDS as well
-    while (KP < kTilesMaxKP && KP < S && !tiles_plan(T, K, M, 4, 2, 2, KP, CS, p)) KP *= 2;
     RT = KP * CS >= 4 ? 4 : 2;
     KW = KP * CS >= 4 ? 2 : 4;
 }
 
-template <class TF, int MP, int RT, int KW, int D, bool GLU = false>
+template <class TF, int MP, int RT, int KW, int D>
 hipError_t launch_tiles_cfg(const TilesPlan& p, const void* Wt, const void* Xq, float* Y, void* ws, int N, int K,
-                            int M, hipStream_t s, GluArgs<GLU> ga = {}) {
+                            int M, hipStream_t s) {
     uint32_t* tickets = reinterpret_cast<uint32_t*>(ws);
     f32x4* part = reinterpret_cast<f32x4*>(reinterpret_cast<uint8_t*>(ws) + kTicketBytes);
     const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) + (uint64_t)p.cs_slots - 1) / (uint64_t)p.cs_slots);
     const int grid = p.CS == 1 ? p.groups * p.KP : (p.groups * p.KP + 7) / 8 * 8 * p.CS;
-    hipLaunchKernelGGL((k_tiles<TF, MP, RT, KW, D, GLU>), dim3(grid), dim3(64 * RT * KW), p.lds, s, (const uint8_t*)Wt,
+    hipLaunchKernelGGL((k_tiles<TF, MP, RT, KW, D>), dim3(grid), dim3(64 * RT * KW), p.lds, s, (const uint8_t*)Wt,
                        (const uint8_t*)Xq, Y, tickets, part, N, K, M, p.KP, p.spw, p.cs_slots, magic, p.CS,
-                       p.groups, p.pre, ga);
+                       p.groups, p.pre);
     return hipGetLastError();
 }
 
@@ -777,25 +796,115 @@ hipError_t launch_tiles_fmt(const TilesPlan& p, const void* Wt, const void* Xq, 
     return launch_tiles_mp<TF, 24>(p, Wt, Xq, Y, ws, N, K, M, s);
 }
 
-// The gated product's configurations: pairs of row tiles over KW parts of K.
+// ---- the gated product's launch --------------------------------------------------
+struct GluPlan {
+    int RT, KW, D;    // row tiles of both matrices and K parts per workgroup, groups in flight per wave
+    int CS, Mh;       // column slices and their columns
+    int spp;          // groups of K per pass
+    int cs_slots;     // LDS column stride, 16-byte slots (odd)
+    int groups;       // row groups
+    size_t lds;
+};
+
+size_t glu_tiles_lds(const GluPlan& p) {
+    const size_t act = (size_t)((p.Mh * p.cs_slots + kWave - 1) / kWave) * 1024 +
+                       (p.Mh <= 8 || p.Mh > 16 ? (size_t)p.cs_slots * 16 : 0);
+    const size_t red = (size_t)p.RT * p.KW * tiles_accumulators(p.Mh) * kWave * 16;
+    return act > red ? act : red;
+}
+
+// From sweeps of ten shapes of workgroup, one to six passes and one to three
+// column slices on MI355X over 4096 x 4096, 14336 x 4096, 28672 x 8192, 5504 x
+// 14336 and 1376 x 2048, M = 1..24, both formats.
+//
+// Workgroups of many row tiles, as long as there are enough of them: the
+// columns are copied once for all, and no partial sums are exchanged.  From
+// 1024 row tiles on (of each matrix), eight tiles of both matrices with whole
+// rows, or sixteen for Q4_0 beyond 8 columns (28672 x 8192 Q4_0 at 24: 57 us
+// against 61 with eight and 64 with four over two parts of K); from 512 on
+// eight, for Q4_0 in two parts of K beyond 8 columns and four in two parts up
+// to 8; from 320 on four in four parts (Q8_0: two up to 16 columns); below,
+// two in four parts, or in eight beyond 16 columns.  Below 128 row tiles and
+// beyond 8 columns, two column slices of a row group share its weights in
+// their XCD's L2.
+//
+// Passes.  The columns of a pass fill at most a workgroup's LDS, or half of a
+// CU's where two workgroups of eight waves can share it; a pass is a whole
+// number of rounds of loads of every wave.  28672 x 8192 Q8_0 at 24 columns,
+// whose columns do not fit at once: 84 us in four passes against 112 in
+// column slices and 115 with K split over workgroups.
+void glu_tiles_plan(bool q8, int N, int K, int M, GluPlan& p) {
+    const int T = (N + 15) / 16;
+    const int S = K >> 8;
+    p.D = 2;
+    p.CS = 1;
+    if (T >= 1024) {
+        p.RT = !q8 && M > 8 ? 16 : 8;
+        p.KW = 1;
+        if (!q8 && M <= 8) p.D = 4;
+    } else if (T >= 512) {
+        p.RT = q8 || M > 8 ? 8 : 4;
+        p.KW = q8 ? 1 : 2;
+    } else if (T >= 320) {
+        p.RT = 4;
+        p.KW = q8 && M <= 16 ? 2 : 4;
+    } else {
+        p.RT = 2;
+        p.KW = M > 16 ? 8 : 4;
+        if (T < 128 && M > 8) {
+            p.CS = 2;
+            p.KW = 4;
+        }
+    }
+    p.Mh = (M + p.CS - 1) / p.CS;
+    p.groups = (2 * T + p.RT - 1) / p.RT;
+    const bool two = p.RT * p.KW <= 8 && (int64_t)p.groups * p.CS > 256;   // two workgroups to a CU
+    const size_t limit = two ? 80 * 1024 : kTilesMaxLds;
+    const int round = p.KW * p.D;
+    auto fits = [&](int spp) {
+        p.spp = spp;
+        p.cs_slots = kGroupSlots * spp + 1;
+        p.lds = glu_tiles_lds(p);
+        return p.lds <= limit && p.Mh * p.cs_slots + kWave < (1 << 18);
+    };
+    if (fits(S)) return;
+    int passes = 2;   // equal ones, each a whole number of rounds where that does not cost a pass
+    while (!fits((((S + passes - 1) / passes) + round - 1) / round * round) && passes < S) ++passes;
+    if (p.lds > limit) fits(1);
+}
+
+template <class TF, int MP, int RT, int KW, int D>
+hipError_t launch_glu_tiles_cfg(const GluPlan& p, const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M,
+                                hipStream_t s) {
+    const GluArgs<true> ga = {(const uint8_t*)w.up, w.act, p.spp};
+    const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) + (uint64_t)p.cs_slots - 1) / (uint64_t)p.cs_slots);
+    const int grid = p.CS == 1 ? p.groups : (p.groups + 7) / 8 * 8 * p.CS;
+    hipLaunchKernelGGL((k_glu_tiles<TF, MP, RT, KW, D>), dim3(grid), dim3(64 * RT * KW), p.lds, s,
+                       (const uint8_t*)w.gate, (const uint8_t*)Xq, Y, N, K, M, p.cs_slots, magic, p.CS, p.groups, ga);
+    return hipGetLastError();
+}
+
 template <class TF, int MP>
-hipError_t launch_tiles_glu_mp(const TilesPlan& p, const GluMatrices& w, const void* Xq, float* Y, void* ws, int N,
-                               int K, int M, hipStream_t s) {
-    const GluArgs<true> ga = {(const uint8_t*)w.up, w.act};
-#define DG_TG(RR, WW, DD)                                                                                   \
-    if (p.RT == RR && p.KW == WW && p.D == DD)                                                              \
-        return launch_tiles_cfg<TF, MP, RR, WW, DD, true>(p, w.gate, Xq, Y, ws, N, K, M, s, ga);
-    DG_TG(2, 4, 2) DG_TG(2, 8, 2) DG_TG(4, 2, 2) DG_TG(4, 4, 2)
+hipError_t launch_glu_tiles_mp(const GluPlan& p, const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M,
+                               hipStream_t s) {
+    constexpr bool q4 = TF::kCodeLoads == 2;
+#define DG_TG(BUILT, RR, WW, DD)                                                         \
+    if constexpr (BUILT)                                                                 \
+        if (p.RT == RR && p.KW == WW && p.D == DD)                                       \
+            return launch_glu_tiles_cfg<TF, MP, RR, WW, DD>(p, w, Xq, Y, N, K, M, s);
+    DG_TG(q4 && MP > 8, 16, 1, 2) DG_TG(q4 && MP == 8, 8, 1, 4) DG_TG(!q4, 8, 1, 2)
+    DG_TG(q4 && MP > 8, 8, 2, 2) DG_TG(q4 && MP == 8, 4, 2, 2) DG_TG(!q4 && MP < 24, 4, 2, 2)
+    DG_TG(q4 || MP == 24, 4, 4, 2) DG_TG(true, 2, 4, 2) DG_TG(MP == 24, 2, 8, 2)
 #undef DG_TG
     return hipErrorInvalidValue;
 }
 
 template <class TF>
-hipError_t launch_tiles_glu_fmt(const TilesPlan& p, const GluMatrices& w, const void* Xq, float* Y, void* ws, int N,
-                                int K, int M, hipStream_t s) {
-    if (p.Mh <= 8) return launch_tiles_glu_mp<TF, 8>(p, w, Xq, Y, ws, N, K, M, s);
-    if (p.Mh <= 16) return launch_tiles_glu_mp<TF, 16>(p, w, Xq, Y, ws, N, K, M, s);
-    return launch_tiles_glu_mp<TF, 24>(p, w, Xq, Y, ws, N, K, M, s);
+hipError_t launch_glu_tiles_fmt(const GluPlan& p, const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M,
+                                hipStream_t s) {
+    if (p.Mh <= 8) return launch_glu_tiles_mp<TF, 8>(p, w, Xq, Y, N, K, M, s);
+    if (p.Mh <= 16) return launch_glu_tiles_mp<TF, 16>(p, w, Xq, Y, N, K, M, s);
+    return launch_glu_tiles_mp<TF, 24>(p, w, Xq, Y, N, K, M, s);
 }
 
 }  // namespace
@@ -836,7 +945,7 @@ static bool tiles_resolve(bool q8, int N, int K, int M, int unroll, TilesPlan& p
     }
     const int late = D >= 10;   // D + 10: the other prologue order (measurements only)
     if (late) D -= 10;
-    const bool ok = tiles_plan((N + 15) / 16, K, M, RT, KW, D, KP, CS, p);
+    const bool ok = tiles_plan(N, K, M, RT, KW, D, KP, CS, p);
     p.pre = !late;
     return ok;
 }
@@ -856,31 +965,13 @@ hipError_t launch_tiles(bool q8, int M, int unroll, const void* Wt, const void* 
               : launch_tiles_fmt<TilesQ4_0>(p, Wt, Xq, Y, ws, N, K, M, s);
 }
 
-// The gated product's plan: that of a GEMV over the row tiles of both
-// matrices, one row tile per workgroup becoming a pair over 8 parts of K.
-static bool tiles_glu_resolve(bool q8, int N, int K, int M, TilesPlan& p) {
-    const int T2 = 2 * ((N + 15) / 16);
-    int RT, KW, D, KP, CS;
-    tiles_default(q8, 16 * T2, K, M, RT, KW, D, KP, CS);
-    if (RT == 1) RT = 2;
-    const bool ok = tiles_plan(T2, K, M, RT, KW, D, KP, CS, p);
-    p.pre = 1;
-    return ok;
-}
-
-bool tiles_glu_config(bool q8, int N, int K, int M, size_t* ws_bytes) {
-    TilesPlan p;
-    if (N <= 0 || K <= 0 || M <= 0 || M > 24 || !tiles_glu_resolve(q8, N, K, M, p)) return false;
-    *ws_bytes = tiles_ws_bytes(p);
-    return true;
-}
-
-hipError_t launch_tiles_glu(bool q8, int M, const GluMatrices& w, const void* Xq, float* Y, void* ws, int N, int K,
+hipError_t launch_tiles_glu(bool q8, int M, const GluMatrices& w, const void* Xq, float* Y, int N, int K,
                             hipStream_t s) {
-    TilesPlan p;
-    if (!tiles_glu_resolve(q8, N, K, M, p) || p.lds > device_max_lds_per_block()) return hipErrorInvalidValue;
-    return q8 ? launch_tiles_glu_fmt<TilesQ8_0>(p, w, Xq, Y, ws, N, K, M, s)
-              : launch_tiles_glu_fmt<TilesQ4_0>(p, w, Xq, Y, ws, N, K, M, s);
+    GluPlan p;
+    glu_tiles_plan(q8, N, K, M, p);
+    if (p.lds > device_max_lds_per_block()) return hipErrorInvalidValue;
+    return q8 ? launch_glu_tiles_fmt<TilesQ8_0>(p, w, Xq, Y, N, K, M, s)
+              : launch_glu_tiles_fmt<TilesQ4_0>(p, w, Xq, Y, N, K, M, s);
 }
 
 }  // namespace dg

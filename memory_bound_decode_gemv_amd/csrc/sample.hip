@@ -341,9 +341,11 @@ k_sample_hist(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
     // top-k needs the counts, top-p the masses.  Counting alone takes no
     // weights: elements without weight are in the last bin, behind all others.
     const bool by_mass = q.p < 1.0, by_count = q.k > 0;
+    Share<T> ahead;
+    ahead.load(row, c0, a.C, a.vec);
     for (int64_t c = c0; c < c1; c += kSubMin) {
-        Share<T> e;
-        e.load(row, c, a.C, a.vec);
+        const Share<T> e = ahead;
+        if (c + kSubMin < c1) ahead.load(row, c + kSubMin, a.C, a.vec);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const float v = e.v[i];
@@ -482,6 +484,7 @@ template <class T>
 __global__ void __launch_bounds__(kChunkThreads)
 k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs a) {
     __shared__ u64 list[kCand];
+    __shared__ u64 sums[kMaxSubs];   // of the chunk's sub-chunks
     __shared__ uint32_t n_list, base;
     const int g = blockIdx.x;
     const int64_t r = blockIdx.y;
@@ -493,36 +496,48 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
     if (q.known != -2) return;   // workgroup-uniform
     const Borders b = q.k || q.p < 1.0 ? find_borders(ws, q) : no_borders();
     const bool listing = b.kbin < kBins || b.p0 <= b.p1;
-    if (threadIdx.x == 0) n_list = 0;
-    __syncthreads();
     const T* row = x + r * a.ld;
     const int s0 = g * a.subs_per_chunk;
-    const int s1 = s0 + a.subs_per_chunk < a.nsub ? s0 + a.subs_per_chunk : a.nsub;
-    for (int s = s0; s < s1; ++s) {
-        const int64_t c0 = (int64_t)s * a.sub;
-        const int64_t c1 = c0 + a.sub < a.C ? c0 + a.sub : a.C;
-        u64 sum = 0;
-        for (int64_t c = c0; c < c1; c += kSubMin) {
-            Share<T> e;
-            e.load(row, c, a.C, a.vec);
+    const int subs = a.nsub - s0 < a.subs_per_chunk ? a.nsub - s0 : a.subs_per_chunk;
+    if (threadIdx.x == 0) n_list = 0;
+    for (int i = threadIdx.x; i < subs; i += kChunkThreads) sums[i] = 0;
+    __syncthreads();
+    const int64_t c0 = (int64_t)s0 * a.sub;
+    const int64_t c1 = c0 + (int64_t)subs * a.sub < a.C ? c0 + (int64_t)subs * a.sub : a.C;
+    const int steps = a.sub / kSubMin;   // load steps of a sub-chunk
+    Share<T> ahead;
+    ahead.load(row, c0, a.C, a.vec);
+    int step = 0, sub = 0;
+    u64 sum = 0;
+    for (int64_t c = c0; c < c1; c += kSubMin) {
+        const Share<T> e = ahead;
+        if (c + kSubMin < c1) ahead.load(row, c + kSubMin, a.C, a.vec);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const float v = e.v[i];
-                const int bin = q.bin(v);
-                if (bin < b.sure) {
-                    const double w = q.weight(v);
-                    if (w >= q.min_p) sum += q.fixed(w);
-                } else if (listing && border_bin(b, bin) && q.fixed(q.weight(v))) {
+        for (int i = 0; i < kPer; ++i) {
+            const float v = e.v[i];
+            const int bin = q.bin(v);
+            const bool whole = bin < b.sure;
+            if (whole || (listing && border_bin(b, bin))) {
+                const double w = q.weight(v);
+                const u64 W = q.fixed(w);
+                if (whole) sum += w >= q.min_p ? W : 0ull;
+                else if (W) {
                     const uint32_t at = atomicAdd(&n_list, 1u);
                     if (at < (uint32_t)kCand)
                         list[at] = pack_key(order_image(v), (uint32_t)(c + Share<T>::element(i, a.vec)));
                 }
             }
         }
-        u64 total;
-        block_scan_u64<kChunkThreads>(sum, &total);
-        if (threadIdx.x == 0) ws->sum[s] = total;
+        if (++step == steps || c + kSubMin >= c1) {
+            sum = wave_sum_u64(sum);
+            if (lane_id() == 0 && sum) atomicAdd(&sums[sub], sum);
+            sum = 0;
+            step = 0;
+            ++sub;
+        }
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < subs; i += kChunkThreads) ws->sum[s0 + i] = sums[i];
     if (!listing) return;   // workgroup-uniform
     __syncthreads();
     // past kCand in one workgroup or in all of them: the pick reads the row

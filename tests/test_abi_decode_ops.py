@@ -144,15 +144,5 @@ def test_sample_workspace(lib):
 def test_gemv_glu_rejects_before_launch(lib, args, expect):
     for f in ("q4_0", "q8_0"):
         assert getattr(lib, f"dg_gemv_{f}_glu")(*args, None) == expect
-        assert getattr(lib, f"dg_gemv_{f}_tiles_glu")(*args, None, 0, None) == expect
+        assert getattr(lib, f"dg_gemv_{f}_tiles_glu")(*args, None) == expect
 
-
-def test_gemv_tiles_glu_workspace(lib):
-    need = lib.dg_gemv_q4_0_tiles_glu_workspace_bytes(64, 28672, 24)
-    assert need > 0 and lib.dg_gemv_q4_0_tiles_glu_workspace_bytes(14336, 4096, 16) == 0
-    assert lib.dg_gemv_q4_0_tiles_glu_workspace_bytes(64, 100, 24) == 0
-    assert lib.dg_gemv_q8_0_tiles_glu_workspace_bytes(0, 4096, 24) == 0
-    f = lib.dg_gemv_q4_0_tiles_glu
-    assert f(A, A, A, A, 64, 28672, 24, 0, None, 0, None) == WORKSPACE
-    assert f(A, A, A, A, 64, 28672, 24, 0, A, need - 1, None) == WORKSPACE
-    assert f(A, A, A, A, 64, 28672, 24, 0, P(0x1008), need, None) == MISALIGNED

@@ -44,8 +44,7 @@ class Step:
         self.T, self.p = torch.full((M,), 0.8, **f32), torch.full((M,), 0.95, **f32)
         self.k = torch.full((M,), 40, dtype=torch.int32, device=dev)
         self.idx = torch.zeros(M, dtype=torch.int64, device=dev)
-        need = max(getattr(dg, f"dg_gemv_{fmt}_tiles_glu_workspace_bytes")(F, D, M),
-                   getattr(dg, f"dg_gemv_{fmt}_tiles_workspace_bytes")(D, F, M), 16)
+        need = max(getattr(dg, f"dg_gemv_{fmt}_tiles_workspace_bytes")(D, F, M), 16)
         self.ws = torch.zeros(need, **u8)
         self.sws = torch.zeros(dg.dg_sample_workspace_bytes(M, V), **u8)
         self.new_inputs()
@@ -60,7 +59,7 @@ class Step:
         dg, M, D, F, V, fmt = self.dg, self.M, self.D, self.F, self.V, self.fmt
         dg.dg_rmsnorm_q8_1(self.x, self.w1, self.x8, res=self.h, h=self.h, eps=EPS)
         if self.tiles:
-            getattr(dg, f"dg_gemv_{fmt}_tiles_glu")(self.gate, self.up, self.x8, self.f, F, D, M, ws=self.ws)
+            getattr(dg, f"dg_gemv_{fmt}_tiles_glu")(self.gate, self.up, self.x8, self.f, F, D, M)
         else:
             getattr(dg, f"dg_gemv_{fmt}_glu")(self.gate, self.up, self.x8, self.f, F, D, M)
         dg.dg_quantize_q8_1(self.f, self.f8, M, F)
