@@ -228,8 +228,7 @@ def _run_own(state):
         return (y, state["h"][:, :K]) if c["res"] else (y,)
     if c["op"] == "glu":
         name = "dg_gemv_%s%s_glu" % (c["fmt"], "_tiles" if c["tiles"] else "")
-        more = {"ws": state["ws"]} if c["tiles"] else {}
-        getattr(dg, name)(state["Wg"], state["Wu"], state["X"], state["Y"], c["N"], c["K"], c["M"], act=c["act"], **more)
+        getattr(dg, name)(state["Wg"], state["Wu"], state["X"], state["Y"], c["N"], c["K"], c["M"], act=c["act"])
         return state["Y"]
     dg.dg_sample_rows(state["x"], state["u"], state["idx"], R=c["R"], C=c["C"], ld=c["ld"], temperature=state["T"],
                       top_k=state["k"], top_p=state["p"], min_p=state["mp"], ws=state["ws"])
