@@ -216,6 +216,14 @@ k_units(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
     store(out_row0, nout);
 }
 
+// The gated product takes up to five columns of Q4_0 rows of one unit and four
+// of longer ones, as many of Q8_0 as fit the registers, and two or three units
+// in flight.
+template <class F, bool GLU>
+constexpr bool units_instantiated(int S, int M, int depth) {
+    return !GLU || (depth <= 3 && M <= 8 && (F::kBlockBytes == 34 || M <= (S == 1 ? 5 : 4)));
+}
+
 template <class F, bool GLU>
 hipError_t launch_units(int K, int M, int depth, const void* Wq, const void* Xq, float* Y, int N, int grid, int block,
                         GluArgs<GLU> ga, hipStream_t s) {
@@ -240,6 +248,7 @@ hipError_t launch_units(int K, int M, int depth, const void* Wq, const void* Xq,
     const uint8_t* w = (const uint8_t*)Wq;
     const uint8_t* x = (const uint8_t*)Xq;
 #define DG_SMD(SS, MM, DD)                                                                                 \
+    if constexpr (units_instantiated<F, GLU>(SS, MM, DD))                                                  \
     if (S == SS && M == MM && depth == DD) {                                                               \
         hipLaunchKernelGGL((k_units<F, SS, MM, DD, GLU>), dim3(grid), dim3(block), lds, s, w, x, Y, N, K, ga); \
         return hipGetLastError();                                                                          \
@@ -281,11 +290,25 @@ hipError_t launch_units_glu(bool q8, int K, int M, int depth, const GluMatrices&
 // and of two GEMVs and an elementwise kernel two launches are gone.
 hipError_t launch_gemv_glu(bool q8, const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M,
                            hipStream_t s) {
+    // Measured on MI355X over 14336 x 4096, 28672 x 8192, 5504 x 14336, 5003 x
+    // 2048 and 1376 x 4096, both formats, M = 1..24, against every matrix-core
+    // shape, six grids and three depths.  Q4_0 rows of one unit stream to five
+    // columns (14336 x 4096 at 5: 18.2 us against 20.0 on the matrix cores, at
+    // 6 21.7 against 19.9), longer ones to four; Q8_0, whose rows hold the
+    // memory longer, as far as the registers reach (14336 x 4096 at 8: 26.3
+    // against 29.0).
     const int S = (K / 64 + kWave - 1) / kWave;
-    if (S <= 4 && M <= 4 && M * S <= 8) {
-        int grid, block;
-        units_default_grid(N, M, grid, block);
-        return launch_units_glu(q8, K, M, 0, w, Xq, Y, N, grid, block, s);
+    if (S <= 4 && M * S <= 8 && (q8 || M <= (S == 1 ? 5 : 4))) {
+        // Workgroups of four waves, two or three to a CU (14336 x 4096 Q4_0 at 4
+        // columns: 15.6 us with 768 of them, 17.3 with 512; Q8_0 at 8: 26.3
+        // with 512, 28.4 with 768); for one column of many long rows, one row
+        // pair after another on all that fit (28672 x 8192 Q4_0 38.9 us with
+        // 4096, 40.2 with 2048).  A wave with a single pair has both its rows
+        // in flight at once (1376 x 4096 Q4_0: 3.8 us against 4.1).
+        const int need = (N + 3) / 4;
+        const int g = S >= 2 ? (M == 1 && N >= 16384 ? 4096 : 512) : (q8 && M > 4 ? 512 : 768);
+        const bool single = need <= g;
+        return launch_units_glu(q8, K, M, single && S == 1 && M == 1 ? 3 : 0, w, Xq, Y, N, single ? need : g, 256, s);
     }
     return launch_mfma_glu(q8, M, w, Xq, Y, N, K, s);
 }

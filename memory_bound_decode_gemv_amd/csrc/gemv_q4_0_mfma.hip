@@ -514,10 +514,21 @@ hipError_t launch_qmfma(int M, int unroll, const void* Wq, const void* Xq, float
     return launch_mfma_mp<WF, 24>(RT, KS, DEPTH, CB, Wq, Xq, Y, N, K, M, grid, s);
 }
 
-// The gated product: one pair of row tiles per workgroup, K in four parts.
+// The gated product's configurations, two chunks deep.  Measured on MI355X
+// over 14336 x 4096, 28672 x 8192, 5504 x 14336, 5003 x 2048, 1376 x 4096 and
+// 4096 x 20480, M = 1..24: two pairs of row tiles with whole rows from 512 row
+// tiles on for rows up to 4096, or beyond 16 columns from 1024 on (14336 x
+// 4096 Q4_0 at 16 columns: 21.8 us, 24.2 with one pair over two parts of K,
+// 36.4 over four); one pair over two parts from 257 on (28672 x 8192 Q4_0 at 8:
+// 61.4 against 70.6 us with two pairs and 69.1 over four); else over four
+// (1376 x 4096 Q4_0 at 8: 8.9 us).
 template <class WF, int MP>
 hipError_t launch_glu_mp(const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M, hipStream_t s) {
     const GluArgs<true> ga = {(const uint8_t*)w.up, w.act};
+    const int tiles = (N + 15) / 16;
+    if (tiles >= 512 && (K <= 4096 || (M > 16 && tiles >= 1024)))
+        return launch_mfma_cfg<WF, 8, MP, 4, 1, 2, true>(w.gate, Xq, Y, N, K, M, 0, s, ga);
+    if (tiles > 256) return launch_mfma_cfg<WF, 8, MP, 2, 2, 2, true>(w.gate, Xq, Y, N, K, M, 0, s, ga);
     return launch_mfma_cfg<WF, 8, MP, 2, 4, 2, true>(w.gate, Xq, Y, N, K, M, 0, s, ga);
 }
 

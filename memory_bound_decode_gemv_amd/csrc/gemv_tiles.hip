@@ -824,7 +824,7 @@ size_t glu_tiles_lds(const GluPlan& p) {
 // against 61 with eight and 64 with four over two parts of K); from 512 on
 // eight, for Q4_0 in two parts of K beyond 8 columns and four in two parts up
 // to 8; from 320 on four in four parts (Q8_0: two up to 16 columns); below,
-// two in four parts, or in eight beyond 16 columns.  Below 128 row tiles and
+// two in four parts, or in eight beyond 16 columns on rows of 4096 and more.  Below 128 row tiles and
 // beyond 8 columns, two column slices of a row group share its weights in
 // their XCD's L2.
 //
@@ -850,7 +850,7 @@ void glu_tiles_plan(bool q8, int N, int K, int M, GluPlan& p) {
         p.KW = q8 && M <= 16 ? 2 : 4;
     } else {
         p.RT = 2;
-        p.KW = M > 16 ? 8 : 4;
+        p.KW = M > 16 && S >= 16 ? 8 : 4;   // every wave has a round of loads
         if (T < 128 && M > 8) {
             p.CS = 2;
             p.KW = 4;

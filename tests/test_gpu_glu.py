@@ -121,7 +121,7 @@ class Case:
 # row-major: units of one to four (M * units <= 8), matrix cores at every padded column count; rows not a multiple of
 # any tile; K of an odd number of 256s and past four units
 SHAPES = [(1, 256, 1), (15, 256, 4), (16, 512, 24), (17, 768, 17), (300, 4096, 1), (129, 4096, 2), (65, 4352, 3),
-          (40, 4096, 4), (33, 8448, 2), (70, 8192, 4), (50, 16384, 2), (31, 16384, 3), (20, 16640, 1), (45, 2048, 5),
+          (40, 4096, 4), (33, 8448, 2), (70, 8192, 4), (8200, 512, 6), (8195, 512, 20), (4200, 768, 7), (4100, 4352, 17), (23, 4096, 5), (25, 4096, 6), (50, 16384, 2), (31, 16384, 3), (20, 16640, 1), (45, 2048, 5),
           (37, 2304, 8), (64, 4096, 9), (100, 1280, 16), (81, 4608, 17), (95, 2560, 18), (48, 4096, 24)]
 
 
