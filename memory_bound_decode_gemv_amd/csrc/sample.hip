@@ -45,10 +45,12 @@ namespace {
 
 constexpr int kBins = 512;
 constexpr int kCand = 4096;          // keys that the pick kernel holds in LDS
+constexpr int kChunkList = 2048;     // of them that one workgroup of the gather kernel lists
 constexpr int kSubMin = 2048;        // elements of a sub-chunk, at least
 constexpr int kMaxSubs = 1024;       // sub-chunks of a row, at most
 constexpr int kChunkThreads = 256;
 constexpr int kPickThreads = 1024;
+static_assert(kPickThreads == kMaxSubs, "a thread of the pick kernel per sub-chunk");
 constexpr int kTargetGroups = 1024;
 constexpr int kBatchRows = 512;      // rows whose workspace exists at once
 constexpr double kLog2e = 1.4426950408889634;
@@ -109,18 +111,6 @@ struct SampleArgs {
     bool vec;       // rows are 16-byte aligned
 };
 
-// The workspace of one row.
-struct RowSpace {
-    u64 key[kMaxSubs];       // per chunk: largest key
-    float low[kMaxSubs];     // per chunk: smallest finite value (+inf if none)
-    u64 mass[kBins];
-    uint32_t count[kBins];
-    uint32_t ncand;
-    uint32_t pad;
-    u64 sum[kMaxSubs];       // per sub-chunk: kept for sure
-    u64 cand[kCand];
-};
-
 __device__ __forceinline__ float key_value(u64 key) {
     const uint32_t img = (uint32_t)(key >> 32);
     return __builtin_bit_cast(float, (img & 0x80000000u) ? img ^ 0x80000000u : ~img);
@@ -137,66 +127,126 @@ struct Row {
     int64_t known;    // the token, when no draw is needed; else -2
     int k;            // 0: off
     int F;
+    float far;        // elements whose m - x exceeds this have w < min_p
 
-    // w = 2^t, t = (x - m) log2(e) / T, as a binary64 number in [0, 1] (0 where
-    // t is not a number): t = n + f with n an integer and |f| <= 1/2, and
-    // 2^f = sum (f ln 2)^k / k!, whose terms past k = 12 are below 2^-52.
+    // w as a binary64 number in [0, 1]
     __device__ __forceinline__ double weight(float x) const {
-        const double d = x == m ? 0.0 : (double)x - (double)m;
-        const double t = fmax(d * c, -1100.0);
-        const double n = rint(t);
-        const double f = t - n;
-        double e = 2.5678435993488196e-11;   // (ln 2)^k / k!, k = 12 .. 0
-        e = fma(e, f, 4.44553827187081e-10);
-        e = fma(e, f, 7.054911620801121e-09);
-        e = fma(e, f, 1.0178086009239696e-07);
-        e = fma(e, f, 1.3215486790144305e-06);
-        e = fma(e, f, 1.5252733804059838e-05);
-        e = fma(e, f, 1.5403530393381606e-04);
-        e = fma(e, f, 1.3333558146428441e-03);
-        e = fma(e, f, 9.618129107628477e-03);
-        e = fma(e, f, 5.5504108664821576e-02);
-        e = fma(e, f, 2.402265069591007e-01);
-        e = fma(e, f, 6.931471805599453e-01);
-        e = fma(e, f, 1.0);
-        return ldexp(e, (int)n);
+        double w[1];
+        const float v[1] = {x};
+        weights(v, w);
+        return w[0];
+    }
+    // The weights of N elements, side by side so that their chains of dependent
+    // operations overlap.  w = 2^t, t = (x - m) log2(e) / T; t = n + f with n an
+    // integer and |f| <= 1/2, and 2^f by the polynomial of degree 10 that
+    // interpolates it at the Chebyshev nodes of [-1/2, 1/2] (within 3.2e-16,
+    // and 1 at 0).  w = 0 where t is not a number; an infinite m, which cannot
+    // be subtracted, is the largest binary64 number instead.
+    template <int N>
+    __device__ __forceinline__ void weights(const float (&x)[N], double (&w)[N]) const {
+        constexpr double kLargest = 1.7976931348623157e308;
+        const double top = fmin((double)m, kLargest);
+        double n[N], f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const double t = fmax((fmin((double)x[i], kLargest) - top) * c, -1100.0);
+            n[i] = rint(t);
+            f[i] = t - n[i];
+            w[i] = 7.072585949269223e-09;
+        }
+#define DG_TERM(C)                                          \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) w[i] = fma(w[i], f[i], C);
+        DG_TERM(1.0208690299958306e-07)
+        DG_TERM(1.321544258792169e-06)
+        DG_TERM(1.5252657260200837e-05)
+        DG_TERM(0.0001540353044173605)
+        DG_TERM(0.0013333558230164974)
+        DG_TERM(0.009618129107606888)
+        DG_TERM(0.05550410866444772)
+        DG_TERM(0.24022650695910097)
+        DG_TERM(0.69314718055995)
+        DG_TERM(1.0)
+#undef DG_TERM
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = ldexp(w[i], (int)n[i]);
     }
     // round(2^F w) by the binary64 addition 2^52 + 2^F w (F <= 51)
     __device__ __forceinline__ u64 fixed(double w) const {
         const double v = fma(w, (double)(1ull << F), 4503599627370496.0);
         return __builtin_bit_cast(u64, v) & 0x000FFFFFFFFFFFFFull;
     }
-    // the step of m - x, larger for smaller x; equal values share a bin
-    __device__ __forceinline__ int bin(float x) const {
-        const float d = x == m ? 0.0f : fminf(m - x, 3.4028234e38f);
-        return (int)fminf(d * scale, (float)(kBins - 1));
-    }
+    // m - x, 0 also where both are infinite
+    __device__ __forceinline__ float below(float x) const { return x == m ? 0.0f : fminf(m - x, 3.4028234e38f); }
+    // its step, larger for smaller x; equal values share a bin
+    __device__ __forceinline__ int bin(float x) const { return bin_of(below(x)); }
+    __device__ __forceinline__ int bin_of(float d) const { return (int)fminf(d * scale, (float)(kBins - 1)); }
 };
 
-__device__ __forceinline__ Row make_row(const SampleArgs& a, int64_t r, u64 top, float low) {
+// What the bins say about the borders of top-k and top-p.
+struct Borders {
+    int sure;              // bins below this are kept whole
+    int kbin;              // the bin of the k-th token, or kBins when top-k is off
+    int p0, p1;            // bins p0..p1 may hold top-p's border (p0 > p1: top-p is off)
+    uint32_t krank;        // its rank within kbin, from 1
+    u64 kmass;             // mass above kbin
+    u64 pmass;             // mass above p0
+    u64 total;             // mass of all bins (0 without top-p)
+};
+
+__device__ __forceinline__ bool border_bin(const Borders& b, int i) { return i == b.kbin || (i >= b.p0 && i <= b.p1); }
+
+// The workspace of one row.
+struct RowSpace {
+    Row row;                 // from the gather kernel to the pick kernel
+    Borders borders;
+    u64 key[kMaxSubs];       // per chunk: largest key
+    float low[kMaxSubs];     // per chunk: smallest finite value (+inf if none)
+    u64 mass[kBins];
+    uint32_t count[kBins];
+    uint32_t ncand;
+    uint32_t pad;
+    u64 sum[kMaxSubs];       // per sub-chunk: kept for sure
+    u64 cand[kCand];
+};
+
+// A row's parameters as the caller gave them.
+struct Params {
+    float T, p, min_p, u;
+    int k;
+};
+
+__device__ __forceinline__ Params load_params(const SampleArgs& a, int64_t r) {
+    Params t;
+    t.T = a.temperature ? a.temperature[r] : 1.0f;
+    t.p = a.top_p ? a.top_p[r] : 1.0f;
+    t.min_p = a.min_p ? a.min_p[r] : 0.0f;
+    t.u = a.u[r];
+    t.k = a.top_k ? a.top_k[r] : 0;
+    return t;
+}
+
+__device__ __forceinline__ Row make_row(const SampleArgs& a, const Params& t, u64 top, float low) {
     Row q;
-    const uint32_t img = (uint32_t)(top >> 32);
-    const double T = a.temperature ? (double)a.temperature[r] : 1.0;
-    const int k = a.top_k ? a.top_k[r] : 0;
-    const double p = a.top_p ? (double)a.top_p[r] : 1.0;
-    const double mp = a.min_p ? (double)a.min_p[r] : 0.0;
-    const double u = (double)a.u[r];
     q.m = key_value(top);
     q.known = -2;
-    if (img == 0xFFFFFFFFu || !(T > 0.0)) q.known = (int64_t)key_index(top);   // a NaN, or greedy
-    else if (q.m == -INFINITY) q.known = -1;                                   // nothing to draw from
-    q.k = k > 0 && k < a.C ? k : 0;
-    q.p = p < 1.0 ? (p > 0.0 ? p : 0.0) : 1.0;
-    q.min_p = mp > 0.0 ? (mp < 1.0 ? mp : 1.0) : 0.0;
-    q.u = u > 0.0 ? (u < 1.0 ? u : 1.0) : 0.0;
+    if ((uint32_t)(top >> 32) == 0xFFFFFFFFu || !(t.T > 0.0f)) q.known = (int64_t)key_index(top);   // a NaN, or greedy
+    else if (q.m == -INFINITY) q.known = -1;                                                       // nothing to draw from
+    q.k = t.k > 0 && t.k < a.C ? t.k : 0;
+    q.p = t.p < 1.0f ? (t.p > 0.0f ? t.p : 0.0f) : 1.0f;
+    q.min_p = t.min_p > 0.0f ? (t.min_p < 1.0f ? t.min_p : 1.0f) : 0.0f;
+    q.u = t.u > 0.0f ? (t.u < 1.0f ? t.u : 1.0f) : 0.0f;
     q.F = a.F;
-    q.c = kLog2e / T;
+    q.c = kLog2e / (double)t.T;
     // the range that has weight: down to the smallest value, and no further than W = 0
-    double range = (double)q.m - (double)low;
-    const double reach = (double)(a.F + 1) / q.c;
-    if (reach < range) range = reach;
-    q.scale = range > 0.0 ? fminf((float)((double)kBins / range), 1e30f) : 0.0f;
-    if (q.m == INFINITY) q.scale = 1.0f;   // m - x is 0 or infinite
+    constexpr float kLn2 = 0.69314718f;
+    const float range = fminf(q.m - low, (float)(a.F + 1) * kLn2 * t.T);
+    q.scale = range > 0.0f ? fminf((float)kBins / range, 1e30f) : 0.0f;
+    if (q.m == INFINITY) {   // m - x is 0 or infinite, at any temperature
+        q.scale = 1.0f;
+        q.c = 1.0;
+    }
+    // -log2(min_p) / c, and more than its roundings
+    q.far = q.min_p > 0.0 ? (1.001f * -log2f((float)q.min_p) + 1e-5f) * kLn2 * t.T : INFINITY;
     return q;
 }
 
@@ -325,34 +375,37 @@ k_sample_hist(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
     const int g = blockIdx.x;
     const int64_t r = blockIdx.y;
     RowSpace* ws = spaces + r;
+    const T* row = x + r * a.ld;
+    const int64_t c0 = (int64_t)g * a.subs_per_chunk * a.sub;
+    const int64_t c1 = c0 + (int64_t)a.subs_per_chunk * a.sub < a.C ? c0 + (int64_t)a.subs_per_chunk * a.sub : a.C;
+    Share<T> ahead;
+    const Params given = load_params(a, r);
+    ahead.load(row, c0, a.C, a.vec);   // in flight while the row's extremes arrive
     u64 top;
     float low;
     row_extremes(ws, a.G, &top, &low);
-    const Row q = make_row(a, r, top, low);
+    const Row q = make_row(a, given, top, low);
     if (q.known != -2 || (q.k == 0 && q.p >= 1.0)) return;   // workgroup-uniform: nothing to select
     for (int i = threadIdx.x; i < kBins; i += kChunkThreads) {
         mass[i] = 0;
         count[i] = 0;
     }
     __syncthreads();
-    const T* row = x + r * a.ld;
-    const int64_t c0 = (int64_t)g * a.subs_per_chunk * a.sub;
-    const int64_t c1 = c0 + (int64_t)a.subs_per_chunk * a.sub < a.C ? c0 + (int64_t)a.subs_per_chunk * a.sub : a.C;
     // top-k needs the counts, top-p the masses.  Counting alone takes no
     // weights: elements without weight are in the last bin, behind all others.
     const bool by_mass = q.p < 1.0, by_count = q.k > 0;
-    Share<T> ahead;
-    ahead.load(row, c0, a.C, a.vec);
     for (int64_t c = c0; c < c1; c += kSubMin) {
         const Share<T> e = ahead;
         if (c + kSubMin < c1) ahead.load(row, c + kSubMin, a.C, a.vec);
+        double w[kPer];
+        if (by_mass) q.weights(e.v, w);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const float v = e.v[i];
             if (v > -INFINITY) {
                 const int b = q.bin(v);
                 if (by_mass) {
-                    const u64 W = q.fixed(q.weight(v));
+                    const u64 W = q.fixed(w[i]);
                     if (W) atomicAdd(&mass[b], W);
                 }
                 if (by_count) atomicAdd(&count[b], 1u);
@@ -367,38 +420,41 @@ k_sample_hist(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
 }
 
 // ---- borders ------------------------------------------------------------------
-// What the bins say about the borders of top-k and top-p.
-struct Borders {
-    int sure;              // bins below this are kept whole
-    int kbin;              // the bin of the k-th token, or kBins when top-k is off
-    int p0, p1;            // bins p0..p1 may hold top-p's border (p0 > p1: top-p is off)
-    uint32_t krank;        // its rank within kbin, from 1
-    u64 kmass;             // mass above kbin
-    u64 pmass;             // mass above p0
-    u64 total;             // mass of all bins (0 without top-p)
-};
-
-__device__ __forceinline__ bool border_bin(const Borders& b, int i) { return i == b.kbin || (i >= b.p0 && i <= b.p1); }
-
 // The shortest prefix has mass >= this: ceil(p * total), at least 1.
 __device__ __forceinline__ u64 p_target(double p, u64 total) {
     const u64 t = (u64)ceil(p * (double)total);
     return t < 1 ? 1 : (t > total ? total : t);
 }
 
+constexpr int kLaneBins = kBins / kWave;
+
+// The bins of a lane of the first wave (the others load nothing).
+struct LaneBins {
+    u64 mass[kLaneBins];
+    uint32_t count[kLaneBins];
+    __device__ __forceinline__ void load(const RowSpace* ws) {
+        if (threadIdx.x < kWave) {
+#pragma unroll
+            for (int i = 0; i < kLaneBins; ++i) {
+                mass[i] = ws->mass[threadIdx.x * kLaneBins + i];
+                count[i] = ws->count[threadIdx.x * kLaneBins + i];
+            }
+        }
+    }
+};
+
 // Every thread of the workgroup calls this; the first wave scans the bins,
 // eight per lane.
-__device__ __forceinline__ Borders find_borders(const RowSpace* ws, const Row& q) {
+__device__ __forceinline__ Borders find_borders(const LaneBins& bins_of, const Row& q) {
     __shared__ Borders out;
-    constexpr int kLaneBins = kBins / kWave;
     if (threadIdx.x < kWave) {
         const int lane = threadIdx.x;
-        u64 mass[kLaneBins], m_in = 0;
-        uint32_t count[kLaneBins], c_in = 0;
+        const u64(&mass)[kLaneBins] = bins_of.mass;
+        const uint32_t(&count)[kLaneBins] = bins_of.count;
+        u64 m_in = 0;
+        uint32_t c_in = 0;
 #pragma unroll
         for (int i = 0; i < kLaneBins; ++i) {
-            mass[i] = ws->mass[lane * kLaneBins + i];
-            count[i] = ws->count[lane * kLaneBins + i];
             m_in += mass[i];
             c_in += count[i];
         }
@@ -483,48 +539,65 @@ __device__ __forceinline__ Borders no_borders() {
 template <class T>
 __global__ void __launch_bounds__(kChunkThreads)
 k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs a) {
-    __shared__ u64 list[kCand];
+    __shared__ u64 list[kChunkList];
     __shared__ u64 sums[kMaxSubs];   // of the chunk's sub-chunks
     __shared__ uint32_t n_list, base;
     const int g = blockIdx.x;
     const int64_t r = blockIdx.y;
     RowSpace* ws = spaces + r;
-    u64 top;
-    float low;
-    row_extremes(ws, a.G, &top, &low);
-    const Row q = make_row(a, r, top, low);
-    if (q.known != -2) return;   // workgroup-uniform
-    const Borders b = q.k || q.p < 1.0 ? find_borders(ws, q) : no_borders();
-    const bool listing = b.kbin < kBins || b.p0 <= b.p1;
     const T* row = x + r * a.ld;
     const int s0 = g * a.subs_per_chunk;
     const int subs = a.nsub - s0 < a.subs_per_chunk ? a.nsub - s0 : a.subs_per_chunk;
+    const int64_t c0 = (int64_t)s0 * a.sub;
+    const int64_t c1 = c0 + (int64_t)subs * a.sub < a.C ? c0 + (int64_t)subs * a.sub : a.C;
+    const Params given = load_params(a, r);
+    LaneBins bins;
+    bins.load(ws);
+    Share<T> ahead;
+    ahead.load(row, c0, a.C, a.vec);   // in flight while the row's extremes and bins arrive
+    u64 top;
+    float low;
+    row_extremes(ws, a.G, &top, &low);
+    const Row q = make_row(a, given, top, low);
+    const bool drawn = q.known == -2;
+    const Borders b = drawn && (q.k || q.p < 1.0) ? find_borders(bins, q) : no_borders();
+    if (g == 0 && threadIdx.x == 0) {
+        ws->row = q;
+        ws->borders = b;
+    }
+    if (!drawn) return;   // workgroup-uniform
+    const bool listing = b.kbin < kBins || b.p0 <= b.p1;
     if (threadIdx.x == 0) n_list = 0;
     for (int i = threadIdx.x; i < subs; i += kChunkThreads) sums[i] = 0;
     __syncthreads();
-    const int64_t c0 = (int64_t)s0 * a.sub;
-    const int64_t c1 = c0 + (int64_t)subs * a.sub < a.C ? c0 + (int64_t)subs * a.sub : a.C;
     const int steps = a.sub / kSubMin;   // load steps of a sub-chunk
-    Share<T> ahead;
-    ahead.load(row, c0, a.C, a.vec);
     int step = 0, sub = 0;
     u64 sum = 0;
     for (int64_t c = c0; c < c1; c += kSubMin) {
         const Share<T> e = ahead;
         if (c + kSubMin < c1) ahead.load(row, c + kSubMin, a.C, a.vec);
+        // 0: no part in the sums or the list; 1: kept for sure unless min-p drops it; 2: listed
+        int part[kPer];
+        bool any = false;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const float v = e.v[i];
-            const int bin = q.bin(v);
-            const bool whole = bin < b.sure;
-            if (whole || (listing && border_bin(b, bin))) {
-                const double w = q.weight(v);
-                const u64 W = q.fixed(w);
-                if (whole) sum += w >= q.min_p ? W : 0ull;
-                else if (W) {
+            const float d = q.below(e.v[i]);
+            const int bin = q.bin_of(d);
+            part[i] = bin < b.sure ? (d <= q.far ? 1 : 0) : (listing && border_bin(b, bin) ? 2 : 0);
+            any |= part[i] != 0;
+        }
+        if (__any(any)) {   // few steps of a wave, where few tokens are kept
+            double w[kPer];
+            q.weights(e.v, w);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const u64 W = q.fixed(w[i]);
+                if (part[i] == 1) {
+                    sum += w[i] >= q.min_p ? W : 0ull;
+                } else if (part[i] == 2 && W) {
                     const uint32_t at = atomicAdd(&n_list, 1u);
-                    if (at < (uint32_t)kCand)
-                        list[at] = pack_key(order_image(v), (uint32_t)(c + Share<T>::element(i, a.vec)));
+                    if (at < (uint32_t)kChunkList)
+                        list[at] = pack_key(order_image(e.v[i]), (uint32_t)(c + Share<T>::element(i, a.vec)));
                 }
             }
         }
@@ -540,10 +613,12 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
     for (int i = threadIdx.x; i < subs; i += kChunkThreads) ws->sum[s0 + i] = sums[i];
     if (!listing) return;   // workgroup-uniform
     __syncthreads();
-    // past kCand in one workgroup or in all of them: the pick reads the row
-    if (threadIdx.x == 0) base = n_list ? atomicAdd(&ws->ncand, n_list) : 0u;
+    // more than kChunkList here, or kCand in all: the pick reads the row
+    if (threadIdx.x == 0)
+        base = n_list ? atomicAdd(&ws->ncand, n_list <= (uint32_t)kChunkList ? n_list : (uint32_t)kCand + 1u) : 0u;
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < n_list && base + i < (uint32_t)kCand; i += kChunkThreads)
+    for (uint32_t i = threadIdx.x; i < n_list && i < (uint32_t)kChunkList && base + i < (uint32_t)kCand;
+         i += kChunkThreads)
         ws->cand[base + i] = list[i];
 }
 
@@ -760,6 +835,7 @@ __device__ __forceinline__ void pick_token(PickShared& s, int n, bool from_row, 
     const int64_t per = (c1 - c0 + kPickThreads - 1) / kPickThreads;   // consecutive elements per thread
     auto kept_weight = [&](int64_t c) -> u64 {
         const float v = Logit<T>::load(row + c);
+        if (q.below(v) > q.far) return 0ull;
         const double w = q.weight(v);
         return w >= q.min_p && pack_key(order_image(v), (uint32_t)c) >= threshold ? q.fixed(w) : 0ull;
     };
@@ -790,20 +866,20 @@ k_sample_pick(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
     __shared__ PickShared s;
     const int64_t r = blockIdx.x;
     RowSpace* ws = spaces + r;
-    u64 top;
-    float low;
-    row_extremes(ws, a.G, &top, &low);
-    const Row q = make_row(a, r, top, low);
+    const u64 first = ws->cand[threadIdx.x];   // most lists are no longer; used only if so many are listed
+    const u64 sum = (int)threadIdx.x < a.nsub ? ws->sum[threadIdx.x] : 0ull;
+    const uint32_t listed = ws->ncand;
+    const Row q = ws->row;
+    const Borders b = ws->borders;
     if (q.known != -2) {   // workgroup-uniform
         if (threadIdx.x == 0) a.idx[r] = q.known;
         return;
     }
-    const Borders b = q.k || q.p < 1.0 ? find_borders(ws, q) : no_borders();
-    const uint32_t listed = ws->ncand;
     const bool from_row = listed > (uint32_t)kCand;
     const int n = from_row ? 0 : (int)listed;
-    for (int i = threadIdx.x; i < n; i += kPickThreads) s.key[i] = ws->cand[i];
-    if ((int)threadIdx.x < a.nsub) s.sum[threadIdx.x] = ws->sum[threadIdx.x];
+    if ((int)threadIdx.x < n) s.key[threadIdx.x] = first;
+    for (int i = threadIdx.x + kPickThreads; i < n; i += kPickThreads) s.key[i] = ws->cand[i];
+    s.sum[threadIdx.x] = sum;
     if (threadIdx.x == 0) s.found = 0;
     __syncthreads();
     pick_token<T>(s, n, from_row, x + r * a.ld, q, b, a, false, r);
@@ -828,7 +904,7 @@ k_sample_row(const T* __restrict__ x, SampleArgs a) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kPickThreads / kWave; ++w) top = umax64(top, keys[w]);
-    Row q = make_row(a, r, top, 0.0f);
+    Row q = make_row(a, load_params(a, r), top, 0.0f);
     if (q.known != -2) {   // workgroup-uniform
         if (threadIdx.x == 0) a.idx[r] = q.known;
         return;
