@@ -200,7 +200,7 @@ struct RowSpace {
     Row row;                 // from the gather kernel to the pick kernel
     Borders borders;
     u64 key[kMaxSubs];       // per chunk: largest key
-    float low[kMaxSubs];     // per chunk: smallest finite value (+inf if none)
+    uint32_t low[kMaxSubs];  // per chunk: inverted image of its smallest value above -infinity (0 if none)
     u64 mass[kBins];
     uint32_t count[kBins];
     uint32_t ncand;
@@ -250,9 +250,25 @@ __device__ __forceinline__ Row make_row(const SampleArgs& a, const Params& t, u6
     return q;
 }
 
-__device__ __forceinline__ float wave_min_f32(float v) {
-#pragma unroll
-    for (int o = kWave / 2; o >= 1; o >>= 1) v = fminf(v, __shfl_xor(v, o));
+__device__ __forceinline__ uint32_t umax32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = umax32(v, dpp_mov_u32<kDppRowShr1, 0xF>(v));
+    v = umax32(v, dpp_mov_u32<kDppRowShr2, 0xF>(v));
+    v = umax32(v, dpp_mov_u32<kDppRowShr4, 0xF>(v));
+    v = umax32(v, dpp_mov_u32<kDppRowShr8, 0xF>(v));
+    v = umax32(v, dpp_mov_u32<kDppRowBcast15, 0xA>(v));
+    v = umax32(v, dpp_mov_u32<kDppRowBcast31, 0xC>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
+}
+
+__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {   // inclusive sums
+    v += dpp_mov_u32<kDppRowShr1, 0xF>(v);
+    v += dpp_mov_u32<kDppRowShr2, 0xF>(v);
+    v += dpp_mov_u32<kDppRowShr4, 0xF>(v);
+    v += dpp_mov_u32<kDppRowShr8, 0xF>(v);
+    v += dpp_mov_u32<kDppRowBcast15, 0xA>(v);
+    v += dpp_mov_u32<kDppRowBcast31, 0xC>(v);
     return v;
 }
 
@@ -309,13 +325,14 @@ __device__ __forceinline__ u64 block_scan_u64(u64 v, u64* total) {
 // A row's extremes from its chunks (every wave by itself).
 __device__ __forceinline__ void row_extremes(const RowSpace* ws, int G, u64* top, float* low) {
     u64 t = 0;
-    float l = INFINITY;
+    uint32_t l = 0;
     for (int g = lane_id(); g < G; g += kWave) {
         t = umax64(t, ws->key[g]);
-        l = fminf(l, ws->low[g]);
+        l = umax32(l, ws->low[g]);
     }
     *top = wave_max_u64(t);
-    *low = wave_min_f32(l);
+    l = wave_max_u32(l);
+    *low = l ? key_value((u64)~l << 32) : INFINITY;
 }
 
 // ---- max ----------------------------------------------------------------------
@@ -328,8 +345,7 @@ k_sample_max(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs 
     const T* row = x + r * a.ld;
     const int64_t c0 = (int64_t)g * a.subs_per_chunk * a.sub;
     const int64_t c1 = c0 + (int64_t)a.subs_per_chunk * a.sub < a.C ? c0 + (int64_t)a.subs_per_chunk * a.sub : a.C;
-    uint32_t best = 0u, bidx = 0xFFFFFFFFu;
-    float low = INFINITY;
+    uint32_t best = 0u, bidx = 0xFFFFFFFFu, low = 0u;
     for (int64_t c = c0; c < c1; c += kSubMin) {
         Share<T> e;
         e.load(row, c, a.C, a.vec);
@@ -337,13 +353,13 @@ k_sample_max(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs 
         for (int i = 0; i < kPer; ++i) {   // a thread's elements in increasing order
             const uint32_t img = order_image(e.v[i]);
             if (img > best) { best = img; bidx = (uint32_t)(c + Share<T>::element(i, a.vec)); }
-            if (e.v[i] > -INFINITY) low = fminf(low, e.v[i]);
+            if (e.v[i] > -INFINITY) low = umax32(low, ~img);
         }
     }
     u64 key = wave_max_u64(pack_key(best, bidx));
-    low = wave_min_f32(low);
+    low = wave_max_u32(low);
     __shared__ u64 keys[kChunkThreads / kWave];
-    __shared__ float lows[kChunkThreads / kWave];
+    __shared__ uint32_t lows[kChunkThreads / kWave];
     if (lane_id() == 0) {
         keys[threadIdx.x / kWave] = key;
         lows[threadIdx.x / kWave] = low;
@@ -353,7 +369,7 @@ k_sample_max(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs 
 #pragma unroll
         for (int w = 1; w < kChunkThreads / kWave; ++w) {
             key = umax64(key, keys[w]);
-            low = fminf(low, lows[w]);
+            low = umax32(low, lows[w]);
         }
         ws->key[g] = key;
         ws->low[g] = low;
@@ -451,59 +467,64 @@ __device__ __forceinline__ Borders find_borders(const LaneBins& bins_of, const R
         const int lane = threadIdx.x;
         const u64(&mass)[kLaneBins] = bins_of.mass;
         const uint32_t(&count)[kLaneBins] = bins_of.count;
-        u64 m_in = 0;
-        uint32_t c_in = 0;
-#pragma unroll
-        for (int i = 0; i < kLaneBins; ++i) {
-            m_in += mass[i];
-            c_in += count[i];
-        }
-        const u64 m_to = wave_scan_u64(m_in), c_to = wave_scan_u64((u64)c_in);
-        const u64 m_all = lane_u64(m_to, kWave - 1), c_all = lane_u64(c_to, kWave - 1);
         Borders b;
-        b.total = m_all;
+        b.total = 0;
         b.kbin = kBins;
         b.krank = 0;
         b.kmass = 0;
-        u64 m_low = m_all, m_high = m_all;   // the mass that top-p is a share of, at least and at most
-        if (q.k && (u64)q.k < c_all) {
-            // the lane and the bin in which the count reaches k
-            u64 c = c_to - c_in, m = m_to - m_in;
-            int bin = kBins;
-            u64 rank = 0, above = 0, upto = 0;
-#pragma unroll
-            for (int i = 0; i < kLaneBins; ++i) {
-                if (bin == kBins && c < (u64)q.k && c + count[i] >= (u64)q.k) {
-                    bin = lane * kLaneBins + i;
-                    rank = (u64)q.k - c;
-                    above = m;
-                    upto = m + mass[i];
-                }
-                c += count[i];
-                m += mass[i];
-            }
-            const int src = __ffsll((unsigned long long)__ballot(bin != kBins)) - 1;   // exactly one lane
-            b.kbin = __builtin_amdgcn_readlane(bin, src);
-            b.krank = (uint32_t)lane_u64(rank, src);
-            b.kmass = lane_u64(above, src);
-            m_low = b.kmass;
-            m_high = lane_u64(upto, src);
-        }
         b.p0 = 1;
         b.p1 = 0;
         b.pmass = 0;
+        u64 m_in = 0, m_to = 0;
+        if (q.p < 1.0) {
+#pragma unroll
+            for (int i = 0; i < kLaneBins; ++i) m_in += mass[i];
+            m_to = wave_scan_u64(m_in);
+            b.total = lane_u64(m_to, kWave - 1);
+        }
+        u64 m_low = b.total, m_high = b.total;   // the mass that top-p is a share of, at least and at most
+        if (q.k) {
+            uint32_t c_in = 0;
+#pragma unroll
+            for (int i = 0; i < kLaneBins; ++i) c_in += count[i];
+            const uint32_t c_to = wave_scan_u32(c_in);
+            if ((uint32_t)q.k < (uint32_t)__builtin_amdgcn_readlane((int)c_to, kWave - 1)) {
+                // the lane and the bin in which the count reaches k
+                uint32_t c = c_to - c_in, rank = 0;
+                u64 m = m_to - m_in, above = 0, upto = 0;
+                int bin = kBins;
+#pragma unroll
+                for (int i = 0; i < kLaneBins; ++i) {
+                    if (c < (uint32_t)q.k && c + count[i] >= (uint32_t)q.k) {
+                        bin = lane * kLaneBins + i;
+                        rank = (uint32_t)q.k - c;
+                        above = m;
+                        upto = m + mass[i];
+                    }
+                    c += count[i];
+                    m += mass[i];
+                }
+                const int src = __ffsll((unsigned long long)__ballot(bin != kBins)) - 1;   // exactly one lane
+                b.kbin = __builtin_amdgcn_readlane(bin, src);
+                b.krank = (uint32_t)__builtin_amdgcn_readlane((int)rank, src);
+                if (q.p < 1.0) {
+                    b.kmass = lane_u64(above, src);
+                    m_low = b.kmass;
+                    m_high = lane_u64(upto, src);
+                }
+            }
+        }
         if (q.p < 1.0) {
             const u64 t[2] = {m_low ? p_target(q.p, m_low) : 1ull, p_target(q.p, m_high)};
             int bins[2];
             u64 aboves[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                u64 m = m_to - m_in;
+                u64 m = m_to - m_in, above = 0;
                 int bin = kBins;
-                u64 above = 0;
 #pragma unroll
                 for (int i = 0; i < kLaneBins; ++i) {
-                    if (bin == kBins && m < t[j] && m + mass[i] >= t[j]) {
+                    if (m < t[j] && m + mass[i] >= t[j]) {
                         bin = lane * kLaneBins + i;
                         above = m;
                     }
@@ -589,15 +610,28 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
         if (__any(any)) {   // few steps of a wave, where few tokens are kept
             double w[kPer];
             q.weights(e.v, w);
+            // the listed ones of the wave take consecutive places, element by element
+            u64 masks[kPer];
+            uint32_t listed = 0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const u64 W = q.fixed(w[i]);
-                if (part[i] == 1) {
-                    sum += w[i] >= q.min_p ? W : 0ull;
-                } else if (part[i] == 2 && W) {
-                    const uint32_t at = atomicAdd(&n_list, 1u);
-                    if (at < (uint32_t)kChunkList)
-                        list[at] = pack_key(order_image(e.v[i]), (uint32_t)(c + Share<T>::element(i, a.vec)));
+                sum += part[i] == 1 && w[i] >= q.min_p ? W : 0ull;
+                masks[i] = __ballot(part[i] == 2 && W != 0);
+                listed += (uint32_t)__popcll(masks[i]);
+            }
+            if (listed) {   // wave-uniform
+                uint32_t at = 0;
+                if (lane_id() == 0) at = atomicAdd(&n_list, listed);
+                at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const uint32_t place = at + __builtin_amdgcn_mbcnt_hi(
+                                                    (uint32_t)(masks[i] >> 32),
+                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)masks[i], 0u));
+                    if ((masks[i] >> lane_id()) & 1 && place < (uint32_t)kChunkList)
+                        list[place] = pack_key(order_image(e.v[i]), (uint32_t)(c + Share<T>::element(i, a.vec)));
+                    at += (uint32_t)__popcll(masks[i]);
                 }
             }
         }
@@ -754,6 +788,40 @@ __device__ __forceinline__ u64 select_key(PickShared& s, int n, const T* row, co
     return prefix;
 }
 
+// The element of c0..c1 at which the kept weight passes u times the kept total
+// (`before` is what is kept ahead of c0; whole: the range is the row and its
+// own sum the total).
+template <class T>
+__device__ __forceinline__ void find_element(const T* row, const Row& q, const SampleArgs& a, u64 threshold, int64_t c0,
+                                             int64_t c1, u64 before, u64 kept, bool whole, int64_t r) {
+    const int64_t per = (c1 - c0 + kPickThreads - 1) / kPickThreads;   // consecutive elements per thread
+    auto kept_weight = [&](int64_t c) -> u64 {
+        const float v = Logit<T>::load(row + c);
+        if (q.below(v) > q.far) return 0ull;
+        const double w = q.weight(v);
+        return w >= q.min_p && pack_key(order_image(v), (uint32_t)c) >= threshold ? q.fixed(w) : 0ull;
+    };
+    const int64_t a0 = c0 + per * threadIdx.x;
+    const int64_t a1 = a0 + per < c1 ? a0 + per : c1;
+    u64 mine = 0;
+    for (int64_t c = a0; c < a1; ++c) mine += kept_weight(c);
+    u64 all;
+    const u64 upto = block_scan_u64<kPickThreads>(mine, &all);
+    if (whole) kept = all;
+    u64 t = (u64)(q.u * (double)kept);
+    if (t >= kept) t = kept - 1;
+    if (before + upto > t && before + upto - mine <= t) {   // exactly one thread
+        u64 at = before + upto - mine;
+        for (int64_t c = a0; c < a1; ++c) {
+            at += kept_weight(c);
+            if (at > t) {
+                a.idx[r] = c;
+                break;
+            }
+        }
+    }
+}
+
 // Resolves a row whose border elements are in s.key[0..n) or in `row`, and
 // writes its token.  whole: the list is the whole row (nothing was summed).
 template <class T>
@@ -832,32 +900,7 @@ __device__ __forceinline__ void pick_token(PickShared& s, int n, bool from_row, 
         c0 = s.found * a.sub;
         c1 = c0 + a.sub < C ? c0 + a.sub : C;
     }
-    const int64_t per = (c1 - c0 + kPickThreads - 1) / kPickThreads;   // consecutive elements per thread
-    auto kept_weight = [&](int64_t c) -> u64 {
-        const float v = Logit<T>::load(row + c);
-        if (q.below(v) > q.far) return 0ull;
-        const double w = q.weight(v);
-        return w >= q.min_p && pack_key(order_image(v), (uint32_t)c) >= threshold ? q.fixed(w) : 0ull;
-    };
-    const int64_t a0 = c0 + per * threadIdx.x;
-    const int64_t a1 = a0 + per < c1 ? a0 + per : c1;
-    u64 mine = 0;
-    for (int64_t c = a0; c < a1; ++c) mine += kept_weight(c);
-    u64 all;
-    const u64 upto = block_scan_u64<kPickThreads>(mine, &all);
-    if (whole) kept = all;
-    u64 t = (u64)(q.u * (double)kept);
-    if (t >= kept) t = kept - 1;
-    if (before + upto > t && before + upto - mine <= t) {   // exactly one thread
-        u64 at = before + upto - mine;
-        for (int64_t c = a0; c < a1; ++c) {
-            at += kept_weight(c);
-            if (at > t) {
-                a.idx[r] = c;
-                break;
-            }
-        }
-    }
+    find_element<T>(row, q, a, threshold, c0, c1, before, kept, whole, r);
 }
 
 template <class T>
@@ -873,6 +916,61 @@ k_sample_pick(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
     const Borders b = ws->borders;
     if (q.known != -2) {   // workgroup-uniform
         if (threadIdx.x == 0) a.idx[r] = q.known;
+        return;
+    }
+    if (listed <= (uint32_t)kWave && a.nsub <= kWave) {
+        // A short list and few sub-chunks, one of each per lane: the first wave
+        // settles the borders by comparing every listed key with every other.
+        if (threadIdx.x < kWave) {
+            const int lane = threadIdx.x;
+            const int n = (int)listed;
+            const bool have = lane < n;
+            const u64 key = have ? first : 0ull;
+            const float v = key_value(key);
+            const double w = have ? q.weight(v) : 0.0;
+            const u64 W = have ? q.fixed(w) : 0ull;
+            const int bin = have ? q.bin(v) : kBins;
+            const u64 in_k = __ballot(have && bin == b.kbin);
+            const u64 in_p = __ballot(have && bin >= b.p0 && bin <= b.p1);
+            uint32_t ahead = 0;   // keys of kbin before this one
+            u64 mass = 0;         // mass of the keys of p0..p1 before this one
+            for (int j = 0; j < n; ++j) {
+                const u64 Wj = lane_u64(W, j);   // with every lane active: lane j's own comparison is false
+                const bool before = lane_u64(key, j) > key;
+                ahead += before && (in_k >> j & 1) ? 1u : 0u;
+                mass += before && (in_p >> j & 1) ? Wj : 0ull;
+            }
+            bool keep = have && (bin != b.kbin || ahead < b.krank);
+            if (q.p < 1.0) {
+                u64 total = b.total;
+                if (b.kbin < kBins) total = b.kmass + wave_sum_u64(keep && bin == b.kbin ? W : 0ull);
+                keep = keep && (in_p >> lane & 1) && b.pmass + mass < p_target(q.p, total);
+            }
+            // the smallest kept key (0, all of them, where nothing is listed)
+            const u64 threshold = n ? ~wave_max_u64(keep ? ~key : 0ull) : 0ull;
+            s.sum[lane] = sum;
+            if (keep && w >= q.min_p) atomicAdd(&s.sum[min(key_index(key) / (uint32_t)a.sub, (uint32_t)kWave - 1)], W);
+            // other lanes' additions, too: without the clobber the compiler reads
+            // back only in lanes that added something themselves
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            const u64 mine = s.sum[lane];
+            const u64 upto = wave_scan_u64(mine);
+            const u64 kept = lane_u64(upto, kWave - 1);
+            u64 t = (u64)(q.u * (double)kept);
+            if (t >= kept) t = kept - 1;
+            const u64 hit = __ballot(upto > t);   // the first sub-chunk to pass u
+            const int src = hit ? __ffsll((unsigned long long)hit) - 1 : 0;
+            if (lane == 0) {
+                s.prefix = threshold;
+                s.some_set = kept;
+                s.left = lane_u64(upto, src) - lane_u64(mine, src);
+                s.found = src;
+            }
+        }
+        __syncthreads();
+        const int64_t c0 = s.found * a.sub;
+        const int64_t c1 = c0 + a.sub < a.C ? c0 + a.sub : a.C;
+        find_element<T>(x + r * a.ld, q, a, s.prefix, c0, c1, s.left, s.some_set, false, r);
         return;
     }
     const bool from_row = listed > (uint32_t)kCand;
