@@ -63,6 +63,7 @@ struct Logit {
 };
 
 constexpr int kPer = 8;   // elements per thread of the chunk kernels: kChunkThreads of them fill a shortest sub-chunk
+constexpr int kTogether = 4;   // of them whose weights are computed side by side
 static_assert(kPer * kChunkThreads == kSubMin, "one load step per shortest sub-chunk");
 
 // This thread's kPer elements of the kSubMin from c0 on (those at C and past
@@ -132,26 +133,30 @@ struct Row {
     // w as a binary64 number in [0, 1]
     __device__ __forceinline__ double weight(float x) const {
         double w[1];
-        const float v[1] = {x};
-        weights(v, w);
+        weights(&x, w);
         return w[0];
     }
     // The weights of N elements, side by side so that their chains of dependent
     // operations overlap.  w = 2^t, t = (x - m) log2(e) / T; t = n + f with n an
     // integer and |f| <= 1/2, and 2^f by the polynomial of degree 10 that
     // interpolates it at the Chebyshev nodes of [-1/2, 1/2] (within 3.2e-16,
-    // and 1 at 0).  w = 0 where t is not a number; an infinite m, which cannot
-    // be subtracted, is the largest binary64 number instead.
+    // and 1 at 0).  n is the low word of t + 1.5 2^52 and goes into the exponent
+    // by an integer addition: every operation but the first is a full-rate
+    // binary64 one.  t below -200, or not a number, counts as -200, far below
+    // any weight that counts; an infinite m, which cannot be subtracted, is the
+    // largest binary64 number instead.
     template <int N>
-    __device__ __forceinline__ void weights(const float (&x)[N], double (&w)[N]) const {
-        constexpr double kLargest = 1.7976931348623157e308;
+    __device__ __forceinline__ void weights(const float* x, double (&w)[N]) const {
+        constexpr double kLargest = 1.7976931348623157e308, kRound = 6755399441055744.0;
         const double top = fmin((double)m, kLargest);
-        double n[N], f[N];
+        double f[N];
+        uint32_t n[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const double t = fmax((fmin((double)x[i], kLargest) - top) * c, -1100.0);
-            n[i] = rint(t);
-            f[i] = t - n[i];
+            const double t = fmax((fmin((double)x[i], kLargest) - top) * c, -200.0);
+            const double z = t + kRound;
+            n[i] = (uint32_t)__builtin_bit_cast(u64, z);
+            f[i] = t - (z - kRound);
             w[i] = 7.072585949269223e-09;
         }
 #define DG_TERM(C)                                          \
@@ -168,15 +173,24 @@ struct Row {
         DG_TERM(1.0)
 #undef DG_TERM
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = ldexp(w[i], (int)n[i]);
+        for (int i = 0; i < N; ++i) {
+            const u64 v = __builtin_bit_cast(u64, w[i]);
+            w[i] = __builtin_bit_cast(double, (u64)((uint32_t)(v >> 32) + (n[i] << 20)) << 32 | (uint32_t)v);
+            // bound here, or the compiler moves each chain into the branch of its
+            // first use, one after the other (gather, 256 rows: 97 us against 52)
+            if constexpr (N > 1) asm volatile("" : "+v"(w[i]));
+        }
     }
     // round(2^F w) by the binary64 addition 2^52 + 2^F w (F <= 51)
     __device__ __forceinline__ u64 fixed(double w) const {
         const double v = fma(w, (double)(1ull << F), 4503599627370496.0);
         return __builtin_bit_cast(u64, v) & 0x000FFFFFFFFFFFFFull;
     }
-    // m - x, 0 also where both are infinite
-    __device__ __forceinline__ float below(float x) const { return x == m ? 0.0f : fminf(m - x, 3.4028234e38f); }
+    // m - x with infinities as the largest number: 0 where both are infinite
+    __device__ __forceinline__ float below(float x) const {
+        constexpr float kLargest = 3.4028234663852886e38f;
+        return fminf(fminf(m, kLargest) - fminf(x, kLargest), kLargest);
+    }
     // its step, larger for smaller x; equal values share a bin
     __device__ __forceinline__ int bin(float x) const { return bin_of(below(x)); }
     __device__ __forceinline__ int bin_of(float d) const { return (int)fminf(d * scale, (float)(kBins - 1)); }
@@ -413,18 +427,21 @@ k_sample_hist(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
     for (int64_t c = c0; c < c1; c += kSubMin) {
         const Share<T> e = ahead;
         if (c + kSubMin < c1) ahead.load(row, c + kSubMin, a.C, a.vec);
-        double w[kPer];
-        if (by_mass) q.weights(e.v, w);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float v = e.v[i];
-            if (v > -INFINITY) {
-                const int b = q.bin(v);
-                if (by_mass) {
-                    const u64 W = q.fixed(w[i]);
-                    if (W) atomicAdd(&mass[b], W);
+        for (int h = 0; h < kPer; h += kTogether) {
+            double w[kTogether];
+            if (by_mass) q.weights(e.v + h, w);
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i) {
+                const float v = e.v[h + i];
+                if (v > -INFINITY) {
+                    const int b = q.bin(v);
+                    if (by_mass) {
+                        const u64 W = q.fixed(w[i]);
+                        if (W) atomicAdd(&mass[b], W);
+                    }
+                    if (by_count) atomicAdd(&count[b], 1u);
                 }
-                if (by_count) atomicAdd(&count[b], 1u);
             }
         }
     }
@@ -560,7 +577,7 @@ __device__ __forceinline__ Borders no_borders() {
 template <class T>
 __global__ void __launch_bounds__(kChunkThreads)
 k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs a) {
-    __shared__ u64 list[kChunkList];
+    __shared__ uint32_t list[kChunkList];   // offsets from the chunk's first element
     __shared__ u64 sums[kMaxSubs];   // of the chunk's sub-chunks
     __shared__ uint32_t n_list, base;
     const int g = blockIdx.x;
@@ -587,7 +604,11 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
         ws->borders = b;
     }
     if (!drawn) return;   // workgroup-uniform
-    const bool listing = b.kbin < kBins || b.p0 <= b.p1;
+    // border bins lie in sure .. last (p1 <= kbin)
+    const bool borders = b.kbin < kBins || b.p0 <= b.p1;
+    const int last = b.kbin < kBins ? b.kbin : b.p1;
+    const uint32_t span = (uint32_t)(last - b.sure);   // without borders the listed bits are not used
+    const bool sift = (b.p0 <= b.p1 && b.kbin < kBins && b.kbin > b.p1 + 1) || last == kBins - 1;
     if (threadIdx.x == 0) n_list = 0;
     for (int i = threadIdx.x; i < subs; i += kChunkThreads) sums[i] = 0;
     __syncthreads();
@@ -597,43 +618,41 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
     for (int64_t c = c0; c < c1; c += kSubMin) {
         const Share<T> e = ahead;
         if (c + kSubMin < c1) ahead.load(row, c + kSubMin, a.C, a.vec);
-        // 0: no part in the sums or the list; 1: kept for sure unless min-p drops it; 2: listed
-        int part[kPer];
-        bool any = false;
+        uint32_t listed = 0;   // of this thread's elements, a bit each
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float d = q.below(e.v[i]);
-            const int bin = q.bin_of(d);
-            part[i] = bin < b.sure ? (d <= q.far ? 1 : 0) : (listing && border_bin(b, bin) ? 2 : 0);
-            any |= part[i] != 0;
+        for (int h = 0; h < kPer; h += kTogether) {
+            bool whole[kTogether], some = false;   // kept for sure unless min-p drops it
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i) {
+                const float d = q.below(e.v[h + i]);
+                const int bin = q.bin_of(d);
+                whole[i] = bin < b.sure && d <= q.far;
+                some |= whole[i];
+                listed |= (uint32_t)(bin - b.sure) <= span ? 1u << (h + i) : 0u;
+            }
+            if (!__any(some)) continue;   // most steps of a wave, where few tokens are kept
+            double w[kTogether];
+            q.weights(e.v + h, w);
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i) sum += whole[i] && w[i] >= q.min_p ? q.fixed(w[i]) : 0ull;
         }
-        if (__any(any)) {   // few steps of a wave, where few tokens are kept
-            double w[kPer];
-            q.weights(e.v, w);
-            // the listed ones of the wave take consecutive places, element by element
-            u64 masks[kPer];
-            uint32_t listed = 0;
+        if (borders && __any(listed != 0)) {
+            if (sift) {   // bins between top-p's and top-k's, or elements without weight
+                uint32_t kept = 0;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const u64 W = q.fixed(w[i]);
-                sum += part[i] == 1 && w[i] >= q.min_p ? W : 0ull;
-                masks[i] = __ballot(part[i] == 2 && W != 0);
-                listed += (uint32_t)__popcll(masks[i]);
+                for (int i = 0; i < kPer; ++i)
+                    if ((listed >> i & 1) && border_bin(b, q.bin(e.v[i])) && q.fixed(q.weight(e.v[i]))) kept |= 1u << i;
+                listed = kept;
             }
-            if (listed) {   // wave-uniform
-                uint32_t at = 0;
-                if (lane_id() == 0) at = atomicAdd(&n_list, listed);
-                at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const uint32_t place = at + __builtin_amdgcn_mbcnt_hi(
-                                                    (uint32_t)(masks[i] >> 32),
-                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)masks[i], 0u));
-                    if ((masks[i] >> lane_id()) & 1 && place < (uint32_t)kChunkList)
-                        list[place] = pack_key(order_image(e.v[i]), (uint32_t)(c + Share<T>::element(i, a.vec)));
-                    at += (uint32_t)__popcll(masks[i]);
-                }
-            }
+            // places in the list: the wave's from one atomic, a lane's after those of the lanes before it
+            const uint32_t mine = (uint32_t)__popc(listed);
+            const uint32_t upto = wave_scan_u32(mine);
+            uint32_t at = 0;
+            if (lane_id() == kWave - 1) at = atomicAdd(&n_list, upto);
+            at = (uint32_t)__builtin_amdgcn_readlane((int)at, kWave - 1) + upto - mine;
+            for (; listed; listed &= listed - 1, ++at)
+                if (at < (uint32_t)kChunkList)
+                    list[at] = (uint32_t)(c - c0) + (uint32_t)Share<T>::element(__ffs((int)listed) - 1, a.vec);
         }
         if (++step == steps || c + kSubMin >= c1) {
             sum = wave_sum_u64(sum);
@@ -645,15 +664,17 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
     }
     __syncthreads();
     for (int i = threadIdx.x; i < subs; i += kChunkThreads) ws->sum[s0 + i] = sums[i];
-    if (!listing) return;   // workgroup-uniform
+    if (!borders) return;   // workgroup-uniform
     __syncthreads();
     // more than kChunkList here, or kCand in all: the pick reads the row
     if (threadIdx.x == 0)
         base = n_list ? atomicAdd(&ws->ncand, n_list <= (uint32_t)kChunkList ? n_list : (uint32_t)kCand + 1u) : 0u;
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < n_list && i < (uint32_t)kChunkList && base + i < (uint32_t)kCand;
-         i += kChunkThreads)
-        ws->cand[base + i] = list[i];
+         i += kChunkThreads) {
+        const int64_t c = c0 + list[i];
+        ws->cand[base + i] = pack_key(order_image(Logit<T>::load(row + c)), (uint32_t)c);
+    }
 }
 
 // ---- pick ---------------------------------------------------------------------
