@@ -177,7 +177,8 @@ struct Row {
             const u64 v = __builtin_bit_cast(u64, w[i]);
             w[i] = __builtin_bit_cast(double, (u64)((uint32_t)(v >> 32) + (n[i] << 20)) << 32 | (uint32_t)v);
             // bound here, or the compiler moves each chain into the branch of its
-            // first use, one after the other (gather, 256 rows: 97 us against 52)
+            // first use, one after the other (the gather of 256 rows of 128000:
+            // 97 us against 81)
             if constexpr (N > 1) asm volatile("" : "+v"(w[i]));
         }
     }
@@ -680,15 +681,20 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
 // ---- pick ---------------------------------------------------------------------
 struct PickShared {
     u64 key[kCand];
+    u64 W[kCand];        // the keys' weights
     u64 mass[256];
     uint32_t count[256];
     u64 sum[kMaxSubs];
     u64 prefix, left, some_set, some_clear, found_key;
     uint32_t hits;
     int64_t found;
+    __device__ __forceinline__ void put(int i, u64 k, const Row& q) {
+        key[i] = k;
+        W[i] = q.fixed(q.weight(key_value(k)));
+    }
 };
 
-// Calls f(key, w, W) for this thread's share of the border elements: those of
+// Calls f(key, W) for this thread's share of the border elements: those of
 // the list in LDS, or (row != nullptr) those of the row that lie in a border
 // bin.
 template <class T, class Fn>
@@ -697,16 +703,11 @@ __device__ __forceinline__ void each_listed(const PickShared& s, int n, const T*
     if (row) {
         for (int64_t c = threadIdx.x; c < C; c += kPickThreads) {
             const float v = Logit<T>::load(row + c);
-            const double w = q.weight(v);
-            const u64 W = q.fixed(w);
-            if (W && border_bin(b, q.bin(v))) f(pack_key(order_image(v), (uint32_t)c), w, W);
+            const u64 W = q.fixed(q.weight(v));
+            if (W && border_bin(b, q.bin(v))) f(pack_key(order_image(v), (uint32_t)c), W);
         }
     } else {
-        for (int i = threadIdx.x; i < n; i += kPickThreads) {
-            const u64 key = s.key[i];
-            const double w = q.weight(key_value(key));
-            f(key, w, q.fixed(w));
-        }
+        for (int i = threadIdx.x; i < n; i += kPickThreads) f(s.key[i], s.W[i]);
     }
 }
 
@@ -722,7 +723,7 @@ __device__ __forceinline__ u64 select_key(PickShared& s, int n, const T* row, co
     if (threadIdx.x == 0) s.some_set = s.some_clear = 0;
     __syncthreads();
     u64 set = 0, clear = 0;
-    each_listed(s, n, row, q, b, C, [&](u64 key, double, u64) {
+    each_listed(s, n, row, q, b, C, [&](u64 key, u64) {
         if (take(key)) {
             set |= key;
             clear |= ~key;
@@ -749,7 +750,7 @@ __device__ __forceinline__ u64 select_key(PickShared& s, int n, const T* row, co
             s.count[threadIdx.x] = 0;
         }
         __syncthreads();
-        each_listed(s, n, row, q, b, C, [&](u64 key, double, u64 W) {
+        each_listed(s, n, row, q, b, C, [&](u64 key, u64 W) {
             if (take(key) && (key & mask) == prefix) {
                 const int d = (int)((key >> next) & 255u) & ((1 << bits) - 1);
                 if (BY_MASS) atomicAdd(&s.mass[d], W);
@@ -799,7 +800,7 @@ __device__ __forceinline__ u64 select_key(PickShared& s, int n, const T* row, co
         shift = next;
         if (hits == 1 && shift > 0) {   // one key has this prefix: the rest of its bits
             const u64 found = ~0ull << shift;
-            each_listed(s, n, row, q, b, C, [&](u64 key, double, u64) {
+            each_listed(s, n, row, q, b, C, [&](u64 key, u64) {
                 if (take(key) && (key & found) == prefix) s.found_key = key;
             });
             __syncthreads();
@@ -860,7 +861,7 @@ __device__ __forceinline__ void pick_token(PickShared& s, int n, bool from_row, 
         threshold = kkey;
         if (q.p < 1.0) {   // the mass that top-k keeps
             u64 part = 0;
-            each_listed(s, n, scan, q, b, C, [&](u64 key, double, u64 W) {
+            each_listed(s, n, scan, q, b, C, [&](u64 key, u64 W) {
                 if (in_kbin(key) && key >= kkey) part += W;
             });
             u64 all;
@@ -903,8 +904,7 @@ __device__ __forceinline__ void pick_token(PickShared& s, int n, bool from_row, 
         } else {
             for (int i = threadIdx.x; i < n; i += kPickThreads) {
                 const u64 key = s.key[i];
-                const double w = q.weight(key_value(key));
-                if (key >= threshold && w >= q.min_p) atomicAdd(&s.sum[min(key_index(key) / (uint32_t)a.sub, (uint32_t)kMaxSubs - 1)], q.fixed(w));
+                if (key >= threshold && q.weight(key_value(key)) >= q.min_p) atomicAdd(&s.sum[min(key_index(key) / (uint32_t)a.sub, (uint32_t)kMaxSubs - 1)], s.W[i]);
             }
         }
         __syncthreads();
@@ -996,10 +996,10 @@ k_sample_pick(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
     }
     const bool from_row = listed > (uint32_t)kCand;
     const int n = from_row ? 0 : (int)listed;
-    if ((int)threadIdx.x < n) s.key[threadIdx.x] = first;
-    for (int i = threadIdx.x + kPickThreads; i < n; i += kPickThreads) s.key[i] = ws->cand[i];
+    if ((int)threadIdx.x < n) s.put(threadIdx.x, first, q);
+    for (int i = threadIdx.x + kPickThreads; i < n; i += kPickThreads) s.put(i, ws->cand[i], q);
     s.sum[threadIdx.x] = sum;
-    if (threadIdx.x == 0) s.found = 0;
+    if (threadIdx.x == 0) s.found = s.left = 0;
     __syncthreads();
     pick_token<T>(s, n, from_row, x + r * a.ld, q, b, a, false, r);
 }
@@ -1038,7 +1038,10 @@ k_sample_row(const T* __restrict__ x, SampleArgs a) {
         b.p0 = 0;
         b.p1 = 0;
         u64 mass = 0;
-        for (int c = threadIdx.x; c < a.C; c += kPickThreads) mass += q.fixed(q.weight(key_value(s.key[c])));
+        for (int c = threadIdx.x; c < a.C; c += kPickThreads) {   // this thread's own keys
+            s.put(c, s.key[c], q);
+            mass += s.W[c];
+        }
         block_scan_u64<kPickThreads>(mass, &b.total);
     }
     pick_token<T>(s, a.C, false, row, q, b, a, true, r);
