@@ -13,6 +13,10 @@
 // and an ulp of r moves the codes of activations next to a rounding border:
 // the Q8_1 bytes would depend on the launch.
 //
+// Every binary32 result that is rounded on to a 16-bit type is bound to a
+// register (bind_f32): the compiler would otherwise round some of the exact
+// sums and products once, straight to binary16 (v_fma_mixlo_f16).
+//
 // One workgroup per row, eight consecutive elements per thread and group (16
 // bytes of a 16-bit type, two 16-byte loads of binary32), so the four
 // neighbouring threads of a quad hold one 32-element Q8_1 block and its
@@ -169,14 +173,14 @@ k_rmsnorm(const typename E::raw* x, const typename E::raw* res, typename E::raw*
             float a[kGroup];
             load_group8<E>(rr, k0, K, vrow, a);
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) v[i] = E::widen(E::narrow(v[i] + a[i]));
+            for (int i = 0; i < kGroup; ++i) v[i] = E::widen(E::narrow(bind_f32(v[i] + a[i])));
         }
     };
     auto finish = [&](int k0, const float (&v)[kGroup], float r) {
         float y[kGroup], wv[kGroup];
         load_weights8(w, wdtype, k0, K, vw, wv);
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i) y[i] = (v[i] * r) * wv[i];
+        for (int i = 0; i < kGroup; ++i) y[i] = bind_f32((v[i] * r) * wv[i]);
         store_out<OUT>(out, row, ldy, K, k0, vy, y);
     };
 

@@ -164,6 +164,25 @@ def test_special_rows(dg, dev):
     assert (y[5] == y[5, 0]).all() and abs(float(y[5, 0]) - 2.0) < 1e-4
 
 
+@pytest.mark.parametrize("dtype,ydtype", [("f16", "f16"), ("f32", "f16"), ("bf16", "f16"), ("f16", "bf16")])
+def test_each_rounding_of_many_values(dg, dev, dtype, ydtype):
+    """About one value in 10^5 tells the binary32 product rounded to binary16 from the exact one rounded once, and so
+    for the sum x + res: two million values have some of both."""
+    import torch
+    M, K = 700, 2821
+    g = torch.Generator(device=dev).manual_seed(11)
+    x = (torch.randn(M, K, device=dev, generator=g) * 3).to(tdtype(dtype))
+    res = (torch.randn(M, K, device=dev, generator=g) * 0.01).to(tdtype(dtype))
+    w = 1 + 0.2 * torch.randn(K, device=dev, generator=g)
+    h = torch.zeros_like(x)
+    y = torch.zeros(M, K, dtype=tdtype(ydtype), device=dev)
+    dg.dg_rmsnorm(x, w, y, res=res, h=h, eps=EPS)
+    torch.cuda.synchronize()
+    href, y32, _ = reference(x.cpu(), res.cpu(), w.cpu())
+    assert torch.equal(h.cpu().float(), href.float())
+    assert torch.equal(y.cpu().float(), torch.from_numpy(y32).to(tdtype(ydtype)).float())
+
+
 def test_many_rows(dg, dev):
     import torch
     M, K = 70000, 64
