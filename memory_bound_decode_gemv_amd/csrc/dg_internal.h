@@ -45,6 +45,10 @@ inline void units_default_grid(int N, int M, int& grid, int& block) {
     grid = need < g ? need : g;
 }
 
+// Rows of one launch of a kernel with up to 1024 threads per row: a launch has
+// fewer than 2^32 threads.
+constexpr int64_t kMaxRowsPerLaunch = int64_t(1) << 21;
+
 // Device properties used to size grids and check launches; cached per device.
 int device_cu_count();
 size_t device_max_lds_per_block();

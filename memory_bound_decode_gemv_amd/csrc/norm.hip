@@ -234,15 +234,24 @@ hipError_t launch_norm_out(const RmsNorm& a, hipStream_t s) {
     if (aligned16(a.x) && aligned16(a.res) && aligned16(a.h) && a.ld * (int64_t)sizeof(raw) % 16 == 0) vec |= 1;
     if (aligned16(a.w)) vec |= 2;
     if (aligned16(a.out) && a.ldy * ysize % 16 == 0) vec |= 4;
-#define DG_NORM(GG)                                                                                                  \
-    hipLaunchKernelGGL((k_rmsnorm<E, OUT, GG>), dim3((unsigned)a.M), dim3(threads), 0, s, (const raw*)a.x,           \
-                       (const raw*)a.res, (raw*)a.h, a.w, a.wdtype, a.out, K, a.ld, a.ldy, a.eps, vec)
-    if (per <= 1) DG_NORM(1);
-    else if (per <= 2) DG_NORM(2);
-    else if (per <= kMaxGroups) DG_NORM(kMaxGroups);
-    else DG_NORM(0);
+    for (int64_t r0 = 0; r0 < a.M; r0 += kMaxRowsPerLaunch) {
+        const unsigned rows = (unsigned)(a.M - r0 < kMaxRowsPerLaunch ? a.M - r0 : kMaxRowsPerLaunch);
+        const raw* x = (const raw*)a.x + r0 * a.ld;
+        const raw* res = a.res ? (const raw*)a.res + r0 * a.ld : nullptr;
+        raw* h = a.h ? (raw*)a.h + r0 * a.ld : nullptr;
+        void* out = (uint8_t*)a.out + r0 * (OUT == kOutQ81 ? (int64_t)(K / 32) * 36 : a.ldy * ysize);
+#define DG_NORM(GG)                                                                                               \
+    hipLaunchKernelGGL((k_rmsnorm<E, OUT, GG>), dim3(rows), dim3(threads), 0, s, x, res, h, a.w, a.wdtype, out, K, \
+                       a.ld, a.ldy, a.eps, vec)
+        if (per <= 1) DG_NORM(1);
+        else if (per <= 2) DG_NORM(2);
+        else if (per <= kMaxGroups) DG_NORM(kMaxGroups);
+        else DG_NORM(0);
 #undef DG_NORM
-    return hipGetLastError();
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <class E>

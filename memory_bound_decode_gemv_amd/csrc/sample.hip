@@ -1080,8 +1080,14 @@ template <class T>
 hipError_t launch_sample(const SampleRows& p, hipStream_t s) {
     const T* x = (const T*)p.x;
     if (p.C <= kCand) {
-        hipLaunchKernelGGL((k_sample_row<T>), dim3((unsigned)p.R), dim3(kPickThreads), 0, s, x, plan_rows(p, 0, p.R));
-        return hipGetLastError();
+        for (int64_t r0 = 0; r0 < p.R; r0 += kMaxRowsPerLaunch) {
+            const int64_t rn = p.R - r0 < kMaxRowsPerLaunch ? p.R - r0 : kMaxRowsPerLaunch;
+            hipLaunchKernelGGL((k_sample_row<T>), dim3((unsigned)rn), dim3(kPickThreads), 0, s, x + r0 * p.ld,
+                               plan_rows(p, r0, rn));
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
     }
     RowSpace* ws = (RowSpace*)p.ws;
     for (int64_t r0 = 0; r0 < p.R; r0 += kBatchRows) {

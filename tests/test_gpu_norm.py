@@ -183,9 +183,9 @@ def test_each_rounding_of_many_values(dg, dev, dtype, ydtype):
     assert torch.equal(y.cpu().float(), torch.from_numpy(y32).to(tdtype(ydtype)).float())
 
 
-def test_many_rows(dg, dev):
+@pytest.mark.parametrize("M,K", [(70000, 64), ((1 << 21) + 3, 8)])   # the second in two launches
+def test_many_rows(dg, dev, M, K):
     import torch
-    M, K = 70000, 64
     x = torch.randn(M, K, device=dev, generator=torch.Generator(device=dev).manual_seed(5))
     w = torch.ones(K, device=dev)
     y = torch.zeros(M, K, device=dev)
@@ -193,6 +193,23 @@ def test_many_rows(dg, dev):
     torch.cuda.synchronize()
     _, y32, _ = reference(x.cpu(), None, w.cpu())
     assert np.array_equal(y.cpu().numpy(), y32)
+
+
+def test_many_rows_in_place_into_q8_1(dg, dev, orc):
+    import torch
+    M, K = (1 << 21) + 3, 32
+    g = torch.Generator(device=dev).manual_seed(6)
+    x = torch.randn(M, K, device=dev, generator=g).bfloat16()
+    res = torch.randn(M, K, device=dev, generator=g).bfloat16()
+    h0 = (x.float() + res.float()).bfloat16()
+    w = torch.ones(K, device=dev)
+    Xq = torch.zeros(M * 36, dtype=torch.uint8, device=dev)
+    dg.dg_rmsnorm_q8_1(x, w, Xq, res=res, h=res, eps=EPS)
+    torch.cuda.synchronize()
+    assert torch.equal(res, h0)
+    for at in (0, (1 << 21) - 2):   # the first rows, and those across the launches' border
+        _, y32, _ = reference(h0[at:at + 5].cpu(), None, w.cpu())
+        assert np.array_equal(Xq.view(M, 36)[at:at + 5].cpu().numpy(), orc.quantize_q8_1(y32))
 
 
 def test_empty(dg, dev):

@@ -217,6 +217,20 @@ def test_more_rows_than_a_workspace_holds_at_once(dg, dev):
           top_p=rng.uniform(0.5, 1.1, R), min_p=rng.uniform(-0.1, 0.1, R))
 
 
+def test_more_rows_than_a_launch_has(dg, dev):
+    import torch
+    R, C = (1 << 21) + 5, 3
+    g = torch.Generator(device=dev).manual_seed(4)
+    x = torch.randn(R, C, device=dev, generator=g)
+    u = torch.rand(R, device=dev, generator=g)
+    idx = torch.full((R,), -7, dtype=torch.int64, device=dev)
+    dg.dg_sample_rows(x, u, idx)
+    torch.cuda.synchronize()
+    w = torch.exp(x.double() - x.double().amax(1, keepdim=True))
+    cum = torch.cumsum(w, 1)
+    assert torch.equal(idx, (cum <= u.double().unsqueeze(1) * cum[:, -1:]).sum(1))
+
+
 def test_a_row_does_not_depend_on_its_batch(dg, dev):
     R, C = 40, 20011
     x = logits((1270, 1, 0, 0), R, C, "f16", 3.0)
