@@ -298,9 +298,265 @@ __device__ __forceinline__ void bind_group(u32x4 (&w)[L]) {
     else asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]), "+v"(w[4])::"memory");
 }
 
-// The tile's outputs, scaled: out[j][r] of column 16 j + ... as stored below.
-// The full tile adds its even- and odd-block sums; the pair tile's sit in lane
-// groups g and g + 2 (output rows m' and m' + 8).  All 64 lanes call this.
+// Stores the tile's outputs (unscaled).  The full tile adds its even- and
+// odd-block sums; the pair tile's sit in lane groups g and g + 2 (output rows
+// m' and m' + 8).  All 64 lanes of the wave call this.
+template <class TF, int MP>
+__device__ __forceinline__ void store_tile(const f32x4 (&acc)[TileSet<MP>::kNA], float* __restrict__ Y, int N, int M,
+                                           int t, int g, int rn) {
+    constexpr float kUnscale = TF::kUnscale;
+    using TS = TileSet<MP>;
+    const int n = t * 16 + rn;
+    f32x4 pr = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (TS::kPair) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) pr[r] = acc[TS::kPairAcc][r] + __shfl_xor(acc[TS::kPairAcc][r], 32);
+    }
+    if (n >= N) return;
+    if constexpr (TS::kFull) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int m = g * 4 + r;
+            if (m < M) Y[(size_t)m * N + n] = (acc[0][r] + acc[1][r]) * kUnscale;
+        }
+    }
+    if constexpr (TS::kPair) {
+        if (g < 2) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int m = TS::kC0 + g * 4 + r;
+                if (m < M) Y[(size_t)m * N + n] = pr[r] * kUnscale;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The GEMV.  MP = 8 (M <= 8: one pair tile), 16 (one full tile) or 24 (a
+// full tile and a pair tile); columns past M re-read column M - 1, their
+// results dropped.
+// ---------------------------------------------------------------------------
+template <class TF, int MP, int RT, int KW, int D>
+__global__ void __launch_bounds__(64 * RT * KW)
+k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* __restrict__ Y,
+           uint32_t* __restrict__ tickets, f32x4* __restrict__ part, int N, int K, int M, int KP, int spw,
+           int cs_slots, uint32_t cs_magic, int CS, int groups, int pre) {
+    using TS = TileSet<MP>;
+    constexpr int NA = TS::kNA;
+    constexpr int W = RT * KW;
+    extern __shared__ u32x4 tiles_lds[];
+    __shared__ int last_ticket;
+    uint8_t* const lds = reinterpret_cast<uint8_t*>(tiles_lds);
+    const int lane = lane_id();
+    const int wave = wave_in_block();
+    const int rt = wave / KW, kw = wave - rt * KW;
+    const int g = lane >> 4, rn = lane & 15;
+    const int S = K >> 8;
+    const int nblk = K >> 5;
+    const int T = (N + 15) >> 4;
+    int grp, kp, cs = 0;
+    if (CS == 1) {
+        grp = (int)blockIdx.x / KP;
+        kp = (int)blockIdx.x - grp * KP;
+    } else {
+        // Column slices: the CS workgroups of a (row group, K range) unit take
+        // Mh = ceil(M / CS) columns each and sit 8 workgroup ids apart, so the
+        // round-robin placement puts them on one XCD, whose L2 serves their
+        // shared weight rows once.  Units are padded to whole blocks of 8.
+        const int b = (int)blockIdx.x;
+        const int hi = b >> 3;
+        cs = hi % CS;
+        const int u = (hi / CS) * 8 + (b & 7);
+        if (u >= groups * KP) return;   // workgroup-uniform, before any barrier
+        grp = u / KP;
+        kp = u - grp * KP;
+        const int Mh = (M + CS - 1) / CS;
+        const int mc0 = cs * Mh;
+        Xq += (size_t)mc0 * (size_t)(K >> 5) * kQ81Bytes;
+        Y += (size_t)mc0 * (size_t)N;
+        M = min(Mh, M - mc0);
+    }
+    const int s0 = kp * spw;                       // first group of the workgroup's range
+    const int ns = min(spw, S - s0);               // groups in the range (>= 1)
+    const int spk = (ns + KW - 1) / KW;
+    const int w0 = kw * spk;                       // the wave's part: groups w0 .. w0 + cnt - 1 of the range
+    const int cnt = max(0, min(spk, ns - w0));     // wave-uniform
+    const int t = grp * RT + rt;
+    const int tc = t < T ? t : T - 1;
+    constexpr int kGroupBytes = TF::kGroupBytes;
+    constexpr int L = TF::kCodeLoads + 1;   // 16-byte loads per lane and group
+    const uint8_t* const wbase = Wt + ((size_t)tc * S + s0 + (cnt > 0 ? w0 : 0)) * kGroupBytes;
+    const int last = cnt > 0 ? cnt - 1 : 0;
+
+    // (1) the activation columns of the range, copied into LDS by DMA, and a
+    // wait for them; then (2) the first D groups of this wave's weights (past
+    // its part: its last group again, never used).  The wait is the builtin
+    // (not inline asm) and waits for everything: only then does the
+    // compiler's own wait counting know that no copy into LDS is outstanding.
+    // With copies possibly outstanding it treats the counter as out of order
+    // and waits for every load before each use (measured: vmcnt(0) at the top
+    // of every round of the loop).  Waiting for the copies before the first
+    // weight loads leaves those loads to the compiler's exact counting, so the
+    // first group's products start when that group has arrived; with the
+    // weights issued before the wait (pre = 0, kept for measurements) they
+    // start when all D have.  Measured 2-16% faster on most shapes.
+    {
+        const int used = ns * kGroupSlots;
+        const int copies = (M * cs_slots + kWave - 1) / kWave;
+        const uint8_t* const xr = Xq + (size_t)s0 * kGroupBlocks * kQ81Bytes;
+        for (int j = wave; j < copies; j += W) {
+            const uint32_t q = (uint32_t)(j * kWave + lane);
+            const uint32_t m = __umulhi(q, cs_magic);          // q / cs_slots
+            const uint32_t c = q - m * (uint32_t)cs_slots;
+            const bool ok = m < (uint32_t)M && c < (uint32_t)used;
+            const uint8_t* src = xr + (ok ? (size_t)m * nblk * kQ81Bytes + (size_t)c * 16 : 0);
+            __builtin_amdgcn_global_load_lds(src, (lds_void_t*)(lds + j * 1024), 16, 0, 0);
+        }
+        if constexpr (TS::kPair) {   // the zero column after the copies (its used slots)
+            u32x4* const z = reinterpret_cast<u32x4*>(lds + copies * 1024);
+            for (int e = wave * kWave + lane; e < used; e += W * kWave) z[e] = u32x4{0u, 0u, 0u, 0u};
+        }
+    }
+    u32x4 wb[D][L];
+    if (pre) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the copies only
+        lds_barrier();                        // every other wave's copies have landed too
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            load_group<TF>(wbase + (size_t)(d < cnt ? d : last) * kGroupBytes, lane, rn, wb[d]);
+    } else {
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            load_group<TF>(wbase + (size_t)(d < cnt ? d : last) * kGroupBytes, lane, rn, wb[d]);
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0); expcnt, lgkmcnt at their maximum: no wait
+        lds_barrier();   // every other wave's copies have landed too
+    }
+
+    // A operand offsets (columns past M: column M - 1 again, results dropped)
+    ALanes al;
+    {
+        const uint32_t stride = (uint32_t)cs_slots * 16u;
+        const uint32_t zero = (uint32_t)((M * cs_slots + kWave - 1) / kWave) * 1024u;   // the zero column
+        al.full = (uint32_t)(rn < M ? rn : M - 1) * stride;
+        const int c = TS::kC0 + (rn & 7);
+        const uint32_t pc = (uint32_t)(c < M ? c : M - 1) * stride;
+        const bool hi = rn >= 8;
+        al.p01 = hi ? zero : pc;
+        al.p23 = hi ? pc : zero;
+        al.ps = pc + (hi ? (uint32_t)kQ81Bytes : 0u);
+        al.sel = hi ? 0x01000C0Cu : 0x0C0C0100u;
+    }
+    f32x4 acc[NA];
+#pragma unroll
+    for (int a = 0; a < NA; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // D groups per round; the loads of the next round are issued right after
+    // each group's products, with no branch between them, so the compiler's
+    // waits count exactly the D - 1 groups still in flight.  The last round
+    // is peeled (no loads).
+    const int rounds = (cnt + D - 1) / D;
+    for (int rd = 0; rd + 1 < rounds; ++rd) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int i = rd * D + d;
+            tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(w0 + i) * kGroupBlocks, g, acc);
+            const int nx = i + D;
+            load_group<TF>(wbase + (size_t)(nx < cnt ? nx : last) * kGroupBytes, lane, rn, wb[d]);
+            // Keep the loads here and the next group's arithmetic behind them:
+            // binding that group's registers ("bind values, not memory", the
+            // third finding of "The kernel that waited for itself") stops the
+            // scheduler from interleaving the groups, which made it wait for
+            // every group in flight at the top of each round.
+            bind_group(wb[(d + 1) % D]);
+        }
+    }
+    if (rounds > 0) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int i = (rounds - 1) * D + d;
+            if (d > 0) bind_group(wb[d]);
+            if (i < cnt)   // wave-uniform; no loads follow, so the branch costs no wait
+                tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(w0 + i) * kGroupBlocks, g, acc);
+        }
+    }
+
+    // the KW parts of each tile, added in the order 0..KW-1
+    if constexpr (KW > 1) {
+        lds_barrier();   // every wave is done with the activation copies
+        f32x4* red = reinterpret_cast<f32x4*>(lds);
+        if (kw > 0) {
+#pragma unroll
+            for (int a = 0; a < NA; ++a) red[(wave * NA + a) * kWave + lane] = acc[a];
+        }
+        lds_barrier();
+        if (kw == 0) {
+            for (int k2 = 1; k2 < KW; ++k2)
+#pragma unroll
+                for (int a = 0; a < NA; ++a) {
+                    const f32x4 v = red[((wave + k2) * NA + a) * kWave + lane];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[a][r] += v[r];
+                }
+        }
+    }
+    if (KP == 1) {
+        if (kw == 0 && t < T) store_tile<TF, MP>(acc, Y, N, M, t, g, rn);
+        return;
+    }
+
+    // KP ranges: partial tile sums to the workspace, then a ticket.  Every
+    // access to the workspace is an agent-scope atomic (device-coherent loads
+    // and stores, sc1 on gfx950), and each wave waits for its stores to
+    // complete before the workgroup takes its ticket; the workgroup that draws
+    // the last ticket issues its loads only after the ticket has returned.
+    // Agent-scope release and acquire fences (an L2 write-back and an L2
+    // invalidate on this chip, both of whole caches) measured 15-140 us per
+    // call, and are not needed when every shared access is atomic.
+    const int slot = grp * CS + cs;   // this slice's ticket counter and partial sums
+    float* const mine = reinterpret_cast<float*>(part + (((size_t)slot * KP + kp) * RT + rt) * NA * kWave);
+    if (kw == 0) {
+#pragma unroll
+        for (int a = 0; a < NA; ++a)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                __hip_atomic_store(mine + (a * kWave + lane) * 4 + r, acc[a][r], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's partial sums are stored
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last_ticket = __hip_atomic_fetch_add(tickets + slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                      (uint32_t)(KP - 1);
+    __syncthreads();
+    if (!last_ticket) return;   // workgroup-uniform
+    if (kw == 0 && t < T) {
+        f32x4 sum[NA];
+        for (int k2 = 0; k2 < KP; ++k2) {
+            const float* const src =
+                reinterpret_cast<const float*>(part + (((size_t)slot * KP + k2) * RT + rt) * NA * kWave);
+#pragma unroll
+            for (int a = 0; a < NA; ++a) {
+                f32x4 v = acc[a];
+                if (k2 != kp) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[r] = __hip_atomic_load(src + (a * kWave + lane) * 4 + r, __ATOMIC_RELAXED,
+                                                 __HIP_MEMORY_SCOPE_AGENT);
+                }
+                if (k2 == 0) sum[a] = v;
+                else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sum[a][r] += v[r];
+                }
+            }
+        }
+        store_tile<TF, MP>(sum, Y, N, M, t, g, rn);
+    }
+    if (threadIdx.x == 0) __hip_atomic_store(tickets + slot, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The same outputs held for the gated product's epilogue (made by all 64
+// lanes).
 template <class TF, int MP>
 struct TileOut {
     using TS = TileSet<MP>;
@@ -349,128 +605,55 @@ struct TileOut {
 };
 
 // ---------------------------------------------------------------------------
-// The GEMV.  MP = 8 (M <= 8: one pair tile), 16 (one full tile) or 24 (a
-// full tile and a pair tile); columns past M re-read column M - 1, their
-// results dropped.  A gated product is one range of K per row group (KP = 1,
-// no workspace), in passes.
+// The gated product.  Wave (rt, kw) of RT x KW streams tile grp * RT/2 + rt/2 of
+// the gate (rt even) or up matrix; a workgroup has the whole K, in passes of
+// `spp` groups whose columns take the same LDS in turn, so that neither many
+// columns nor long rows need column slices or a K split.  Within a pass the
+// data flow is that of k_tiles.
 // ---------------------------------------------------------------------------
-template <class TF, int MP, int RT, int KW, int D, bool GLU>
-__device__ __forceinline__ void
-tiles_body(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* __restrict__ Y,
-           uint32_t* __restrict__ tickets, f32x4* __restrict__ part, int N, int K, int M, int KP, int spw,
-           int cs_slots, uint32_t cs_magic, int CS, int groups, int pre, GluArgs<GLU> glu_args) {
-    static_assert(!GLU || RT % 2 == 0, "gate and up tiles in pairs");
+template <class TF, int MP, int RT, int KW, int D>
+__global__ void __launch_bounds__(64 * RT * KW)
+k_glu_tiles(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ Wu, const uint8_t* __restrict__ Xq,
+            float* __restrict__ Y, int N, int K, int M, int act, int spp, int cs_slots, uint32_t cs_magic, int CS,
+            int groups) {
+    static_assert(RT % 2 == 0, "gate and up tiles in pairs");
     using TS = TileSet<MP>;
     constexpr int NA = TS::kNA;
     constexpr int W = RT * KW;
+    constexpr int kGroupBytes = TF::kGroupBytes;
+    constexpr int L = TF::kCodeLoads + 1;   // 16-byte loads per lane and group
     extern __shared__ u32x4 tiles_lds[];
     uint8_t* const lds = reinterpret_cast<uint8_t*>(tiles_lds);
     const int lane = lane_id();
     const int wave = wave_in_block();
     const int rt = wave / KW, kw = wave - rt * KW;
+    const bool up = rt & 1;                        // wave-uniform
     const int g = lane >> 4, rn = lane & 15;
     const int S = K >> 8;
     const int nblk = K >> 5;
     const int T = (N + 15) >> 4;
-    int grp, kp, cs = 0;
-    if (CS == 1) {
-        grp = (int)blockIdx.x / KP;
-        kp = (int)blockIdx.x - grp * KP;
-    } else {
-        // Column slices: the CS workgroups of a (row group, K range) unit take
-        // Mh = ceil(M / CS) columns each and sit 8 workgroup ids apart, so the
-        // round-robin placement puts them on one XCD, whose L2 serves their
-        // shared weight rows once.  Units are padded to whole blocks of 8.
+    int grp = (int)blockIdx.x;
+    if (CS > 1) {   // column slices, placed as in k_tiles
         const int b = (int)blockIdx.x;
-        const int hi = b >> 3;
-        cs = hi % CS;
-        const int u = (hi / CS) * 8 + (b & 7);
-        if (u >= groups * KP) return;   // workgroup-uniform, before any barrier
-        grp = u / KP;
-        kp = u - grp * KP;
+        const int cs = (b >> 3) % CS;
+        grp = (b >> 3) / CS * 8 + (b & 7);
+        if (grp >= groups) return;   // workgroup-uniform, before any barrier
         const int Mh = (M + CS - 1) / CS;
         const int mc0 = cs * Mh;
-        Xq += (size_t)mc0 * (size_t)(K >> 5) * kQ81Bytes;
+        Xq += (size_t)mc0 * (size_t)nblk * kQ81Bytes;
         Y += (size_t)mc0 * (size_t)N;
         M = min(Mh, M - mc0);
     }
-    const int s0 = kp * spw;                       // first group of the workgroup's range
-    const int ns = min(spw, S - s0);               // groups in the range (>= 1)
-    const int t = GLU ? grp * (RT / 2) + (rt >> 1) : grp * RT + rt;
+    const int t = grp * (RT / 2) + (rt >> 1);
     const int tc = t < T ? t : T - 1;
-    const bool up = GLU && (rt & 1);   // wave-uniform
-    if constexpr (GLU) Wt = up ? glu_args.Wu : Wt;
-    constexpr int kGroupBytes = TF::kGroupBytes;
-    constexpr int L = TF::kCodeLoads + 1;   // 16-byte loads per lane and group
-
-    f32x4 acc[NA];
-#pragma unroll
-    for (int a = 0; a < NA; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    // The range in one pass, or (GLU) in passes of glu_args.spp groups whose
-    // columns take the same LDS in turn.
-    int p0 = 0;   // the pass's first group within the range
-    do {
-    int np = ns;  // its groups
-    if constexpr (GLU) {
-        np = min(glu_args.spp, ns - p0);
-        if (p0 > 0) lds_barrier();   // every wave is done with the columns of the pass before
-    }
-    const int sp = s0 + p0;
-    const int spk = (np + KW - 1) / KW;
-    const int w0 = kw * spk;                       // the wave's part: groups w0 .. w0 + cnt - 1 of the pass
-    const int cnt = max(0, min(spk, np - w0));     // wave-uniform
-    const uint8_t* const wbase = Wt + ((size_t)tc * S + sp + (cnt > 0 ? w0 : 0)) * kGroupBytes;
-    const int last = cnt > 0 ? cnt - 1 : 0;
-    // (1) the activation columns of the range, copied into LDS by DMA, and a
-    // wait for them; then (2) the first D groups of this wave's weights (past
-    // its part: its last group again, never used).  The wait is the builtin
-    // (not inline asm) and waits for everything: only then does the
-    // compiler's own wait counting know that no copy into LDS is outstanding.
-    // With copies possibly outstanding it treats the counter as out of order
-    // and waits for every load before each use (measured: vmcnt(0) at the top
-    // of every round of the loop).  Waiting for the copies before the first
-    // weight loads leaves those loads to the compiler's exact counting, so the
-    // first group's products start when that group has arrived; with the
-    // weights issued before the wait (pre = 0, kept for measurements) they
-    // start when all D have.  Measured 2-16% faster on most shapes.
-    {
-        const int used = np * kGroupSlots;
-        const int copies = (M * cs_slots + kWave - 1) / kWave;
-        const uint8_t* const xr = Xq + (size_t)sp * kGroupBlocks * kQ81Bytes;
-        for (int j = wave; j < copies; j += W) {
-            const uint32_t q = (uint32_t)(j * kWave + lane);
-            const uint32_t m = __umulhi(q, cs_magic);          // q / cs_slots
-            const uint32_t c = q - m * (uint32_t)cs_slots;
-            const bool ok = m < (uint32_t)M && c < (uint32_t)used;
-            const uint8_t* src = xr + (ok ? (size_t)m * nblk * kQ81Bytes + (size_t)c * 16 : 0);
-            __builtin_amdgcn_global_load_lds(src, (lds_void_t*)(lds + j * 1024), 16, 0, 0);
-        }
-        if constexpr (TS::kPair) {   // the zero column after the copies (its used slots)
-            u32x4* const z = reinterpret_cast<u32x4*>(lds + copies * 1024);
-            for (int e = wave * kWave + lane; e < used; e += W * kWave) z[e] = u32x4{0u, 0u, 0u, 0u};
-        }
-    }
-    u32x4 wb[D][L];
-    if (pre) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the copies only
-        lds_barrier();                        // every other wave's copies have landed too
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-            load_group<TF>(wbase + (size_t)(d < cnt ? d : last) * kGroupBytes, lane, rn, wb[d]);
-    } else {
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-            load_group<TF>(wbase + (size_t)(d < cnt ? d : last) * kGroupBytes, lane, rn, wb[d]);
-        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0); expcnt, lgkmcnt at their maximum: no wait
-        lds_barrier();   // every other wave's copies have landed too
-    }
+    const uint8_t* const tile = (up ? Wu : Wg) + (size_t)tc * S * kGroupBytes;
+    const int copies = (M * cs_slots + kWave - 1) / kWave;   // 1 KiB copies of the columns of a pass
 
     // A operand offsets (columns past M: column M - 1 again, results dropped)
     ALanes al;
     {
         const uint32_t stride = (uint32_t)cs_slots * 16u;
-        const uint32_t zero = (uint32_t)((M * cs_slots + kWave - 1) / kWave) * 1024u;   // the zero column
+        const uint32_t zero = (uint32_t)copies * 1024u;   // the zero column
         al.full = (uint32_t)(rn < M ? rn : M - 1) * stride;
         const int c = TS::kC0 + (rn & 7);
         const uint32_t pc = (uint32_t)(c < M ? c : M - 1) * stride;
@@ -480,42 +663,66 @@ tiles_body(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float
         al.ps = pc + (hi ? (uint32_t)kQ81Bytes : 0u);
         al.sel = hi ? 0x01000C0Cu : 0x0C0C0100u;
     }
-    // D groups per round; the loads of the next round are issued right after
-    // each group's products, with no branch between them, so the compiler's
-    // waits count exactly the D - 1 groups still in flight.  The last round
-    // is peeled (no loads).
-    const int rounds = (cnt + D - 1) / D;
-    for (int rd = 0; rd + 1 < rounds; ++rd) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int i = rd * D + d;
-            tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(w0 + i) * kGroupBlocks, g, acc);
-            const int nx = i + D;
-            load_group<TF>(wbase + (size_t)(nx < cnt ? nx : last) * kGroupBytes, lane, rn, wb[d]);
-            // Keep the loads here and the next group's arithmetic behind them:
-            // binding that group's registers ("bind values, not memory", the
-            // third finding of "The kernel that waited for itself") stops the
-            // scheduler from interleaving the groups, which made it wait for
-            // every group in flight at the top of each round.
-            bind_group(wb[(d + 1) % D]);
-        }
+    if constexpr (TS::kPair) {   // the zero column behind the columns, for every pass
+        u32x4* const z = reinterpret_cast<u32x4*>(lds + copies * 1024);
+        for (int e = wave * kWave + lane; e < cs_slots; e += W * kWave) z[e] = u32x4{0u, 0u, 0u, 0u};
     }
-    if (rounds > 0) {
+    f32x4 acc[NA];
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int i = (rounds - 1) * D + d;
-            if (d > 0) bind_group(wb[d]);
-            if (i < cnt)   // wave-uniform; no loads follow, so the branch costs no wait
-                tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(w0 + i) * kGroupBlocks, g, acc);
-        }
-    }
-    if constexpr (GLU) p0 += glu_args.spp;
-    } while (GLU && p0 < ns);
+    for (int a = 0; a < NA; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // the KW parts of each tile, added in the order 0..KW-1
+    for (int p0 = 0; p0 < S; p0 += spp) {          // the pass's groups: p0 .. p0 + np - 1
+        const int np = min(spp, S - p0);
+        const int spk = (np + KW - 1) / KW;
+        const int w0 = kw * spk;                   // the wave's part: groups w0 .. w0 + cnt - 1 of the pass
+        const int cnt = max(0, min(spk, np - w0)); // wave-uniform
+        const uint8_t* const wbase = tile + (size_t)(p0 + (cnt > 0 ? w0 : 0)) * kGroupBytes;
+        const int last = cnt > 0 ? cnt - 1 : 0;
+        if (p0 > 0) lds_barrier();                 // every wave is done with the columns of the pass before
+        {
+            const int used = np * kGroupSlots;
+            const uint8_t* const xr = Xq + (size_t)p0 * kGroupBlocks * kQ81Bytes;
+            for (int j = wave; j < copies; j += W) {
+                const uint32_t q = (uint32_t)(j * kWave + lane);
+                const uint32_t m = __umulhi(q, cs_magic);          // q / cs_slots
+                const uint32_t c = q - m * (uint32_t)cs_slots;
+                const bool ok = m < (uint32_t)M && c < (uint32_t)used;
+                const uint8_t* src = xr + (ok ? (size_t)m * nblk * kQ81Bytes + (size_t)c * 16 : 0);
+                __builtin_amdgcn_global_load_lds(src, (lds_void_t*)(lds + j * 1024), 16, 0, 0);
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the copies only
+        lds_barrier();                        // every other wave's copies have landed too
+        u32x4 wb[D][L];
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            load_group<TF>(wbase + (size_t)(d < cnt ? d : last) * kGroupBytes, lane, rn, wb[d]);
+        const int rounds = (cnt + D - 1) / D;
+        for (int rd = 0; rd + 1 < rounds; ++rd) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                const int i = rd * D + d;
+                tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(w0 + i) * kGroupBlocks, g, acc);
+                const int nx = i + D;
+                load_group<TF>(wbase + (size_t)(nx < cnt ? nx : last) * kGroupBytes, lane, rn, wb[d]);
+                bind_group(wb[(d + 1) % D]);
+            }
+        }
+        if (rounds > 0) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                const int i = (rounds - 1) * D + d;
+                if (d > 0) bind_group(wb[d]);
+                if (i < cnt) tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(w0 + i) * kGroupBlocks, g, acc);
+            }
+        }
+    }
+
+    // the KW parts of each tile, added in the order 0..KW-1, then the up sums
+    // to the gate's wave
+    lds_barrier();   // every wave is done with the columns
+    f32x4* const red = reinterpret_cast<f32x4*>(lds);   // NA KiB per wave
     if constexpr (KW > 1) {
-        lds_barrier();   // every wave is done with the activation copies
-        f32x4* red = reinterpret_cast<f32x4*>(lds);
         if (kw > 0) {
 #pragma unroll
             for (int a = 0; a < NA; ++a) red[(wave * NA + a) * kWave + lane] = acc[a];
@@ -531,96 +738,19 @@ tiles_body(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float
                 }
         }
     }
-    if constexpr (GLU) {   // the up sums to the gate's wave, which stores the tile's outputs
-        f32x4* red = reinterpret_cast<f32x4*>(lds);   // a slot per wave; only a pair's waves use those of kw = 0
-        if constexpr (KW == 1) lds_barrier();         // every wave is done with the activation copies
-        if (kw == 0 && up) {
+    if (kw == 0 && up) {   // its own slot, which no wave reads before the barrier
 #pragma unroll
-            for (int a = 0; a < NA; ++a) red[(wave * NA + a) * kWave + lane] = acc[a];
-        }
-        lds_barrier();
-        if (kw == 0 && !up && t < T) {
-            f32x4 us[NA];
-#pragma unroll
-            for (int a = 0; a < NA; ++a) us[a] = red[((wave + KW) * NA + a) * kWave + lane];
-            TileOut<TF, MP> out(acc);
-            out.gate(glu_args.act, TileOut<TF, MP>(us));
-            out.store(Y, N, M, t, g, rn);
-        }
-        return;
+        for (int a = 0; a < NA; ++a) red[(wave * NA + a) * kWave + lane] = acc[a];
     }
-    if (KP == 1) {
-        if (kw == 0 && t < T) TileOut<TF, MP>(acc).store(Y, N, M, t, g, rn);
-        return;
+    lds_barrier();
+    if (kw == 0 && !up && t < T) {
+        f32x4 us[NA];
+#pragma unroll
+        for (int a = 0; a < NA; ++a) us[a] = red[((wave + KW) * NA + a) * kWave + lane];
+        TileOut<TF, MP> out(acc);
+        out.gate(act, TileOut<TF, MP>(us));
+        out.store(Y, N, M, t, g, rn);
     }
-
-    // KP ranges: partial tile sums to the workspace, then a ticket.  Every
-    // access to the workspace is an agent-scope atomic (device-coherent loads
-    // and stores, sc1 on gfx950), and each wave waits for its stores to
-    // complete before the workgroup takes its ticket; the workgroup that draws
-    // the last ticket issues its loads only after the ticket has returned.
-    // Agent-scope release and acquire fences (an L2 write-back and an L2
-    // invalidate on this chip, both of whole caches) measured 15-140 us per
-    // call, and are not needed when every shared access is atomic.
-    __shared__ int last_ticket;
-    const int slot = grp * CS + cs;   // this slice's ticket counter and partial sums
-    float* const mine = reinterpret_cast<float*>(part + (((size_t)slot * KP + kp) * RT + rt) * NA * kWave);
-    if (kw == 0) {
-#pragma unroll
-        for (int a = 0; a < NA; ++a)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                __hip_atomic_store(mine + (a * kWave + lane) * 4 + r, acc[a][r], __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's partial sums are stored
-    __syncthreads();
-    if (threadIdx.x == 0)
-        last_ticket = __hip_atomic_fetch_add(tickets + slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                      (uint32_t)(KP - 1);
-    __syncthreads();
-    if (!last_ticket) return;   // workgroup-uniform
-    if (kw == 0 && t < T) {
-        f32x4 sum[NA];
-        for (int k2 = 0; k2 < KP; ++k2) {
-            const float* const src =
-                reinterpret_cast<const float*>(part + (((size_t)slot * KP + k2) * RT + rt) * NA * kWave);
-#pragma unroll
-            for (int a = 0; a < NA; ++a) {
-                f32x4 v = acc[a];
-                if (k2 != kp) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[r] = __hip_atomic_load(src + (a * kWave + lane) * 4 + r, __ATOMIC_RELAXED,
-                                                 __HIP_MEMORY_SCOPE_AGENT);
-                }
-                if (k2 == 0) sum[a] = v;
-                else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) sum[a][r] += v[r];
-                }
-            }
-        }
-        TileOut<TF, MP>(sum).store(Y, N, M, t, g, rn);
-    }
-    if (threadIdx.x == 0) __hip_atomic_store(tickets + slot, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-template <class TF, int MP, int RT, int KW, int D>
-__global__ void __launch_bounds__(64 * RT * KW)
-k_tiles(const uint8_t* __restrict__ Wt, const uint8_t* __restrict__ Xq, float* __restrict__ Y,
-           uint32_t* __restrict__ tickets, f32x4* __restrict__ part, int N, int K, int M, int KP, int spw,
-           int cs_slots, uint32_t cs_magic, int CS, int groups, int pre) {
-    tiles_body<TF, MP, RT, KW, D, false>(Wt, Xq, Y, tickets, part, N, K, M, KP, spw, cs_slots, cs_magic, CS, groups,
-                                         pre, {});
-}
-
-template <class TF, int MP, int RT, int KW, int D>
-__global__ void __launch_bounds__(64 * RT * KW)
-k_glu_tiles(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ Xq, float* __restrict__ Y, int N, int K, int M,
-            int cs_slots, uint32_t cs_magic, int CS, int groups, GluArgs<true> glu_args) {
-    tiles_body<TF, MP, RT, KW, D, true>(Wg, Xq, Y, nullptr, nullptr, N, K, M, 1, K >> 8, cs_slots, cs_magic, CS,
-                                        groups, 1, glu_args);
 }
 
 // f32x4 accumulators per lane for M columns (TileSet<MP>::kNA).
@@ -876,11 +1006,11 @@ void glu_tiles_plan(bool q8, int N, int K, int M, GluPlan& p) {
 template <class TF, int MP, int RT, int KW, int D>
 hipError_t launch_glu_tiles_cfg(const GluPlan& p, const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M,
                                 hipStream_t s) {
-    const GluArgs<true> ga = {(const uint8_t*)w.up, w.act, p.spp};
     const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) + (uint64_t)p.cs_slots - 1) / (uint64_t)p.cs_slots);
     const int grid = p.CS == 1 ? p.groups : (p.groups + 7) / 8 * 8 * p.CS;
     hipLaunchKernelGGL((k_glu_tiles<TF, MP, RT, KW, D>), dim3(grid), dim3(64 * RT * KW), p.lds, s,
-                       (const uint8_t*)w.gate, (const uint8_t*)Xq, Y, N, K, M, p.cs_slots, magic, p.CS, p.groups, ga);
+                       (const uint8_t*)w.gate, (const uint8_t*)w.up, (const uint8_t*)Xq, Y, N, K, M, w.act, p.spp,
+                       p.cs_slots, magic, p.CS, p.groups);
     return hipGetLastError();
 }
 

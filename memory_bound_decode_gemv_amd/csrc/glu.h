@@ -20,7 +20,6 @@ template <>
 struct GluArgs<true> {
     const uint8_t* Wu;   // the up matrix, laid out like the gate's
     int act;             // DG_ACT_*
-    int spp = 0;         // tiled kernel: groups of K whose columns are in LDS at a time
 };
 
 __device__ __forceinline__ float glu_act(int act, float g) {
