@@ -36,6 +36,19 @@ __global__ void k_fill_zero_f32(float* __restrict__ y, int64_t n) {
     if (i < n) y[i] = 0.0f;
 }
 
+// In pieces of which a launch has threads enough (fewer than 2^32).
+hipError_t fill_zero_f32(float* y, int64_t n, dg_stream stream) {
+    constexpr int64_t kPiece = int64_t(1) << 30;
+    hipError_t e = hipSuccess;
+    for (int64_t i = 0; i < n && e == hipSuccess; i += kPiece) {
+        const int64_t part = n - i < kPiece ? n - i : kPiece;
+        hipLaunchKernelGGL(k_fill_zero_f32, dim3((unsigned)((part + 255) / 256)), dim3(256), 0, (hipStream_t)stream,
+                           y + i, part);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
 dg_status gemv_dense_checked(bool bf16, const void* W, const void* x, void* y, int64_t N, int64_t K,
                              int64_t ldw, const dg_launch* cfg, dg_stream stream) {
     if (N < 0 || N > kI32Max || K < 0 || K > kI32Max || K % 8 != 0 || ldw < K || ldw % 8 != 0)
@@ -60,10 +73,7 @@ dg_status gemv_quant_checked(bool q8, const void* Wq, const void* Xq, float* Y, 
     if (!aligned(Y, 4)) return DG_ERR_MISALIGNED;
     if (K > 0 && (!aligned(Wq, 16) || !aligned(Xq, 16))) return DG_ERR_MISALIGNED;
     if (K == 0) {   // empty sums: Y = 0
-        const int64_t n = N * (int64_t)M;
-        hipLaunchKernelGGL(k_fill_zero_f32, dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
-                           (hipStream_t)stream, Y, n);
-        return hip_status(hipGetLastError());
+        return hip_status(fill_zero_f32(Y, N * (int64_t)M, stream));
     }
     hipError_t e = q8 ? launch_gemv_q8_0(Wq, Xq, Y, (int)N, (int)K, M, cfg, (hipStream_t)stream)
                       : launch_gemv_q4_0(Wq, Xq, Y, (int)N, (int)K, M, cfg, (hipStream_t)stream);
@@ -81,10 +91,7 @@ dg_status gemv_tiles_checked(bool q8, const void* Wt, const void* Xq, float* Y, 
     if (!aligned(Y, 4)) return DG_ERR_MISALIGNED;
     if (K > 0 && (!aligned(Wt, 16) || !aligned(Xq, 16) || !aligned(ws, 16))) return DG_ERR_MISALIGNED;
     if (K == 0) {   // empty sums: Y = 0
-        const int64_t n = N * (int64_t)M;
-        hipLaunchKernelGGL(k_fill_zero_f32, dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
-                           (hipStream_t)stream, Y, n);
-        return hip_status(hipGetLastError());
+        return hip_status(fill_zero_f32(Y, N * (int64_t)M, stream));
     }
     size_t need = 0;
     if (!tiles_config(q8, (int)N, (int)K, M, cfg ? cfg->unroll : 0, &need)) return DG_ERR_ARG;
@@ -125,10 +132,7 @@ dg_status gemv_glu_checked(bool q8, bool tiles, const void* Wg, const void* Wu, 
     if (!aligned(Y, 4)) return DG_ERR_MISALIGNED;
     if (K > 0 && (!aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(Xq, 16))) return DG_ERR_MISALIGNED;
     if (K == 0) {   // empty sums: act(0) * 0 = 0
-        const int64_t n = N * (int64_t)M;
-        hipLaunchKernelGGL(k_fill_zero_f32, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, (hipStream_t)stream, Y,
-                           n);
-        return hip_status(hipGetLastError());
+        return hip_status(fill_zero_f32(Y, N * (int64_t)M, stream));
     }
     const GluMatrices w = {Wg, Wu, act};
     return hip_status(tiles ? launch_tiles_glu(q8, M, w, Xq, Y, (int)N, (int)K, (hipStream_t)stream)
@@ -332,10 +336,7 @@ dg_status dg_gemv_q4_0_f32_ex(const void* Wq, const float* x, float* Y, void* Xq
     if (!aligned(Y, 4)) return DG_ERR_MISALIGNED;
     if (K > 0 && (!aligned(Wq, 16) || !aligned(x, 16) || (Xq && !aligned(Xq, 16)))) return DG_ERR_MISALIGNED;
     if (K == 0) {   // empty sums: Y = 0 (there are no blocks to store)
-        const int64_t n = N * (int64_t)M;
-        hipLaunchKernelGGL(k_fill_zero_f32, dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
-                           (hipStream_t)stream, Y, n);
-        return hip_status(hipGetLastError());
+        return hip_status(fill_zero_f32(Y, N * (int64_t)M, stream));
     }
     hipError_t e = launch_gemv_q4_0_f32(Wq, x, Xq, Y, (int)N, (int)K, M, cfg, (hipStream_t)stream);
     if (e == hipErrorInvalidValue && cfg) return DG_ERR_ARG;

@@ -236,3 +236,14 @@ def test_empty(dg, dev):
     dg.dg_gemv_q8_0_tiles_glu(w, w, w, y, 4, 0, 3)
     torch.cuda.synchronize()
     assert (y == 0.0).all()
+
+
+def test_empty_sums_past_two_to_the_32(dg, dev):
+    """More outputs than one launch has threads."""
+    import torch
+    N, M = 1 << 28, 17
+    Y = torch.ones(M, N, dtype=torch.float32, device=dev)
+    none = torch.zeros(16, dtype=torch.uint8, device=dev)
+    dg.dg_gemv_q4_0_tiles_glu(none, none, none, Y, N, 0, M)
+    for m in range(M):
+        assert torch.count_nonzero(Y[m]).item() == 0
