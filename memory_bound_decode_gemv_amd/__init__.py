@@ -288,6 +288,15 @@ def _dtype_id(t, name):
     return _float_ids[t.dtype]
 
 
+def _rows(t, name, count):
+    """The rows of a tensor of one or two dimensions."""
+    if t.dim() == 2:
+        return t.shape[0]
+    if t.dim() != 1:
+        raise ValueError(f"{name} has {t.dim()} dimensions: pass {count} (and ld) or a view of one or two")
+    return 1
+
+
 def _stream_here(stream, dev):
     """The handle of `stream`, or of the current stream of device dev."""
     if stream is None:
@@ -649,11 +658,14 @@ def _rmsnorm(x, w, out, res, h, eps, M, K, ld, ldy, stream):
     dev = _here(x, "x")
     dtype, wdtype = _dtype_id(x, "x"), _dtype_id(w, "w")
     if M is None:
-        M = x.shape[0] if x.dim() == 2 else 1
+        M = _rows(x, "x", "M")
     if K is None:
         K = x.shape[-1]
-    if ld is None:
+    if ld is None:   # rows as x has them, so res and h have to have them so too
         ld = x.shape[-1]
+        for name, t in (("res", res), ("h", h)):
+            if t is not None and t.shape[-1] != ld:
+                raise ValueError(f"{name} has rows of {t.shape[-1]} elements, x of {ld}")
     M, K, ld = int(M), int(K), int(ld)
     live = M > 0 and K > 0
     span = ((M - 1) * ld + K) * x.element_size() if live and ld >= K else 0
@@ -812,7 +824,7 @@ def dg_sample_rows(x, u, idx, R=None, C=None, ld=None, temperature=None, top_k=N
     dev = _here(x, "x")
     dtype = _dtype_id(x, "x")
     if R is None:
-        R = x.shape[0] if x.dim() == 2 else 1
+        R = _rows(x, "x", "R")
     if C is None:
         C = x.shape[-1]
     if ld is None:

@@ -74,6 +74,10 @@ def test_binding_checks_operands():
     with pytest.raises(TypeError):
         dg._dtype_id(torch.zeros(4, dtype=torch.int32), "x")
     assert [dg._dtype_id(torch.zeros(1, dtype=d), "x") for d in (torch.float32, torch.float16, torch.bfloat16)] == [0, 1, 2]
+    assert dg._rows(t, "x", "M") == 4 and dg._rows(t[0], "x", "M") == 1
+    for odd in (t.view(2, 2, 64), t[0, 0]):   # rows of one matrix only: nothing past the first is left out in silence
+        with pytest.raises(ValueError, match="dimensions"):
+            dg._rows(odd, "x", "M")
     host = t.get_device()   # -1: the checks of one operand, without a device
     assert dg._arg("x", t, host, torch.float32, 4 * 64 * 4) == t.data_ptr()
     assert dg._arg("x", None, host, torch.float32, 1000) is None

@@ -220,3 +220,21 @@ def test_empty(dg, dev):
     dg.dg_rmsnorm(x, w, y, K=0)
     torch.cuda.synchronize()
     assert (y == 3.0).all()
+
+
+def test_operands_of_other_shapes_are_refused(dg, dev):
+    import torch
+    x = torch.ones(4, 64, device=dev)
+    y = torch.empty_like(x)
+    wide = torch.ones(4, 72, device=dev)
+    with pytest.raises(ValueError, match="rows of 72"):
+        dg.dg_rmsnorm(x, x[0], y, res=wide)
+    with pytest.raises(ValueError, match="rows of 72"):
+        dg.dg_rmsnorm(x, x[0], y, res=x, h=wide)
+    with pytest.raises(ValueError, match="3 dimensions"):
+        dg.dg_rmsnorm(x.view(2, 2, 64), x[0], y)
+    with pytest.raises(ValueError, match="3 dimensions"):
+        dg.dg_sample_rows(x.view(2, 2, 64), x[:, 0].contiguous(), torch.zeros(4, dtype=torch.int64, device=dev))
+    dg.dg_rmsnorm(wide, x[0], y, res=wide, K=64)   # rows of 72, 64 used
+    r = np.float32(1.0 / np.sqrt(4.0 + np.float64(np.float32(EPS))))   # h = 2 in every place
+    assert torch.equal(y.cpu(), torch.full((4, 64), float(np.float32(2.0) * r)))
