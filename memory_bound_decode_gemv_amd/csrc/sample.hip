@@ -287,6 +287,12 @@ __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {   // inclusive s
     return v;
 }
 
+constexpr int kQuadXor1 = 0xB1;         // DPP quad_perm [1,0,3,2]
+constexpr int kQuadXor2 = 0x4E;         // DPP quad_perm [2,3,0,1]
+constexpr int kQuadXor3 = 0x1B;         // DPP quad_perm [3,2,1,0]
+constexpr int kHalfRowMirror = 0x141;   // DPP: lane ^ 7
+constexpr int kRowRotate8 = 0x128;      // DPP row_ror 8: lane ^ 8
+
 // Inclusive sums over the wave, on DPP moves (lanes without a source receive 0).
 __device__ __forceinline__ u64 wave_scan_u64(u64 v) {
     v += dpp_key<kDppRowShr1, 0xF>(v);
@@ -361,9 +367,11 @@ k_sample_max(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs 
     const int64_t c0 = (int64_t)g * a.subs_per_chunk * a.sub;
     const int64_t c1 = c0 + (int64_t)a.subs_per_chunk * a.sub < a.C ? c0 + (int64_t)a.subs_per_chunk * a.sub : a.C;
     uint32_t best = 0u, bidx = 0xFFFFFFFFu, low = 0u;
+    Share<T> ahead;
+    ahead.load(row, c0, a.C, a.vec);
     for (int64_t c = c0; c < c1; c += kSubMin) {
-        Share<T> e;
-        e.load(row, c, a.C, a.vec);
+        const Share<T> e = ahead;
+        if (c + kSubMin < c1) ahead.load(row, c + kSubMin, a.C, a.vec);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {   // a thread's elements in increasing order
             const uint32_t img = order_image(e.v[i]);
@@ -692,6 +700,10 @@ struct PickShared {
         key[i] = k;
         W[i] = q.fixed(q.weight(key_value(k)));
     }
+    // A kept key's weight to its sub-chunk.
+    __device__ __forceinline__ void keep(u64 k, u64 w, int sub_size) {
+        atomicAdd(&sum[min(key_index(k) / (uint32_t)sub_size, (uint32_t)kMaxSubs - 1)], w);
+    }
 };
 
 // Calls f(key, W) for this thread's share of the border elements: those of
@@ -844,6 +856,25 @@ __device__ __forceinline__ void find_element(const T* row, const Row& q, const S
     }
 }
 
+// The token, from the kept mass of every sub-chunk in s.sum.
+template <class T>
+__device__ __forceinline__ void draw_from_sums(PickShared& s, const T* row, const Row& q, const SampleArgs& a,
+                                               u64 threshold, int64_t r) {
+    u64 kept;
+    const u64 mine = (int)threadIdx.x < a.nsub ? s.sum[threadIdx.x] : 0ull;
+    const u64 upto = block_scan_u64<kPickThreads>(mine, &kept);
+    u64 t = (u64)(q.u * (double)kept);
+    if (t >= kept) t = kept - 1;
+    if (upto > t && upto - mine <= t) {   // exactly one thread
+        s.found = threadIdx.x;
+        s.left = upto - mine;
+    }
+    __syncthreads();
+    const int64_t c0 = s.found * a.sub;
+    const int64_t c1 = c0 + a.sub < a.C ? c0 + a.sub : a.C;
+    find_element<T>(row, q, a, threshold, c0, c1, s.left, kept, false, r);
+}
+
 // Resolves a row whose border elements are in s.key[0..n) or in `row`, and
 // writes its token.  whole: the list is the whole row (nothing was summed).
 template <class T>
@@ -880,48 +911,131 @@ __device__ __forceinline__ void pick_token(PickShared& s, int n, bool from_row, 
         if (pkey > threshold) threshold = pkey;
     }
 
-    // the part of the row that u falls into
-    u64 before = 0, kept = 0;   // kept mass before it; of the whole row
-    int64_t c0 = 0, c1 = C;
-    if (!whole) {
-        __syncthreads();
-        if (from_row) {
-            // a wave's 64 consecutive elements lie in one sub-chunk
-            for (int64_t base = (int64_t)(threadIdx.x / kWave) * kWave; base < C; base += kPickThreads) {
-                const int64_t c = base + lane_id();
-                u64 add = 0;
-                if (c < C) {
-                    const float v = Logit<T>::load(row + c);
-                    const double w = q.weight(v);
-                    const u64 W = q.fixed(w);
-                    if (W && w >= q.min_p && border_bin(b, q.bin(v)) && q.bin(v) >= b.sure &&
-                        pack_key(order_image(v), (uint32_t)c) >= threshold)
-                        add = W;
-                }
-                add = wave_sum_u64(add);
-                if (add && lane_id() == 0) atomicAdd(&s.sum[base / a.sub], add);
-            }
-        } else {
-            for (int i = threadIdx.x; i < n; i += kPickThreads) {
-                const u64 key = s.key[i];
-                if (key >= threshold && q.weight(key_value(key)) >= q.min_p) atomicAdd(&s.sum[min(key_index(key) / (uint32_t)a.sub, (uint32_t)kMaxSubs - 1)], s.W[i]);
-            }
-        }
-        __syncthreads();
-        const u64 mine = (int)threadIdx.x < a.nsub ? s.sum[threadIdx.x] : 0ull;
-        const u64 upto = block_scan_u64<kPickThreads>(mine, &kept);
-        u64 t = (u64)(q.u * (double)kept);
-        if (t >= kept) t = kept - 1;
-        if (upto > t && upto - mine <= t) {   // exactly one thread
-            s.found = threadIdx.x;
-            s.left = upto - mine;
-        }
-        __syncthreads();
-        before = s.left;
-        c0 = s.found * a.sub;
-        c1 = c0 + a.sub < C ? c0 + a.sub : C;
+    if (whole) {
+        find_element<T>(row, q, a, threshold, 0, C, 0, 0, true, r);
+        return;
     }
-    find_element<T>(row, q, a, threshold, c0, c1, before, kept, whole, r);
+    __syncthreads();
+    if (from_row) {
+        // a wave's 64 consecutive elements lie in one sub-chunk
+        for (int64_t base = (int64_t)(threadIdx.x / kWave) * kWave; base < C; base += kPickThreads) {
+            const int64_t c = base + lane_id();
+            u64 add = 0;
+            if (c < C) {
+                const float v = Logit<T>::load(row + c);
+                const double w = q.weight(v);
+                const u64 W = q.fixed(w);
+                if (W && w >= q.min_p && border_bin(b, q.bin(v)) && q.bin(v) >= b.sure &&
+                    pack_key(order_image(v), (uint32_t)c) >= threshold)
+                    add = W;
+            }
+            add = wave_sum_u64(add);
+            if (add && lane_id() == 0) atomicAdd(&s.sum[base / a.sub], add);
+        }
+    } else {
+        for (int i = threadIdx.x; i < n; i += kPickThreads) {
+            const u64 key = s.key[i];
+            if (key >= threshold && q.weight(key_value(key)) >= q.min_p) s.keep(key, s.W[i], a.sub);
+        }
+    }
+    __syncthreads();
+    draw_from_sums<T>(s, row, q, a, threshold, r);
+}
+
+// The words of lane ^ 16 or lane ^ 32: the two copies trade their odd rows (or
+// upper half) for even rows (lower half), which leaves every lane's partner in
+// one of them.
+template <int D>
+__device__ __forceinline__ uint32_t swap_rows(uint32_t v) {
+    static_assert(D == 16 || D == 32, "rows or halves");
+    const auto p = D == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                           : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return lane_id() & D ? p[0] : p[1];
+}
+
+template <int D>
+__device__ __forceinline__ u64 lane_xor(u64 v) {   // the value of lane ^ D
+    if constexpr (D == 1) return dpp_key<kQuadXor1, 0xF>(v);
+    else if constexpr (D == 2) return dpp_key<kQuadXor2, 0xF>(v);
+    else if constexpr (D == 4) return dpp_key<kQuadXor3, 0xF>(dpp_key<kHalfRowMirror, 0xF>(v));   // ^ 7, then ^ 3
+    else if constexpr (D == 8) return dpp_key<kRowRotate8, 0xF>(v);
+    else return (u64)swap_rows<D>((uint32_t)(v >> 32)) << 32 | swap_rows<D>((uint32_t)v);
+}
+
+// Sorts a key per thread of the first P (a power of two, from 64 to
+// kPickThreads), largest first: a bitonic network, its exchanges within a wave
+// on lane moves and those between waves through s.key, of which two halves take
+// turns so that one barrier separates them.
+__device__ __forceinline__ u64 sort_keys(PickShared& s, u64 key, int P) {
+    const int tid = threadIdx.x;
+    const bool in = tid < P;   // wave-uniform
+    int half = 0;
+    for (int k = 2; k <= P; k <<= 1) {   // sorted runs of k, every other one in ascending order
+        const bool falling = (tid & k) == 0;
+        auto exchange = [&](u64 other, int d) {
+            if ((other > key) == (((tid & d) == 0) == falling)) key = other;
+        };
+        for (int d = k >> 1; d >= kWave; d >>= 1) {
+            s.key[half + tid] = key;
+            __syncthreads();
+            exchange(s.key[half + (tid ^ d)], d);
+            half ^= kPickThreads;
+        }
+        if (in) {
+            if (k > 32) exchange(lane_xor<32>(key), 32);
+            if (k > 16) exchange(lane_xor<16>(key), 16);
+            if (k > 8) exchange(lane_xor<8>(key), 8);
+            if (k > 4) exchange(lane_xor<4>(key), 4);
+            if (k > 2) exchange(lane_xor<2>(key), 2);
+            exchange(lane_xor<1>(key), 1);
+        }
+    }
+    return key;
+}
+
+// As pick_token, for a list of at most a key per thread (this thread's: `key`,
+// 0 past n): sorted, so that the border of top-k is a place and that of top-p a
+// running sum.  Entered with s.hits = 0 and s.found_key = ~0.
+template <class T>
+__device__ __forceinline__ void pick_sorted(PickShared& s, int n, u64 key, const T* row, const Row& q, const Borders& b,
+                                            const SampleArgs& a, int64_t r) {
+    int P = kWave;
+    while (P < n) P <<= 1;
+    key = sort_keys(s, key, P);
+    const int place = threadIdx.x;
+    const bool have = place < n;
+    double w = 0.0;
+    u64 W = 0;
+    int bin = kBins;
+    if (have) {
+        const float v = key_value(key);
+        w = q.weight(v);
+        W = q.fixed(w);
+        bin = q.bin(v);
+    }
+    // listed keys of bins ahead of kbin, and the mass of those of p0..p1 ahead of this one
+    const u64 ahead = __ballot(have && bin < b.kbin);
+    if (lane_id() == 0 && ahead) atomicAdd(&s.hits, (uint32_t)__popcll(ahead));
+    const bool in_p = have && bin >= b.p0 && bin <= b.p1;
+    u64 all;
+    const u64 mass = block_scan_u64<kPickThreads>(in_p ? W : 0ull, &all) - (in_p ? W : 0ull);
+    bool keep = have && (bin != b.kbin || (uint32_t)place - s.hits < b.krank);
+    if (q.p < 1.0) {
+        u64 total = b.total;
+        if (b.kbin < kBins) {   // the mass that top-k keeps
+            block_scan_u64<kPickThreads>(keep && bin == b.kbin ? W : 0ull, &all);
+            total = b.kmass + all;
+        }
+        keep = keep && in_p && b.pmass + mass < p_target(q.p, total);
+    }
+    const u64 kept = __ballot(keep);
+    if (kept) {   // wave-uniform; the wave's smallest kept key is its last
+        const u64 least = lane_u64(key, 63 - __clzll((long long)kept));
+        if (lane_id() == 0) atomicMin(&s.found_key, least);
+    }
+    if (keep && w >= q.min_p) s.keep(key, W, a.sub);
+    __syncthreads();
+    draw_from_sums<T>(s, row, q, a, n ? s.found_key : 0ull, r);
 }
 
 template <class T>
@@ -996,11 +1110,20 @@ k_sample_pick(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
     }
     const bool from_row = listed > (uint32_t)kCand;
     const int n = from_row ? 0 : (int)listed;
-    if ((int)threadIdx.x < n) s.put(threadIdx.x, first, q);
-    for (int i = threadIdx.x + kPickThreads; i < n; i += kPickThreads) s.put(i, ws->cand[i], q);
+    const bool sorted = listed <= (uint32_t)kPickThreads;
+    if (!sorted)
+        for (int i = threadIdx.x; i < n; i += kPickThreads) s.put(i, i < kPickThreads ? first : ws->cand[i], q);
     s.sum[threadIdx.x] = sum;
-    if (threadIdx.x == 0) s.found = s.left = 0;
+    if (threadIdx.x == 0) {
+        s.found = s.left = 0;
+        s.hits = 0;
+        s.found_key = ~0ull;
+    }
     __syncthreads();
+    if (sorted) {
+        pick_sorted<T>(s, n, (int)threadIdx.x < n ? first : 0ull, x + r * a.ld, q, b, a, r);
+        return;
+    }
     pick_token<T>(s, n, from_row, x + r * a.ld, q, b, a, false, r);
 }
 
