@@ -194,7 +194,8 @@ struct Row {
     }
     // its step, larger for smaller x; equal values share a bin
     __device__ __forceinline__ int bin(float x) const { return bin_of(below(x)); }
-    __device__ __forceinline__ int bin_of(float d) const { return (int)fminf(d * scale, (float)(kBins - 1)); }
+    __device__ __forceinline__ int bin_of(float d) const { return (int)place(d); }
+    __device__ __forceinline__ float place(float d) const { return fminf(d * scale, (float)(kBins - 1)); }
 };
 
 // What the bins say about the borders of top-k and top-p.
@@ -431,26 +432,30 @@ k_sample_hist(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
     }
     __syncthreads();
     // top-k needs the counts, top-p the masses.  Counting alone takes no
-    // weights: elements without weight are in the last bin, behind all others.
+    // weights: elements without weight are in the last bin, behind all others,
+    // and it does not matter whether they are counted.
     const bool by_mass = q.p < 1.0, by_count = q.k > 0;
     for (int64_t c = c0; c < c1; c += kSubMin) {
         const Share<T> e = ahead;
         if (c + kSubMin < c1) ahead.load(row, c + kSubMin, a.C, a.vec);
 #pragma unroll
         for (int h = 0; h < kPer; h += kTogether) {
-            double w[kTogether];
-            if (by_mass) q.weights(e.v + h, w);
+            if (by_mass) {
+                double w[kTogether];
+                q.weights(e.v + h, w);
 #pragma unroll
-            for (int i = 0; i < kTogether; ++i) {
-                const float v = e.v[h + i];
-                if (v > -INFINITY) {
-                    const int b = q.bin(v);
-                    if (by_mass) {
-                        const u64 W = q.fixed(w[i]);
-                        if (W) atomicAdd(&mass[b], W);
+                for (int i = 0; i < kTogether; ++i) {
+                    const u64 W = q.fixed(w[i]);
+                    if (W) {
+                        const int b = q.bin(e.v[h + i]);
+                        atomicAdd(&mass[b], W);
+                        if (by_count) atomicAdd(&count[b], 1u);
                     }
-                    if (by_count) atomicAdd(&count[b], 1u);
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kTogether; ++i)
+                    if (e.v[h + i] > -INFINITY) atomicAdd(&count[q.bin(e.v[h + i])], 1u);
             }
         }
     }
@@ -616,7 +621,7 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
     // border bins lie in sure .. last (p1 <= kbin)
     const bool borders = b.kbin < kBins || b.p0 <= b.p1;
     const int last = b.kbin < kBins ? b.kbin : b.p1;
-    const uint32_t span = (uint32_t)(last - b.sure);   // without borders the listed bits are not used
+    const float sure = (float)b.sure, past = (float)(last + 1);   // without borders the listed bits are not used
     const bool sift = (b.p0 <= b.p1 && b.kbin < kBins && b.kbin > b.p1 + 1) || last == kBins - 1;
     if (threadIdx.x == 0) n_list = 0;
     for (int i = threadIdx.x; i < subs; i += kChunkThreads) sums[i] = 0;
@@ -634,10 +639,10 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
 #pragma unroll
             for (int i = 0; i < kTogether; ++i) {
                 const float d = q.below(e.v[h + i]);
-                const int bin = q.bin_of(d);
-                whole[i] = bin < b.sure && d <= q.far;
+                const float at = q.place(d);   // below n exactly where the bin is
+                whole[i] = at < sure && d <= q.far;
                 some |= whole[i];
-                listed |= (uint32_t)(bin - b.sure) <= span ? 1u << (h + i) : 0u;
+                listed |= at >= sure && at < past ? 1u << (h + i) : 0u;
             }
             if (!__any(some)) continue;   // most steps of a wave, where few tokens are kept
             double w[kTogether];
