@@ -174,12 +174,15 @@ struct Row {
 #undef DG_TERM
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            // the high word plus n << 20, as one operation (the compiler widens the
+            // addition to 64 bits), and bound here, or it moves each chain into the
+            // branch of its first use, one after the other (the gather of 256 rows
+            // of 128000: 97 us against 81)
             const u64 v = __builtin_bit_cast(u64, w[i]);
-            w[i] = __builtin_bit_cast(double, (u64)((uint32_t)(v >> 32) + (n[i] << 20)) << 32 | (uint32_t)v);
-            // bound here, or the compiler moves each chain into the branch of its
-            // first use, one after the other (the gather of 256 rows of 128000:
-            // 97 us against 81)
-            if constexpr (N > 1) asm volatile("" : "+v"(w[i]));
+            uint32_t hi = (uint32_t)(v >> 32);
+            if constexpr (N > 1) asm volatile("v_lshl_add_u32 %0, %1, 20, %0" : "+v"(hi) : "v"(n[i]));
+            else hi += n[i] << 20;
+            w[i] = __builtin_bit_cast(double, (u64)hi << 32 | (uint32_t)v);
         }
     }
     // round(2^F w) by the binary64 addition 2^52 + 2^F w (F <= 51)
@@ -648,7 +651,11 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
             double w[kTogether];
             q.weights(e.v + h, w);
 #pragma unroll
-            for (int i = 0; i < kTogether; ++i) sum += whole[i] && w[i] >= q.min_p ? q.fixed(w[i]) : 0ull;
+            for (int i = 0; i < kTogether; ++i) {
+                u64 W = q.fixed(w[i]);
+                asm volatile("" : "+v"(W));   // or a branch around each
+                sum += whole[i] && w[i] >= q.min_p ? W : 0ull;
+            }
         }
         if (borders && __any(listed != 0)) {
             if (sift) {   // bins between top-p's and top-k's, or elements without weight
