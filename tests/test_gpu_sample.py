@@ -301,3 +301,67 @@ def test_graph_replays(dg, dev):
         step()
         torch.cuda.synchronize()
         assert torch.equal(got, idx)
+
+
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 127, 128, 129, 300, 512, 513, 1000, 1023, 1024, 1025, 2500, 4097])
+def test_border_lists_of_every_length(dg, dev, n):
+    """n tokens share one bin, equal or a few steps apart, and every border falls among them."""
+    import torch
+    C = 9001
+    g = np.random.default_rng(n)
+    rows, par = [], {"temperature": [], "top_k": [], "top_p": [], "min_p": []}
+    for steps in (0, 1, 5):   # distinct values of the bin
+        for k, p, mp in ((n // 2 + 1, 1.0, 0.0), (0, 0.37, 0.0), (n // 3 + 1, 0.61, 0.0), (n, 0.999, 0.5), (0, 0.0, 0.0)):
+            v = np.full(C, -np.inf, np.float32)
+            at = g.permutation(C)[:n]
+            v[at] = np.float32(3.0) + np.float32(2.0 ** -20) * g.integers(0, steps + 1, n).astype(np.float32)
+            v[g.permutation(C)[:50]] = -60.0   # a long range, so that the values above share a bin
+            v[at] = np.maximum(v[at], np.float32(3.0))
+            rows.append(v)
+            for name, value in zip(("temperature", "top_k", "top_p", "min_p"), (1.0, k, p, mp)):
+                par[name].append(value)
+    check(dg, dev, torch.from_numpy(np.stack(rows)), g.random(len(rows)), **par)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("ld", [33000, 33001])   # rows aligned for wide loads, and not
+def test_extremes_of_chunks_of_several_steps(dg, dev, dtype, ld):
+    """So many rows that a workgroup takes several load steps: NaN, equal maxima, zeros of both signs, masked rows."""
+    import torch
+    R, C = 90, 32999
+    x = logits((1295, 1, 0, 0), R, ld, dtype, 2.0)
+    x[:, C:] = float("nan")   # behind the rows, never read
+    g = np.random.default_rng(5)
+    want = []
+    for r in range(R):
+        spots = np.sort(g.choice(C, 3, replace=False))
+        kind = r % 9
+        if kind == 0:
+            x[r, spots] = 20.0
+        elif kind == 1:
+            x[r, spots] = float("nan")
+        elif kind == 2:
+            x[r, :C] = -float("inf")
+        elif kind == 3:
+            x[r, :C] = -float("inf")
+            x[r, spots] = 1.0
+        elif kind == 4:
+            x[r, :C] = -x[r, :C].abs() - 1
+            x[r, spots] = 0.0
+            x[r, spots[0]] = -0.0
+        elif kind == 5:
+            x[r, :C] = -7.0
+        elif kind == 6:
+            x[r, spots[1:]] = float("inf")
+            x[r, spots[0]] = -float("inf")
+        elif kind == 7:
+            x[r, 0], x[r, C - 1] = 30.0, 30.0
+        row = x[r, :C].double().numpy()
+        want.append(int(np.flatnonzero(np.isnan(row))[0]) if np.isnan(row).any() else int(row.argmax()))
+    got = sample(dg, dev, x, [0.3] * R, C=C, temperature=[0.0] * R)
+    assert np.array_equal(got, want)
+    draws = x.clone()
+    keep = [r for r in range(R) if r % 9 not in (1, 2)]
+    many = torch.cat([draws[keep], draws[keep][:20]])   # still so many rows
+    n = many.shape[0]
+    check(dg, dev, many, g.random(n), C=C, temperature=[0.9] * n, top_k=[60] * n, top_p=[0.95] * n)
