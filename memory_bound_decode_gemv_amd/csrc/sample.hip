@@ -26,12 +26,20 @@
 //   gather  every workgroup reads the bins and finds the ones that the
 //           borders fall into; sums what lies above them for sure, per
 //           sub-chunk, and lists the keys of the border bins;
-//   pick    one workgroup per row resolves the borders within the listed keys
-//           (a radix descent over the key bits that differ), adds the kept
-//           ones to the sub-chunk sums, and finds the sub-chunk and in it the
-//           element that u falls into.
+//   pick    one workgroup per row resolves the borders within the listed keys,
+//           adds the kept ones to the sub-chunk sums, and finds the sub-chunk and
+//           in it the element that u falls into.  Up to 64 keys: every key against
+//           every other, in one wave; up to 1024: sorted, one per thread; more: a
+//           radix descent over the key bits that differ.
 // A row whose border bins hold more than kCand elements (many equal values)
 // is resolved by the same descent reading the row instead of the list.
+//
+// One row of 128256 float32 logits takes 18 us, four dependent launches of 3 to
+// 6 us; 256 rows of 128000 with top-p alone 124 us, bound by instruction issue
+// (the vector unit is busy for 87 to 90 % of hist and gather, which compute
+// every weight anew: 43 and 59 us) after a first pass at 6 TB/s (22 us).  64
+// rows of 128256 bfloat16 logits with mixed filters take 43 us; the pick sorts
+// their lists in 9.5 us, where the descent took 13.1.
 #include "argkey.h"
 #include "dg_device.h"
 #include "dg_internal.h"
