@@ -43,6 +43,7 @@
 #include "argkey.h"
 #include "dg_device.h"
 #include "dg_internal.h"
+#include "sample_bins.h"
 
 // Every kernel computes an element's weight and bin anew; they have to agree
 // to the bit, so no kernel may contract what another does not.
@@ -51,7 +52,6 @@
 namespace dg {
 namespace {
 
-constexpr int kBins = 512;
 constexpr int kCand = 4096;          // keys that the pick kernel holds in LDS
 constexpr int kChunkList = 2048;     // of them that one workgroup of the gather kernel lists
 constexpr int kSubMin = 2048;        // elements of a sub-chunk, at least
@@ -198,15 +198,9 @@ struct Row {
         const double v = fma(w, (double)(1ull << F), 4503599627370496.0);
         return __builtin_bit_cast(u64, v) & 0x000FFFFFFFFFFFFFull;
     }
-    // m - x with infinities as the largest number: 0 where both are infinite
-    __device__ __forceinline__ float below(float x) const {
-        constexpr float kLargest = 3.4028234663852886e38f;
-        return fminf(fminf(m, kLargest) - fminf(x, kLargest), kLargest);
-    }
-    // its step, larger for smaller x; equal values share a bin
-    __device__ __forceinline__ int bin(float x) const { return bin_of(below(x)); }
-    __device__ __forceinline__ int bin_of(float d) const { return (int)place(d); }
-    __device__ __forceinline__ float place(float d) const { return fminf(d * scale, (float)(kBins - 1)); }
+    __device__ __forceinline__ float below(float x) const { return bin_distance(m, x); }
+    __device__ __forceinline__ float place(float d) const { return bin_place(d, scale); }
+    __device__ __forceinline__ int bin(float x) const { return (int)place(below(x)); }
 };
 
 // What the bins say about the borders of top-k and top-p.
@@ -264,14 +258,9 @@ __device__ __forceinline__ Row make_row(const SampleArgs& a, const Params& t, u6
     q.u = t.u > 0.0f ? (t.u < 1.0f ? t.u : 1.0f) : 0.0f;
     q.F = a.F;
     q.c = kLog2e / (double)t.T;
-    // the range that has weight: down to the smallest value, and no further than W = 0
     constexpr float kLn2 = 0.69314718f;
-    const float range = fminf(q.m - low, (float)(a.F + 1) * kLn2 * t.T);
-    q.scale = range > 0.0f ? fminf((float)kBins / range, 1e30f) : 0.0f;
-    if (q.m == INFINITY) {   // m - x is 0 or infinite, at any temperature
-        q.scale = 1.0f;
-        q.c = 1.0;
-    }
+    q.scale = bin_scale(q.m, low, (float)(a.F + 1) * kLn2 * t.T);
+    if (q.m == INFINITY) q.c = 1.0;   // m - x is 0 or infinite, at any temperature
     // -log2(min_p) / c, and more than its roundings
     q.far = q.min_p > 0.0 ? (1.001f * -log2f((float)q.min_p) + 1e-5f) * kLn2 * t.T : INFINITY;
     return q;

@@ -365,3 +365,47 @@ def test_extremes_of_chunks_of_several_steps(dg, dev, dtype, ld):
     many = torch.cat([draws[keep], draws[keep][:20]])   # still so many rows
     n = many.shape[0]
     check(dg, dev, many, g.random(n), C=C, temperature=[0.9] * n, top_k=[60] * n, top_p=[0.95] * n)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C,ld", [(4097, 4104), (6145, 6152), (9001, 9001 + 2048), (33001, 33008)])
+def test_nothing_behind_a_row_is_listed(dg, dev, C, ld, dtype):
+    """Rows of one value, of one allowed token, of a few tied ones, and rows whose spread overflows binary32: what is
+    behind a row is neither drawn nor listed (no key of its value in the workspace)."""
+    import torch
+    behind = 12352.0   # exact in every type
+    R = 8
+    x = torch.full((R, ld), behind, dtype=torch.float32)
+    x[0, :C] = 1.0
+    x[1, :C] = NEG
+    x[1, C // 3] = -2.0
+    x[2, :C] = NEG
+    x[2, 7::C // 5] = 0.5
+    x[3, :C] = torch.where(torch.arange(C) % 2 == 0, 3e38, -3e38)
+    x[4, :C] = torch.finfo(torch.float32).min / 2
+    x[5, :C] = NEG
+    x[5, C - 1] = 3.0
+    x[6, :C] = NEG
+    x[6, :20] = -1.0
+    x[7, :C] = 1.0
+    x[:, C:] = behind
+    x = x.to(tdtype(dtype))
+    spread = [1.0, 1.0, 0.7, float("inf"), 2.0, 1.0, 1.5, 1e38]
+    for params in ({"top_p": [0.9] * R}, {"top_k": [3] * R}, {"top_k": [4] * R, "top_p": [0.6] * R, "min_p": [0.5] * R}):
+        want = []
+        for r in range(R):
+            kw = {n: v[r] for n, v in params.items()}
+            want.append(reference_row(x[r, :C].double().numpy(), float(np.float32(0.55)), T=float(np.float32(spread[r])),
+                                      k=kw.get("top_k", 0), p=float(np.float32(kw.get("top_p", 1.0))),
+                                      mp=kw.get("min_p", 0.0)))
+        ws = torch.full((dg.dg_sample_workspace_bytes(R, C),), 0xA5, dtype=torch.uint8, device=dev)
+        idx = torch.zeros(R, dtype=torch.int64, device=dev)
+        given = {n: torch.tensor(v, dtype=torch.int32 if n == "top_k" else torch.float32, device=dev)
+                 for n, v in params.items()}
+        dg.dg_sample_rows(x.to(dev), torch.full((R,), 0.55, device=dev), idx, R=R, C=C, ld=ld, ws=ws,
+                          temperature=torch.tensor(spread, device=dev), **given)
+        torch.cuda.synchronize()
+        assert idx.cpu().tolist() == want
+        image = int(np.float32(behind).view(np.uint32)) | 0x80000000   # the upper half of its keys
+        words = ws.cpu().numpy().view(np.uint32)
+        assert not (words == image).any()
