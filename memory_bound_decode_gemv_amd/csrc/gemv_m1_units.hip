@@ -101,11 +101,15 @@ __device__ __forceinline__ void copy_unit(const uint8_t* __restrict__ row, int s
     }
 }
 
-template <class F, int S, int MC, int DEPTH, bool GLU>
+// Up: nothing, or GluArgs<true> for the gated product.  An empty argument in the
+// plain kernel cost rows of one unit up to 2 % (it moves the hidden arguments).
+template <class F, int S, int MC, int DEPTH, class... Up>
 __global__ void __launch_bounds__(256)
 k_units(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* __restrict__ Y, int N, int K,
-        GluArgs<GLU> glu_args) {
+        Up... up_args) {
     using G = UnitGeom<F>;
+    constexpr bool GLU = sizeof...(Up) > 0;
+    const GluArgs<GLU> glu_args{up_args...};
     constexpr int H = GLU ? 2 : 1;   // weight rows per output: (gate and) the row
     constexpr int U = H * S;         // units per output
     static_assert(DEPTH >= 2 && DEPTH <= 4, "pipeline depth");
@@ -168,15 +172,14 @@ k_units(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
     for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int m = 0; m < MC; ++m) out[h][m] = 0.0f;
-    // the outputs held by the lanes, `count` of them, from row out_row0 on
-    auto store = [&](int out_row, int count) {
-        if (lane < count) {
+    // the output that this lane holds, of those from row out_row on (64 at once
+    // are stored without a lane test, which costs 1 % in the loop)
+    auto store = [&](int out_row) {
 #pragma unroll
-            for (int m = 0; m < MC; ++m) {
-                float v = out[0][m];
-                if constexpr (GLU) v = glu(glu_args.act, v, out[1][m]);
-                Y[(int64_t)m * N + out_row + (int64_t)lane * rstride] = v;
-            }
+        for (int m = 0; m < MC; ++m) {
+            float v = out[0][m];
+            if constexpr (GLU) v = glu(glu_args.act, v, out[1][m]);
+            Y[(int64_t)m * N + out_row + (int64_t)lane * rstride] = v;
         }
     };
     int nout = 0;
@@ -208,12 +211,12 @@ k_units(const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ Xq, float* _
             }
         }
         if (++nout == kWave) {
-            store(out_row0, kWave);
+            store(out_row0);
             nout = 0;
             out_row0 = row + rstride;
         }
     }
-    store(out_row0, nout);
+    if (lane < nout) store(out_row0);
 }
 
 // The gated product takes up to five columns of Q4_0 rows of one unit and four
@@ -224,9 +227,9 @@ constexpr bool units_instantiated(int S, int M, int depth) {
     return !GLU || (depth <= 3 && M <= 8 && (F::kBlockBytes == 34 || M <= (S == 1 ? 5 : 4)));
 }
 
-template <class F, bool GLU>
+template <class F, class... Up>
 hipError_t launch_units(int K, int M, int depth, const void* Wq, const void* Xq, float* Y, int N, int grid, int block,
-                        GluArgs<GLU> ga, hipStream_t s) {
+                        hipStream_t s, Up... up_args) {
     using G = UnitGeom<F>;
     if (!block) block = 256;
     if (block > 256) return hipErrorInvalidValue;   // compiled for <= 256 threads
@@ -248,9 +251,10 @@ hipError_t launch_units(int K, int M, int depth, const void* Wq, const void* Xq,
     const uint8_t* w = (const uint8_t*)Wq;
     const uint8_t* x = (const uint8_t*)Xq;
 #define DG_SMD(SS, MM, DD)                                                                                 \
-    if constexpr (units_instantiated<F, GLU>(SS, MM, DD))                                                  \
+    if constexpr (units_instantiated<F, (sizeof...(Up) > 0)>(SS, MM, DD))                                  \
     if (S == SS && M == MM && depth == DD) {                                                               \
-        hipLaunchKernelGGL((k_units<F, SS, MM, DD, GLU>), dim3(grid), dim3(block), lds, s, w, x, Y, N, K, ga); \
+        hipLaunchKernelGGL((k_units<F, SS, MM, DD, Up...>), dim3(grid), dim3(block), lds, s, w, x, Y, N, K, \
+                           up_args...);                                                                    \
         return hipGetLastError();                                                                          \
     }
 #define DG_SM(SS, MM) DG_SMD(SS, MM, 2) DG_SMD(SS, MM, 3) DG_SMD(SS, MM, 4)
@@ -270,19 +274,19 @@ hipError_t launch_units(int K, int M, int depth, const void* Wq, const void* Xq,
 
 hipError_t launch_q4_units(int K, int M, int depth, const void* Wq, const void* Xq, float* Y, int N, int grid,
                            int block, hipStream_t s) {
-    return launch_units<UnitsQ4_0, false>(K, M, depth, Wq, Xq, Y, N, grid, block, {}, s);
+    return launch_units<UnitsQ4_0>(K, M, depth, Wq, Xq, Y, N, grid, block, s);
 }
 
 hipError_t launch_q8_units(int K, int M, int depth, const void* Wq, const void* Xq, float* Y, int N, int grid,
                            int block, hipStream_t s) {
-    return launch_units<UnitsQ8_0, false>(K, M, depth, Wq, Xq, Y, N, grid, block, {}, s);
+    return launch_units<UnitsQ8_0>(K, M, depth, Wq, Xq, Y, N, grid, block, s);
 }
 
 hipError_t launch_units_glu(bool q8, int K, int M, int depth, const GluMatrices& w, const void* Xq, float* Y, int N,
                             int grid, int block, hipStream_t s) {
     const GluArgs<true> ga = {(const uint8_t*)w.up, w.act};
-    return q8 ? launch_units<UnitsQ8_0, true>(K, M, depth, w.gate, Xq, Y, N, grid, block, ga, s)
-              : launch_units<UnitsQ4_0, true>(K, M, depth, w.gate, Xq, Y, N, grid, block, ga, s);
+    return q8 ? launch_units<UnitsQ8_0>(K, M, depth, w.gate, Xq, Y, N, grid, block, s, ga)
+              : launch_units<UnitsQ4_0>(K, M, depth, w.gate, Xq, Y, N, grid, block, s, ga);
 }
 
 // The gated products over row-major weights, both matrices in one launch: the

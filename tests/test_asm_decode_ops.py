@@ -48,3 +48,15 @@ def test_tiled_gated_product(name, part, tmp_path):
         assert re.search(r"global_load_dwordx4 .* nt", body)
         assert "global_load_lds_dwordx4" in body and "v_mfma_i32_16x16x" in body
         assert "atomic" not in body and "scratch_" not in body and "v_accvgpr_read" not in body
+
+
+def test_plain_units_kernels_pay_nothing_for_the_gated_form(tmp_path):
+    """A wave of the units kernels stores 64 outputs at a time and the rest at the end: only the end depends on the
+    lane.  The plain kernels take their own arguments (32 bytes, then the hidden ones) and no empty one."""
+    t = asm_of("gemv_m1_units.hip", tmp_path)
+    for body in kernels(t, "k_units"):
+        assert body.count("s_and_saveexec_b64") == 1
+    plain = [b for b in kernels(t, "k_units") if "GluArgs" not in b.split(".amdhsa_kernel", 1)[1].split("\n", 1)[0]]
+    assert plain
+    for body in plain:
+        assert re.search(r"\.amdhsa_kernarg_size 288\b", body)

@@ -247,3 +247,11 @@ def test_empty_sums_past_two_to_the_32(dg, dev):
     dg.dg_gemv_q4_0_tiles_glu(none, none, none, Y, N, 0, M)
     for m in range(M):
         assert torch.count_nonzero(Y[m]).item() == 0
+
+
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0"])
+@pytest.mark.parametrize("N,K,M", [(200003, 256, 1), (197001, 512, 3), (132100, 256, 5)])
+def test_more_rows_than_a_wave_holds_outputs(dg, dev, orc, fmt, N, K, M):
+    """Past 64 rows a wave stores a full set of outputs and goes on."""
+    c = Case(dg, dev, orc, fmt, 1390, N, K, M)
+    check("silu", c.run(False, "silu"), c.G, c.U, K)
