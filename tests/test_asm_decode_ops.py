@@ -60,3 +60,14 @@ def test_plain_units_kernels_pay_nothing_for_the_gated_form(tmp_path):
     assert plain
     for body in plain:
         assert re.search(r"\.amdhsa_kernarg_size 288\b", body)
+
+
+def test_norm_squares_and_sums_in_binary64(tmp_path):
+    """Per element of a thread's groups one widening, one product and one addition in binary64, beside the ten additions
+    over the workgroup.  (The root and the quotient are binary64 fused operations whatever the sum is.)"""
+    t = asm_of("norm.hip", tmp_path)
+    for groups in (0, 1, 2, 4):   # 0: rows read twice, a group at a time
+        for body in kernels(t, f"ELi{groups}EEEvPKNT_"):
+            n = 8 * max(groups, 1)
+            assert body.count("v_cvt_f64_f32") >= n + 1   # and eps
+            assert body.count("v_mul_f64") >= n and body.count("v_add_f64") >= n + 10
