@@ -45,9 +45,9 @@ inline void units_default_grid(int N, int M, int& grid, int& block) {
     grid = need < g ? need : g;
 }
 
-// Rows of one launch of a kernel with up to 1024 threads per row: a launch has
-// fewer than 2^32 threads.
-constexpr int64_t kMaxRowsPerLaunch = int64_t(1) << 21;
+// Workgroups of up to 1024 threads that one launch takes: it has fewer than 2^32
+// threads.
+constexpr int64_t kMaxGroupsPerLaunch = int64_t(1) << 21;
 
 // Device properties used to size grids and check launches; cached per device.
 int device_cu_count();

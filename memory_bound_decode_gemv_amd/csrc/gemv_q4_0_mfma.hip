@@ -425,7 +425,8 @@ hipError_t launch_mfma_cfg(const void* Wq, const void* Xq, float* Y, int N, int 
     if ((K >> 5) % CB != 0 || K > (1 << 26)) return hipErrorInvalidValue;   // whole chunks, 32-bit offsets
     constexpr int kRows = 16 * (GLU ? RT / 2 : RT);
     const int groups = (N + kRows - 1) / kRows;
-    const int g = grid ? grid : groups;
+    // past a launch's workgroups, each takes several row groups in turn
+    const int g = grid ? grid : (int)std::min<int64_t>(groups, kMaxGroupsPerLaunch);
     hipLaunchKernelGGL((k_qmfma<WF, CB, MP, RT, KS, DEPTH, GLU>), dim3(g), dim3(64 * RT * KS), lds, s,
                        (const uint8_t*)Wq, (const uint8_t*)Xq, Y, N, K, M, ga);
     return hipGetLastError();

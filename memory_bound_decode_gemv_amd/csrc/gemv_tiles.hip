@@ -621,7 +621,7 @@ template <class TF, int MP, int RT, int KW, int D>
 __global__ void __launch_bounds__(64 * RT * KW)
 k_glu_tiles(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ Wu, const uint8_t* __restrict__ Xq,
             float* __restrict__ Y, int N, int K, int M, int act, int spp, int cs_slots, uint32_t cs_magic, int CS,
-            int groups) {
+            int groups, int first) {
     static_assert(RT % 2 == 0, "gate and up tiles in pairs");
     using TS = TileSet<MP>;
     constexpr int NA = TS::kNA;
@@ -638,8 +638,8 @@ k_glu_tiles(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ Wu, cons
     const int S = K >> 8;
     const int nblk = K >> 5;
     const int T = (N + 15) >> 4;
-    int grp = (int)blockIdx.x;
-    if (CS > 1) {   // column slices, placed as in k_tiles
+    int grp = first + (int)blockIdx.x;   // first: 0, or that of a later launch
+    if (CS > 1) {   // column slices, placed as in k_tiles (one launch)
         const int b = (int)blockIdx.x;
         const int cs = (b >> 3) % CS;
         grp = (b >> 3) / CS * 8 + (b & 7);
@@ -1013,11 +1013,16 @@ template <class TF, int MP, int RT, int KW, int D>
 hipError_t launch_glu_tiles_cfg(const GluPlan& p, const GluMatrices& w, const void* Xq, float* Y, int N, int K, int M,
                                 hipStream_t s) {
     const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) + (uint64_t)p.cs_slots - 1) / (uint64_t)p.cs_slots);
-    const int grid = p.CS == 1 ? p.groups : (p.groups + 7) / 8 * 8 * p.CS;
-    hipLaunchKernelGGL((k_glu_tiles<TF, MP, RT, KW, D>), dim3(grid), dim3(64 * RT * KW), p.lds, s,
-                       (const uint8_t*)w.gate, (const uint8_t*)w.up, (const uint8_t*)Xq, Y, N, K, M, w.act, p.spp,
-                       p.cs_slots, magic, p.CS, p.groups);
-    return hipGetLastError();
+    const int grid = p.CS == 1 ? p.groups : (p.groups + 7) / 8 * 8 * p.CS;   // slices: below 128 row groups
+    hipError_t e = hipSuccess;
+    for (int64_t first = 0; first < grid && e == hipSuccess; first += kMaxGroupsPerLaunch) {
+        const int64_t part = std::min<int64_t>(grid - first, kMaxGroupsPerLaunch);
+        hipLaunchKernelGGL((k_glu_tiles<TF, MP, RT, KW, D>), dim3((unsigned)part), dim3(64 * RT * KW), p.lds, s,
+                           (const uint8_t*)w.gate, (const uint8_t*)w.up, (const uint8_t*)Xq, Y, N, K, M, w.act, p.spp,
+                           p.cs_slots, magic, p.CS, p.groups, (int)first);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 template <class TF, int MP>

@@ -269,8 +269,8 @@ hipError_t launch_norm_out(const RmsNorm& a, hipStream_t s) {
     if (aligned16(a.x) && aligned16(a.res) && aligned16(a.h) && a.ld * (int64_t)sizeof(raw) % 16 == 0) vec |= 1;
     if (aligned16(a.w)) vec |= 2;
     if (aligned16(a.out) && a.ldy * ysize % 16 == 0) vec |= 4;
-    for (int64_t r0 = 0; r0 < a.M; r0 += kMaxRowsPerLaunch) {
-        const unsigned rows = (unsigned)(a.M - r0 < kMaxRowsPerLaunch ? a.M - r0 : kMaxRowsPerLaunch);
+    for (int64_t r0 = 0; r0 < a.M; r0 += kMaxGroupsPerLaunch) {
+        const unsigned rows = (unsigned)(a.M - r0 < kMaxGroupsPerLaunch ? a.M - r0 : kMaxGroupsPerLaunch);
         const raw* x = (const raw*)a.x + r0 * a.ld;
         const raw* res = a.res ? (const raw*)a.res + r0 * a.ld : nullptr;
         raw* h = a.h ? (raw*)a.h + r0 * a.ld : nullptr;

@@ -1264,8 +1264,8 @@ template <class T>
 hipError_t launch_sample(const SampleRows& p, hipStream_t s) {
     const T* x = (const T*)p.x;
     if (p.C <= kCand) {
-        for (int64_t r0 = 0; r0 < p.R; r0 += kMaxRowsPerLaunch) {
-            const int64_t rn = p.R - r0 < kMaxRowsPerLaunch ? p.R - r0 : kMaxRowsPerLaunch;
+        for (int64_t r0 = 0; r0 < p.R; r0 += kMaxGroupsPerLaunch) {
+            const int64_t rn = p.R - r0 < kMaxGroupsPerLaunch ? p.R - r0 : kMaxGroupsPerLaunch;
             hipLaunchKernelGGL((k_sample_row<T>), dim3((unsigned)rn), dim3(kPickThreads), 0, s, x + r0 * p.ld,
                                plan_rows(p, r0, rn));
             const hipError_t e = hipGetLastError();

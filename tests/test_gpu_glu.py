@@ -255,3 +255,38 @@ def test_more_rows_than_a_wave_holds_outputs(dg, dev, orc, fmt, N, K, M):
     """Past 64 rows a wave stores a full set of outputs and goes on."""
     c = Case(dg, dev, orc, fmt, 1390, N, K, M)
     check("silu", c.run(False, "silu"), c.G, c.U, K)
+
+
+@pytest.mark.parametrize("tiles,M", [(True, 9), (True, 3), (False, 9)])
+def test_rows_past_a_launch(dg, dev, tiles, M):
+    """More rows than the threads of one launch reach (eight a row), in several or in several row groups a workgroup."""
+    import torch
+    N, K = (1 << 29) + 37, 256
+    nb, row = K // 32, 18 * (K // 32)   # also a tile's bytes a row: one group of K
+    g = torch.Generator(device=dev).manual_seed(9)
+    W = torch.zeros(-(-N // 16) * 16 * row, dtype=torch.uint8, device=dev)   # gate and up; zero but for these rows
+    spots = [0, (1 << 26) - 32, (1 << 27) - 16, (1 << 28) - 16, (1 << 29) - 16]
+    some = []
+    for first in spots:
+        n = min(64, N - first)
+        q = torch.empty(n * row, dtype=torch.uint8, device=dev)
+        dg.dg_quantize_q4_0(torch.randn(n, K, device=dev, generator=g) / 16, q, n, K)
+        some.append((first, n, q.cpu().numpy()))
+        if tiles:
+            t = torch.empty(dg.dg_q4_0_tiles_bytes(n, K), dtype=torch.uint8, device=dev)
+            dg.dg_repack_q4_0_tiles(q, t, n, K)
+            W[first * row:first * row + t.numel()] = t
+        else:
+            W[first * row:first * row + q.numel()] = q
+    Xq = torch.empty(M * nb * 36, dtype=torch.uint8, device=dev)
+    dg.dg_quantize_q8_1(torch.randn(M, K, device=dev, generator=g), Xq, M, K)
+    Y = torch.full((M, N), 5.0, device=dev)
+    (dg.dg_gemv_q4_0_tiles_glu if tiles else dg.dg_gemv_q4_0_glu)(W, W, Xq, Y, N, K, M)
+    torch.cuda.synchronize()
+    x = Xq.cpu().numpy()
+    for first, n, q in some:
+        G = sums("q4_0", q, x, n, K, M)
+        check("silu", Y[:, first:first + n].cpu().numpy(), G, G, K)
+        Y[:, first:first + n] = 0
+    for m in range(M):   # and every other row was written, with zeros
+        assert torch.count_nonzero(Y[m]).item() == 0
