@@ -504,37 +504,48 @@ def asm_resources(asm_text):
 
 
 def _demangle(names):
+    """Readable names.  c++filt knows neither binary16 (DF16_) nor bfloat16 (DF16b): they go through it as other builtin
+    types (a builtin type takes no part in the numbering of a name's repeated parts), __float80 and __float128."""
     import subprocess
+    plain = [n.replace("DF16_", "e").replace("DF16b", "g") for n in names]
     try:
-        r = subprocess.run(["c++filt"], input="\n".join(names), capture_output=True, text=True, check=True)
-        return r.stdout.splitlines()
+        r = subprocess.run(["c++filt"], input="\n".join(plain), capture_output=True, text=True, check=True)
+        return [d.replace("long double", "_Float16").replace("__float128", "__bf16") for d in r.stdout.splitlines()]
     except (OSError, subprocess.CalledProcessError):
         return list(names)
 
 
-def resources_markdown(command=""):
-    """Compiler resource report of every kernel the library builds, one line
-    per kernel template (its instantiations' ranges)."""
+def kernel_records(sources):
+    """asm_resources of the kernels of some sources, with `source`, `name` (demangled) and `norm` (template and arguments,
+    without namespaces)."""
     import tempfile
     from . import _build
+
+    def norm(name):
+        n = re.sub(r"^void\s+", "", name)
+        n = re.sub(r"dg::((\(anonymous namespace\)|mfma|q4)::)?", "", n)
+        return re.sub(r"\s+", "", n.split("(")[0])
     rows = []
     with tempfile.TemporaryDirectory() as d:
-        for src in _build.sources():
+        for src in sources:
             out = _build.device_asm(src, os.path.join(d, os.path.basename(src) + ".s"))
             with open(out) as f:
                 recs = asm_resources(f.read())
             for r, dem in zip(recs, _demangle([r["mangled"] for r in recs])):
                 r["name"] = dem
+                r["norm"] = norm(dem)
                 r["source"] = os.path.basename(src)
                 rows.append(r)
-    def norm(name):
-        n = re.sub(r"^void\s+", "", name)
-        n = n.replace("dg::(anonymous namespace)::", "").replace("dg::mfma::", "").replace("dg::q4::", "")
-        return re.sub(r"\s+", "", n.split("(")[0])
+    return rows
 
+
+def resources_markdown(command=""):
+    """Compiler resource report of every kernel the library builds, one line
+    per kernel template (its instantiations' ranges)."""
+    from . import _build
+    rows = kernel_records(_build.sources())
     groups = collections.OrderedDict()
     for r in rows:
-        r["norm"] = norm(r["name"])
         groups.setdefault((r["source"], re.sub(r"<.*", "", r["norm"])), []).append(r)
 
     def rng(rs, k):
@@ -560,9 +571,8 @@ def resources_markdown(command=""):
               "| workload | kernel | VGPRs | SGPRs | waves/SIMD (registers) |", "|---|---|---|---|---|"]
     by_norm = {r["norm"]: r for r in rows}
     for label, key in DEFAULT_KERNELS:
-        r = by_norm.get(key)
-        if r is not None:
-            lines.append(f"| {label} | `{key}` | {r.get('vgpr')} | {r.get('sgpr')} | {r.get('occupancy')} |")
+        r = by_norm[key]   # a name here that no kernel has is a mistake
+        lines.append(f"| {label} | `{key}` | {r.get('vgpr')} | {r.get('sgpr')} | {r.get('occupancy')} |")
     return "\n".join(lines) + "\n"
 
 
@@ -571,8 +581,8 @@ DEFAULT_KERNELS = [
     ("fp16 GEMV 4096x4096", "k_gemv_wide<false,2,false,2>"),
     ("bf16 GEMV (decoder shapes, lm-head)", "k_gemv_wide<true,2,false,2>"),
     ("Q4_0 M=1 28672x8192", "k_q4_m1_ldsrow<2,5,2,false>"),
-    ("Q4_0 M=16 4096x14336", "k_qmfma<FmtQ4_0,8,16,1,4,2>"),
-    ("Q4_0 M=17..24 4096x14336", "k_qmfma<FmtQ4_0,8,24,1,12,1>"),
+    ("Q4_0 M=16 4096x14336", "k_qmfma<FmtQ4_0,8,16,1,4,2,false>"),
+    ("Q4_0 M=17..24 4096x14336", "k_qmfma<FmtQ4_0,8,24,1,12,1,false>"),
     ("Q4_0 M=9..16 14336x4096 (resident columns)", "k_qres<FmtQ4_0,1,4,2,2>"),
     ("NF4 M=1, K=8192", "k_nf4_rows<8,1>"),
     ("NF4 M=1, other K", "k_nf4_rows<4,1>"),
