@@ -435,7 +435,7 @@ dg_status dg_quantize_q8_0(const float* w, void* Wq, int64_t N, int64_t K,
  * next GEMV's input.  dg_rmsnorm_q8_1 stores y as the Q8_1 columns that the
  * quantised GEMVs read, byte for byte what dg_quantize_q8_1 makes of it;
  * dg_rmsnorm stores it in binary32, binary16 or bfloat16 (the dense GEMVs'
- * x).  One launch.
+ * x).  One launch for up to 2^21 rows.
  *
  * The binary32 sum x + res is rounded once, to the storage type T of x, res
  * and h, and the norm is that of the rounded values, so that it is the norm of

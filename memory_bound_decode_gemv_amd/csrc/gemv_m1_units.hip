@@ -305,9 +305,11 @@ hipError_t launch_gemv_glu(bool q8, const GluMatrices& w, const void* Xq, float*
     if (S <= 4 && M * S <= 8 && (q8 || M <= (S == 1 ? 5 : 4))) {
         // Workgroups of four waves, two or three to a CU (14336 x 4096 Q4_0 at 4
         // columns: 15.6 us with 768 of them, 17.3 with 512; Q8_0 at 8: 26.3
-        // with 512, 28.4 with 768); for one column of many long rows, one row
-        // pair after another on all that fit (28672 x 8192 Q4_0 38.9 us with
-        // 4096, 40.2 with 2048).  A wave with a single pair has both its rows
+        // with 512, 28.4 with 768); for one column of many long rows 4096, one
+        // row pair after another on all that fit (28672 x 8192 Q4_0 39.0 us, 40.5
+        // with 512; Q8_0 71.8 and 72.7; 18944 x 14336 46.0 and 46.6, Q8_0 82.9 and
+        // 84.9; 16384 x 8192 and 32768 x 5120 Q8_0 1 to 2 % less too, but Q4_0 3
+        // and 4 % more: 24.7 and 24.0, 31.8 and 30.6).  A wave with a single pair has both its rows
         // in flight at once (1376 x 4096 Q4_0: 3.8 us against 4.1).
         const int need = (N + 3) / 4;
         const int g = S >= 2 ? (M == 1 && N >= 16384 ? 4096 : 512) : (q8 && M > 4 ? 512 : 768);

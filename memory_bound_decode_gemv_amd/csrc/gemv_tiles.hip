@@ -612,9 +612,9 @@ struct TileOut {
 // data flow is that of k_tiles.  A kernel of its own: one template for both
 // changed the plain kernel's registers and cost it 1 to 2 % at up to 8 columns.
 //
-// 14336 x 4096 Q4_0 at 16 columns: 15.0 us (66 MB, 4.5 TB/s), bound by latency
-// with 224 workgroups of 16 waves on 256 CUs, the vector unit active in 58 % of
-// the busy cycles.  28672 x 8192 Q8_0 at 24: 82 us (499 MB, 6.1 TB/s), bound by
+// 14336 x 4096 Q4_0 at 16 columns: 15.5 us (66 MB from HBM, 4.3 TB/s; 15.0 where
+// the last-level cache holds them), bound by latency with 224 workgroups of 16
+// waves on 256 CUs, the vector unit active in 60 % of the busy cycles.  28672 x 8192 Q8_0 at 24: 82 us (499 MB, 6.1 TB/s), bound by
 // HBM and the barriers between passes.
 // ---------------------------------------------------------------------------
 template <class TF, int MP, int RT, int KW, int D>

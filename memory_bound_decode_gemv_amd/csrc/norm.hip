@@ -25,11 +25,18 @@
 // the output written once.  All the threads a row can use, up to 1024: 2048 rows
 // of 8192 bfloat16 elements take 22.0 us (6.1 TB/s of the 134 MB that they read
 // and write) with 1024 or 512 threads a row, 24.8 with 256 and 31.2 with 64; one
-// row of 4096 binary32 elements takes 3.5 us, 4.4 with 256, about two thirds of
-// it the launch and one memory round trip.  The weights are loaded before the
-// sum and the sum is reduced on DPP: with shuffles and a later load the two
-// took 24.5 and 3.7.  Rows longer than the registers of a workgroup
-// hold (kMaxGroups groups per thread) are read a second time instead.
+// row of 4096 binary32 elements takes 3.5 us, 4.4 with 256.  The weights' loads
+// stand before the sum and the sum is reduced on DPP: with shuffles and a later
+// load the two took 24.5 and 3.7.
+//
+// What bounds short calls: the launch (1.7 us) and round trips to memory one
+// after another.  Loads of binary32 operands are in flight together.  A group of
+// a 16-bit operand is widened within the branch that loads it, so the compiler
+// waits for it there: x, then res, then 16-bit weights are three round trips (24
+// rows of 8192 bfloat16 into Q8_1: 4.6 us, on 24 of 256 CUs), and a 16-bit row
+// that is not 16-byte aligned is eight per operand.  Into Q8_1 eight exact
+// divisions a thread come on top.  Rows longer than the registers of a workgroup
+// hold (kMaxGroups groups per thread) are read a second time.
 #include "dg_device.h"
 #include "dg_internal.h"
 #include "q81_rules.h"
@@ -222,7 +229,7 @@ k_rmsnorm(const typename E::raw* x, const typename E::raw* res, typename E::raw*
         for (int g = 0; g < G; ++g)
             if (k_first + g * step < K) load_h(k_first + g * step, v[g]);
 #pragma unroll
-        for (int g = 0; g < G; ++g)   // in flight during the sum
+        for (int g = 0; g < G; ++g)   // binary32 weights stay in flight during the sum
             if (k_first + g * step < K) load_weights8(w, wdtype, k_first + g * step, K, vw, wv[g]);
 #pragma unroll
         for (int g = 0; g < G; ++g)

@@ -6,7 +6,7 @@
 // every sum of them fits 62 bits and is exact, so it does not depend on the
 // order of summation, on the split of a row over workgroups or on the order
 // in which atomics arrive, and the same call gives the same token on any
-// launch shape.  A token with W_i = 0 (below 2^-F of the likeliest) has no
+// launch shape.  A token with W_i = 0 (below 2^-(F+1) of the likeliest) has no
 // part in anything.
 //
 // Rank order is value descending, index ascending, which is the descending
@@ -31,15 +31,24 @@
 //           in it the element that u falls into.  Up to 64 keys: every key against
 //           every other, in one wave; up to 1024: sorted, one per thread; more: a
 //           radix descent over the key bits that differ.
-// A row whose border bins hold more than kCand elements (many equal values)
-// is resolved by the same descent reading the row instead of the list.
+// A row whose border bins hold more than kCand elements is resolved by the same
+// descent reading the row, several times and from one workgroup, instead of the
+// list.  That is slow: 128256 equal logits with top-p take 560 us.  It happens to
+// many equal values, and to flat rows of which a token is masked with a finite
+// number, which stretches the bins over the whole range that has weight: 128000
+// logits of deviation 0.5 at temperature 1, top-p 0.9, take 25 us, and 408 with
+// one of them at the lowest value; 262144 of deviation 1, 28 and 915 (128000 of
+// deviation 1: 26 and 27).  Tokens masked with -infinity have no part in the bins.
 //
 // One row of 128256 float32 logits takes 18 us, four dependent launches of 3 to
-// 6 us; 256 rows of 128000 with top-p alone 124 us, bound by instruction issue
-// (the vector unit is busy for 87 to 90 % of hist and gather, which compute
-// every weight anew: 43 and 59 us) after a first pass at 6 TB/s (22 us).  64
-// rows of 128256 bfloat16 logits with mixed filters take 43 us; the pick sorts
-// their lists in 9.5 us, where the descent took 13.1.
+// 6 us (16 with one to five tokens allowed, 11 without top-k and top-p, 6.4 if
+// greedy); 256 rows of 128000 with top-p alone 123 us, bound by instruction issue
+// (the vector unit is busy for 82 to 86 % of hist and gather, which compute
+// every weight anew: 43.5 and 57.6 us) after a first pass at 5.9 TB/s (22 us).
+// 64 rows of 128256 bfloat16 logits with mixed filters take 43 us; the pick sorts
+// their lists in 9.2 us, where the descent took 13.1.  Rows of 4096 take 6.5 us
+// without top-k and top-p and 18 to 22 with them, in which the one workgroup's
+// descent has up to eight steps of several barriers each.
 #include "argkey.h"
 #include "dg_device.h"
 #include "dg_internal.h"
@@ -77,7 +86,10 @@ static_assert(kPer * kChunkThreads == kSubMin, "one load step per shortest sub-c
 // This thread's kPer elements of the kSubMin from c0 on (those at C and past
 // it as -infinity, which has no weight): consecutive ones in one or two
 // 16-byte loads where the row is 16-byte aligned, else a coalesced stride
-// apart.  element(i, vec) is the offset of the i-th from c0.
+// apart.  element(i, vec) is the offset of the i-th from c0.  Binary32 loads stay
+// in flight past load(), so that a step is loaded ahead of its use.  16-bit ones
+// do not: they are widened in the branch that loads them and waited for there,
+// eight times in rows that are not 16-byte aligned.
 template <class T>
 struct Share {
     float v[kPer];
@@ -394,9 +406,10 @@ k_sample_max(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs 
         }
         key = pack_key(best, bidx);
     } else {
-        // Per step only the largest image and the smallest value: 4 vector
-        // instructions an element for 20 (64 rows of 128256 bfloat16: 6.4 us for
-        // 8.4).  The place within the step is looked up once, by the lanes that
+        // Per step only the largest image and the smallest value: by the counters
+        // 9 vector instructions an element in place of 20, conversions and the
+        // rest of the launch included (256 rows of 128000 float32); 64 rows of
+        // 128256 bfloat16 take 6.4 us in place of 8.4.  The place within the step is looked up once, by the lanes that
         // hold the wave's maximum, at the cost of another round trip (one step:
         // 3.6 us for 3.1).
         int64_t at = c0;            // the step of `best`
@@ -472,7 +485,7 @@ k_sample_hist(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleArgs
     const int64_t c1 = c0 + (int64_t)a.subs_per_chunk * a.sub < a.C ? c0 + (int64_t)a.subs_per_chunk * a.sub : a.C;
     Share<T> ahead;
     const Params given = load_params(a, r);
-    ahead.load(row, c0, a.C, a.vec);   // in flight while the row's extremes arrive
+    ahead.load(row, c0, a.C, a.vec);   // binary32: in flight while the row's extremes arrive
     u64 top;
     float low;
     row_extremes(ws, a.G, &top, &low);
@@ -658,7 +671,7 @@ k_sample_gather(const T* __restrict__ x, RowSpace* __restrict__ spaces, SampleAr
     LaneBins bins;
     bins.load(ws);
     Share<T> ahead;
-    ahead.load(row, c0, a.C, a.vec);   // in flight while the row's extremes and bins arrive
+    ahead.load(row, c0, a.C, a.vec);   // binary32: in flight while the row's extremes and bins arrive
     u64 top;
     float low;
     row_extremes(ws, a.G, &top, &low);
