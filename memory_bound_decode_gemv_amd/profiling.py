@@ -61,11 +61,12 @@ KERNELS = {
     "gemv_q8_0_m1_28672x8192": (
         r"k_units<[^>]*UnitsQ8_0", "Q8_0 x Q8_1, M = 1, N = 28672, K = 8192",
         34 * 28672 * 8192 // 32 + 36 * 8192 // 32 + 4 * 28672,
-        ["gemv_m1_units.hip", "q4_common.h", "dg_device.h", "dg_internal.h"]),
+        ["gemv_m1_units.hip", "glu.h", "q4_common.h", "dg_device.h", "dg_internal.h"]),
     "gemv_q4_0_m16_4096x14336": (
         r"k_q(mfma|res)<", "Q4_0 x Q8_1, M = 16, N = 4096, K = 14336 (matrix cores)",
         18 * 4096 * 14336 // 32 + 16 * 36 * 14336 // 32 + 4 * 16 * 4096,
-        ["gemv_q4_0_mfma.hip", "gemv_qmfma_res.hip", "mfma_formats.h", "q4_common.h", "dg_device.h", "dg_internal.h"]),
+        ["gemv_q4_0_mfma.hip", "gemv_qmfma_res.hip", "glu.h", "mfma_formats.h", "q4_common.h", "dg_device.h",
+         "dg_internal.h"]),
     "gemv_f16_4096x4096": (
         r"k_gemv_wide<false", "fp16 GEMV, N = K = 4096",
         2 * 4096 * 4096 + 2 * 4096 + 2 * 4096,
@@ -73,7 +74,7 @@ KERNELS = {
     "gemv_nf4_28672x8192_b64": (
         r"k_nf4_rows<", "NF4 x bf16, M = 1, N = 28672, K = 8192, block 64",
         28672 * 8192 // 2 + 4 * 28672 * (8192 // 64) + 2 * 8192 + 64 + 4 * 28672,
-        ["gemv_nf4.hip", "dg_device.h", "dg_internal.h"]),
+        ["gemv_nf4.hip", "q4_common.h", "dg_device.h", "dg_internal.h"]),
     "stream_read_1GiB": (
         r"k_stream_read_wave<", "streaming read of 1 GiB", GIB,
         ["stream_read.hip", "dg_device.h"]),
