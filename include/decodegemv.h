@@ -619,6 +619,166 @@ dg_status dg_sample_rows(const void* x, int dtype, const float* u, const float* 
                          void* ws, size_t ws_bytes, dg_stream stream);
 
 /* ------------------------------------------------------------------------
+ * Penalties, biases and grammar masks on the logits of a batch
+ *
+ *   v = x[r][c]
+ *   repetition   if c is in the row's history:  v = v > 0 ? v / repetition[r] : v * repetition[r]
+ *   frequency,   if c is among the row's output (n > 0 times):
+ *   presence       v = (v - frequency[r] * n) - presence[r]
+ *   bias         v = v + bias[r][i], i the last entry of the row's list with bias_ids[r][i] = c
+ *   mask         v = -infinity unless bit c % 32 of mask[r][c / 32] is set
+ *   y[r][c] = v, rounded once to the type of x
+ *
+ * The step between the head and dg_sample_rows, dg_argmax_rows or
+ * dg_argcompare_rows.  A row's history is its prompt, tokens[r][0 ..
+ * prompt_lens[r] - 1], and its output, tokens[r][prompt_lens[r] .. lens[r] - 1].
+ * Arithmetic is binary32, every operation rounded by itself, IEEE on infinities
+ * and NaN; counts are exact.  Results do not depend on the batch or the launch.
+ *
+ *   x, y     device [R][ld] and [R][ldy] of `dtype`, aligned to the element.
+ *            y may be x itself (with ldy = ld); otherwise they may not
+ *            overlap.  Elements past C are neither read nor written.
+ *   R, C     0 <= R < 2^31, 0 <= C < 2^31 - 1 (0: nothing is launched).
+ *   a        the adjustments, in host memory, read during the call; NULL or
+ *            all zeros: y = x.  Its arrays are device memory, 4-byte aligned:
+ *     tokens       int32 [R][ldt], the first T of each row; or NULL.  A token
+ *                  outside 0..C-1 is ignored.
+ *     lens         int32 [R], or NULL for T everywhere; cut to 0..T.
+ *     prompt_lens  int32 [R], or NULL for 0; cut to 0..lens[r].
+ *     T, ldt       0 <= T <= ldt < 2^31.
+ *     repetition   float32 [R], or NULL: off.  0, a negative number, 1 or NaN:
+ *                  off for the row.
+ *     frequency, presence  float32 [R], or NULL for 0.
+ *     bias_ids, bias  int32 and float32 [R][B], both or neither.  An entry
+ *                  whose token is outside 0..C-1 is ignored.
+ *     bias_lens    int32 [R], or NULL for B everywhere; cut to 0..B.
+ *     B            0 <= B < 2^31.
+ *     mask         uint32 [R][ldm], or NULL: everything allowed.  A row that
+ *                  allows nothing is all -infinity.
+ *     ldm          >= ceil(C / 32) and < 2^31, with a mask.
+ * Errors: DG_ERR_ARG (dtype; one of bias_ids and bias without the other),
+ * DG_ERR_SHAPE, DG_ERR_NULL, DG_ERR_MISALIGNED, DG_ERR_HIP.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    const int32_t *tokens, *lens, *prompt_lens;
+    int64_t T, ldt;
+    const float *repetition, *frequency, *presence;
+    const int32_t* bias_ids;
+    const float* bias;
+    const int32_t* bias_lens;
+    int64_t B;
+    const uint32_t* mask;
+    int64_t ldm;
+} dg_adjustments;
+
+dg_status dg_adjust_rows(const void* x, void* y, int dtype, int64_t R, int64_t C, int64_t ld, int64_t ldy,
+                         const dg_adjustments* a, dg_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Routed experts: the router's choice, and the experts' feed-forward layer
+ *
+ * dg_moe_route: per token (row) m of logits x,
+ *   DG_ROUTE_SOFTMAX  s[e] = exp(x[m][e]) / sum_e' exp(x[m][e']),  rank by x[m][e]
+ *   DG_ROUTE_SIGMOID  s[e] = 1 / (1 + exp(-x[m][e])),              rank by s[e]
+ *   ids[m][0..k-1]     the k experts first in rank, the lowest index first on
+ *                      ties; with a bias the rank is by s[e] + bias[e]
+ *   weights[m][j]      s[ids[m][j]], divided by their sum over j if `renorm`,
+ *                      times `scale`
+ * Scores, sums and ranks are binary64, the weights rounded once.  An expert
+ * whose logit is NaN or -infinity, or whose biased rank is, is never chosen (it
+ * adds nothing to the softmax's sum; +infinity shares all of it among the
+ * infinite ones); where fewer than k are left, the row's last ids are -1 and
+ * their weights 0.  Weights whose sum is 0 are 0.
+ *
+ *   x        device [M][ld] of `dtype`, aligned to the element.
+ *   bias     device float32 [E], or NULL.
+ *   ids      device int32 [M][k].   weights  device float32 [M][k].
+ *   M        0 <= M < 2^31 (0 launches nothing).  1 <= E <= 1024, E <= ld < 2^31,
+ *            1 <= k <= 64, k <= E.   scale finite.
+ * Errors: DG_ERR_ARG (dtype, score, scale), DG_ERR_SHAPE, DG_ERR_NULL,
+ * DG_ERR_MISALIGNED, DG_ERR_HIP.
+ *
+ * dg_moe_q4_0, dg_moe_q8_0: the layer of a few tokens through the experts that
+ * they were routed to,
+ *   H[m][j] = Q8_1( act(Wg[e] X[m]) * (Wu[e] X[m]) ),   e = ids[m][j]
+ *   Y[m]    = sum_j weights[m][j] * (Wd[e] H[m][j])
+ * The products are those of dg_gemv_*_tiles_glu and dg_gemv_*_tiles (exact int32
+ * block sums, exact scale products, fp32 sums over blocks, the activations of
+ * DG_ACT_*), H is what dg_quantize_q8_1 makes of the fp32 products, and the
+ * weighted sum is fp32 in the order of j.  Results are bit-reproducible, and a
+ * token's do not depend on the other tokens of the call.  Each chosen expert's
+ * weights are read once for every 16 of its tokens.
+ *
+ *   Wg, Wu   device, the experts' gate and up matrices in 16-row tiles, one
+ *            after the other: what dg_repack_q4_0_tiles / dg_repack_q8_0_tiles
+ *            makes of the [E * N][K] stack; 16-byte aligned.
+ *   Wd       device, the same of the down matrices, the [E * K][N] stack.
+ *   Xq       device, M columns of K/32 Q8_1 blocks, 16-byte aligned.
+ *   ids      device int32 [M][k].  An id outside 0..E-1 is no expert: the slot
+ *            adds nothing, its weight is not read.  An id may come twice.
+ *   weights  device float32 [M][k].
+ *   Y        device [M][K] of `ydtype`, aligned to the element; a token
+ *            without experts gets zeros.
+ *   N, K     multiples of 256, 0 <= N, K <= 2^26; E * N, E * K < 2^31.
+ *            K = 0 launches nothing; N = 0 gives Y = 0.
+ *   M, E, k  0 <= M <= 4096, 1 <= E <= 1024, k >= 0, M * k <= 4096.  M = 0
+ *            launches nothing; k = 0 gives Y = 0.
+ *   ws       device workspace of dg_moe_workspace_bytes(N, K, M, k) bytes,
+ *            16-byte aligned; contents on entry do not matter; the call owns it
+ *            until the stream passes the call.  It starts with H: column
+ *            m * k + j of N/32 Q8_1 blocks (where ids[m][j] is an expert).
+ * Errors: DG_ERR_ARG (act, ydtype), DG_ERR_SHAPE, DG_ERR_NULL,
+ * DG_ERR_MISALIGNED, DG_ERR_WORKSPACE, DG_ERR_HIP.
+ * ------------------------------------------------------------------------ */
+enum { DG_ROUTE_SOFTMAX = 0, DG_ROUTE_SIGMOID = 1 };
+
+dg_status dg_moe_route(const void* x, int dtype, const float* bias, int32_t* ids, float* weights, int64_t M, int64_t E,
+                       int64_t ld, int k, int score, int renorm, float scale, dg_stream stream);
+
+size_t dg_moe_workspace_bytes(int64_t N, int64_t K, int64_t M, int k);
+dg_status dg_moe_q4_0(const void* Wg, const void* Wu, const void* Wd, const void* Xq, const int32_t* ids,
+                      const float* weights, void* Y, int ydtype, int64_t N, int64_t K, int64_t M, int64_t E, int k,
+                      int act, void* ws, size_t ws_bytes, dg_stream stream);
+dg_status dg_moe_q8_0(const void* Wg, const void* Wu, const void* Wd, const void* Xq, const int32_t* ids,
+                      const float* weights, void* Y, int ydtype, int64_t N, int64_t K, int64_t M, int64_t E, int k,
+                      int act, void* ws, size_t ws_bytes, dg_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection
+ *
+ *   Y[m][n] = base[m][n] + scale[a] * sum_{r < ranks[a]} B[a][n][r] * h[r],
+ *   h[r]    = sum_k A[a][r][k] * x[m][k],   a = adapter[m]
+ *
+ * The projection's output (the Y of a GEMV) with the product of each row's own
+ * adapter added to it.  Products of the 16-bit weights are exact in fp32 or
+ * rounded once, sums are fp32, and so is h.  Rows without an adapter get their
+ * base.  Results are bit-reproducible, and a row's do not depend on the other
+ * rows of the call.
+ *
+ *   x        device [M][ld] of `dtype`, 16-byte aligned; ld a multiple of 8.
+ *   A        device [L][R][K] of `wdtype` (DG_DTYPE_F16 or DG_DTYPE_BF16),
+ *            16-byte aligned.   B  device [L][N][R], the same.
+ *   adapter  device int32 [M].  A value outside 0..L-1: no adapter.
+ *   scale    device float32 [L], or NULL for 1.
+ *   ranks    device int32 [L], or NULL for R; cut to 0..R.  Rows of A and
+ *            columns of B from ranks[a] on add nothing, whatever they hold.
+ *   base     device float32 [M][N], or NULL for 0.  It may be Y itself.
+ *   Y        device float32 [M][N].
+ *   M        0 <= M < 2^31.  N: 0 <= N < 2^31.  M = 0 or N = 0 launches nothing.
+ *   K        a multiple of 8, 0 <= K <= ld < 2^31; 0: h = 0.
+ *   R        a multiple of 8, 8 <= R <= 512.   L  0 <= L < 2^31.
+ *   ws       device workspace of dg_lora_workspace_bytes(M, K, R) bytes,
+ *            16-byte aligned; contents on entry do not matter; the call owns it
+ *            until the stream passes the call.
+ * Errors: DG_ERR_ARG (dtype, wdtype), DG_ERR_SHAPE, DG_ERR_NULL,
+ * DG_ERR_MISALIGNED, DG_ERR_WORKSPACE, DG_ERR_HIP.
+ * ------------------------------------------------------------------------ */
+size_t dg_lora_workspace_bytes(int64_t M, int64_t K, int64_t R);
+dg_status dg_lora_rows(const void* x, int dtype, const void* A, const void* B, int wdtype, const int32_t* adapter,
+                       const float* scale, const int32_t* ranks, const float* base, float* Y, int64_t M, int64_t N,
+                       int64_t K, int64_t R, int64_t L, int64_t ld, void* ws, size_t ws_bytes, dg_stream stream);
+
+/* ------------------------------------------------------------------------
  * Launch overrides (measurement and A/B runs)
  *
  * The *_ex variants take a launch configuration instead of the library's

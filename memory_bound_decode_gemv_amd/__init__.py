@@ -48,6 +48,8 @@ DG_ACT_SILU = 0
 DG_ACT_GELU = 1
 DG_ACT_GELU_TANH = 2
 DG_ACT_RELU = 3
+DG_ROUTE_SOFTMAX = 0
+DG_ROUTE_SIGMOID = 1
 
 DG_VARIANT_DENSE_WIDE = 1
 DG_VARIANT_DENSE_XREG = 2
@@ -86,6 +88,9 @@ EXPORTED = (
     "dg_sample_workspace_bytes", "dg_sample_rows",
     "dg_gemv_q4_0_glu", "dg_gemv_q8_0_glu",
     "dg_gemv_q4_0_tiles_glu", "dg_gemv_q8_0_tiles_glu",
+    "dg_adjust_rows",
+    "dg_moe_route", "dg_moe_workspace_bytes", "dg_moe_q4_0", "dg_moe_q8_0",
+    "dg_lora_workspace_bytes", "dg_lora_rows",
 )
 
 # Size of the library's fixed per-device argmax key array (include/decodegemv.h).
@@ -104,6 +109,14 @@ class DGError(RuntimeError):
 class dg_launch(ctypes.Structure):
     _fields_ = [("variant", ctypes.c_int), ("grid", ctypes.c_int),
                 ("block", ctypes.c_int), ("unroll", ctypes.c_int)]
+
+
+class dg_adjustments(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("prompt_lens", ctypes.c_void_p),
+                ("T", ctypes.c_int64), ("ldt", ctypes.c_int64),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("bias_lens", ctypes.c_void_p),
+                ("B", ctypes.c_int64), ("mask", ctypes.c_void_p), ("ldm", ctypes.c_int64)]
 
 
 _handle = None
@@ -209,6 +222,20 @@ def _lib():
         getattr(lib, f"dg_gemv_{f}_glu").restype = st
         getattr(lib, f"dg_gemv_{f}_tiles_glu").argtypes = [P, P, P, P, I64, I64, I32, I32, P]
         getattr(lib, f"dg_gemv_{f}_tiles_glu").restype = st
+    lib.dg_adjust_rows.argtypes = [P, P, I32, I64, I64, I64, I64, ctypes.POINTER(dg_adjustments), P]
+    lib.dg_adjust_rows.restype = st
+    lib.dg_moe_route.argtypes = [P, I32, P, P, P, I64, I64, I64, I32, I32, I32, F32, P]
+    lib.dg_moe_route.restype = st
+    lib.dg_moe_workspace_bytes.argtypes = [I64, I64, I64, I32]
+    lib.dg_moe_workspace_bytes.restype = ctypes.c_size_t
+    for f in ("q4_0", "q8_0"):
+        getattr(lib, f"dg_moe_{f}").argtypes = [P, P, P, P, P, P, P, I32, I64, I64, I64, I64, I32, I32, P,
+                                                ctypes.c_size_t, P]
+        getattr(lib, f"dg_moe_{f}").restype = st
+    lib.dg_lora_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.dg_lora_workspace_bytes.restype = ctypes.c_size_t
+    lib.dg_lora_rows.argtypes = [P, I32, P, P, I32, P, P, P, P, P, I64, I64, I64, I64, I64, I64, P, ctypes.c_size_t, P]
+    lib.dg_lora_rows.restype = st
     _handle = lib
     return lib
 
@@ -839,3 +866,152 @@ def dg_sample_rows(x, u, idx, R=None, C=None, ld=None, temperature=None, top_k=N
                                  C, ld, _arg("ws", ws, dev, torch.uint8, 0), ws.nbytes if ws is not None else 0,
                                  _stream_here(stream, dev)), "dg_sample_rows")
     return idx
+
+
+def dg_adjust_rows(x, y, tokens=None, lens=None, prompt_lens=None, repetition=None, frequency=None, presence=None,
+                   bias_ids=None, bias=None, bias_lens=None, mask=None, R=None, C=None, ld=None, ldy=None,
+                   stream=None):
+    """y [R][ldy] = the logits x [R][ld] (both float32, float16 or bfloat16; y may be x) after the penalties of their
+    histories, biases and masks.  tokens: int32 [R][T], the first lens[r] of a row (int32 [R]; None: T) its prompt of
+    prompt_lens[r] tokens (int32 [R]; None: 0), then its output; repetition, frequency, presence: float32 [R];
+    bias_ids, bias: int32 and float32 [R][B], the first bias_lens[r] of a row (int32 [R]; None: B), the last one of a
+    token counts; mask: int32 [R][words], bit c % 32 of word c / 32 set where token c is allowed.  Each may be None."""
+    torch = _torch()
+    i32, f32 = torch.int32, torch.float32
+    dev = _here(x, "x")
+    dtype = _dtype_id(x, "x")
+    if R is None:
+        R = _rows(x, "x", "R")
+    if C is None:
+        C = x.shape[-1]
+    if ld is None:
+        ld = x.shape[-1]
+    if ldy is None:
+        ldy = y.shape[-1]
+    R, C, ld, ldy = int(R), int(C), int(ld), int(ldy)
+    n, e = max(R, 0), x.element_size()
+    live = R > 0 and C > 0
+    xa = _arg("x", x, dev, x.dtype, ((R - 1) * ld + C) * e if live and ld >= C else 0)
+    ya = _arg("y", y, dev, x.dtype, ((R - 1) * ldy + C) * e if live and ldy >= C else 0)
+    T = B = ldm = 0
+    if tokens is not None:
+        T = tokens.shape[-1]
+    if bias_ids is not None:
+        B = bias_ids.shape[-1]
+    if mask is not None:
+        ldm = mask.shape[-1]
+    a = dg_adjustments(
+        _arg("tokens", tokens, dev, i32, n * T * 4), _arg("lens", lens, dev, i32, n * 4),
+        _arg("prompt_lens", prompt_lens, dev, i32, n * 4), T, T, _arg("repetition", repetition, dev, f32, n * 4),
+        _arg("frequency", frequency, dev, f32, n * 4), _arg("presence", presence, dev, f32, n * 4),
+        _arg("bias_ids", bias_ids, dev, i32, n * B * 4), _arg("bias", bias, dev, f32, n * B * 4),
+        _arg("bias_lens", bias_lens, dev, i32, n * 4), B, _arg("mask", mask, dev, i32, n * ldm * 4), ldm)
+    _check(_lib().dg_adjust_rows(xa, ya, dtype, R, C, ld, ldy, a, _stream_here(stream, dev)), "dg_adjust_rows")
+    return y
+
+
+_SCORES = {"softmax": DG_ROUTE_SOFTMAX, "sigmoid": DG_ROUTE_SIGMOID}
+
+
+def dg_moe_route(x, ids, weights, bias=None, M=None, E=None, ld=None, k=None, score="softmax", renorm=True, scale=1.0,
+                 stream=None):
+    """ids (int32 [M][k]) and weights (float32 [M][k]) = the k experts of each token (row) of the router's logits x
+    (float32, float16 or bfloat16 [M][ld]); score: "softmax" or "sigmoid"; bias: float32 [E], added to the scores for
+    the choice alone."""
+    torch = _torch()
+    dev = _here(x, "x")
+    dtype = _dtype_id(x, "x")
+    if M is None:
+        M = _rows(x, "x", "M")
+    if E is None:
+        E = x.shape[-1]
+    if ld is None:
+        ld = x.shape[-1]
+    if k is None:
+        k = ids.shape[-1]
+    M, E, ld, k = int(M), int(E), int(ld), int(k)
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {tuple(_SCORES)}, not {score!r}")
+    n = M * k * 4 if M > 0 and k > 0 else 0
+    xa = _arg("x", x, dev, x.dtype, ((M - 1) * ld + E) * x.element_size() if M > 0 and ld >= E > 0 else 0)
+    _check(_lib().dg_moe_route(xa, dtype, _arg("bias", bias, dev, torch.float32, max(E, 0) * 4),
+                               _arg("ids", ids, dev, torch.int32, n), _arg("weights", weights, dev, torch.float32, n),
+                               M, E, ld, k, _SCORES[score],
+                               1 if renorm else 0, scale, _stream_here(stream, dev)), "dg_moe_route")
+    return ids, weights
+
+
+def dg_moe_workspace_bytes(N, K, M, k):
+    return int(_lib().dg_moe_workspace_bytes(int(N), int(K), int(M), int(k)))
+
+
+def _moe(fmt, block_bytes, Wg, Wu, Wd, Xq, ids, weights, Y, N, K, M, E, k, act, ws, stream):
+    torch = _torch()
+    u8 = torch.uint8
+    dev = _here(Y, "Y")
+    ydtype = _dtype_id(Y, "Y")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {tuple(_ACTS)}, not {act!r}")
+    if k is None:
+        k = ids.shape[-1]
+    N, K, M, E, k = int(N), int(K), int(M), int(E), int(k)
+    live = N > 0 and K > 0 and M > 0 and k > 0
+    one = max(E, 0) * N * (K // 32) * block_bytes if live else 0
+    n = M * k * 4 if live else 0
+    _check(getattr(_lib(), f"dg_moe_{fmt}")(
+        _arg("Wg", Wg, dev, u8, one), _arg("Wu", Wu, dev, u8, one), _arg("Wd", Wd, dev, u8, one),
+        _arg("Xq", Xq, dev, u8, M * (K // 32) * 36 if live else 0), _arg("ids", ids, dev, torch.int32, n),
+        _arg("weights", weights, dev, torch.float32, n), _arg("Y", Y, dev, Y.dtype, max(M * K, 0) * Y.element_size()),
+        ydtype, N, K, M, E, k, _ACTS[act], _arg("ws", ws, dev, u8, 0), ws.nbytes if ws is not None else 0,
+        _stream_here(stream, dev)), f"dg_moe_{fmt}")
+    return Y
+
+
+def dg_moe_q4_0(Wg, Wu, Wd, Xq, ids, weights, Y, N, K, M, E, k=None, act="silu", ws=None, stream=None):
+    """Y (float32, float16 or bfloat16 [M][K]) = the feed-forward layer of Q8_1 columns Xq through the experts
+    ids (int32 [M][k]) with weights (float32 [M][k]).  Wg, Wu: the tiled copies of the experts' stacked Q4_0 gate and
+    up matrices (E * N rows of K), Wd: of the down matrices (E * K rows of N).  ws: a device workspace of
+    dg_moe_workspace_bytes(N, K, M, k) bytes."""
+    return _moe("q4_0", 18, Wg, Wu, Wd, Xq, ids, weights, Y, N, K, M, E, k, act, ws, stream)
+
+
+def dg_moe_q8_0(Wg, Wu, Wd, Xq, ids, weights, Y, N, K, M, E, k=None, act="silu", ws=None, stream=None):
+    """As dg_moe_q4_0, from tiled Q8_0 matrices."""
+    return _moe("q8_0", 34, Wg, Wu, Wd, Xq, ids, weights, Y, N, K, M, E, k, act, ws, stream)
+
+
+def dg_lora_workspace_bytes(M, K, R):
+    return int(_lib().dg_lora_workspace_bytes(int(M), int(K), int(R)))
+
+
+def dg_lora_rows(x, A, B, adapter, Y, base=None, scale=None, ranks=None, M=None, N=None, K=None, R=None, L=None,
+                 ld=None, ws=None, stream=None):
+    """Y (float32 [M][N]) = base (float32 [M][N], Y itself, or None for 0) + scale[a] * B[a] (A[a] x[m]), a =
+    adapter[m] (int32 [M]; outside 0..L-1: no adapter).  x: float32, float16 or bfloat16 [M][ld]; A: float16 or
+    bfloat16 [L][R][K]; B: like A [L][N][R]; scale: float32 [L] or None; ranks: int32 [L] or None.  ws: a device
+    workspace of dg_lora_workspace_bytes(M, K, R) bytes."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    dev = _here(x, "x")
+    dtype, wdtype = _dtype_id(x, "x"), _dtype_id(A, "A")
+    if A.dim() == 3:
+        L = A.shape[0] if L is None else L
+        R = A.shape[1] if R is None else R
+        K = A.shape[2] if K is None else K
+    if M is None:
+        M = _rows(x, "x", "M")
+    if N is None:
+        N = Y.shape[-1]
+    if ld is None:
+        ld = x.shape[-1]
+    M, N, K, R, L, ld = int(M), int(N), int(K), int(R), int(L), int(ld)
+    live = M > 0 and N > 0 and L > 0 and R > 0
+    out = M * N * 4 if M > 0 and N > 0 else 0
+    xa = _arg("x", x, dev, x.dtype, ((M - 1) * ld + K) * x.element_size() if live and ld >= K > 0 else 0)
+    _check(_lib().dg_lora_rows(xa, dtype, _arg("A", A, dev, A.dtype, L * R * K * 2 if live else 0),
+                               _arg("B", B, dev, A.dtype, L * N * R * 2 if live else 0), wdtype,
+                               _arg("adapter", adapter, dev, i32, M * 4), _arg("scale", scale, dev, f32, L * 4),
+                               _arg("ranks", ranks, dev, i32, L * 4), _arg("base", base, dev, f32, out),
+                               _arg("Y", Y, dev, f32, out), M, N, K, R, L, ld, _arg("ws", ws, dev, torch.uint8, 0),
+                               ws.nbytes if ws is not None else 0, _stream_here(stream, dev)), "dg_lora_rows")
+    return Y

@@ -181,6 +181,28 @@ dg_status rmsnorm_checked(const RmsNorm& a, dg_stream stream) {
     return hip_status(launch_rmsnorm(a, (hipStream_t)stream));
 }
 
+bool moe_shape_ok(int64_t N, int64_t K, int64_t M, int k) {
+    return N >= 0 && N <= kQuantMaxK && N % 256 == 0 && K >= 0 && K <= kQuantMaxK && K % 256 == 0 && M >= 0 &&
+           M <= 4096 && k >= 0 && k <= 4096 && M * k <= 4096;
+}
+
+dg_status moe_checked(const MoeLayer& q, size_t ws_bytes, dg_stream stream) {
+    if (q.act < DG_ACT_SILU || q.act > DG_ACT_RELU || !dtype_ok(q.ydtype)) return DG_ERR_ARG;
+    if (!moe_shape_ok(q.N, q.K, q.M, q.k) || q.E < 1 || q.E > 1024 || q.E * q.N > kI32Max || q.E * q.K > kI32Max)
+        return DG_ERR_SHAPE;
+    if (q.M == 0 || q.K == 0) return DG_OK;
+    const bool live = q.N > 0 && q.k > 0;
+    if (!q.Y || (live && (!q.Wg || !q.Wu || !q.Wd || !q.Xq || !q.ids || !q.weights))) return DG_ERR_NULL;
+    if (!aligned(q.Y, dtype_size(q.ydtype))) return DG_ERR_MISALIGNED;
+    if (live && (!aligned(q.Wg, 16) || !aligned(q.Wu, 16) || !aligned(q.Wd, 16) || !aligned(q.Xq, 16) ||
+                 !aligned(q.ids, 4) || !aligned(q.weights, 4)))
+        return DG_ERR_MISALIGNED;
+    const size_t need = live ? moe_workspace_bytes(q.N, q.K, q.M, q.k) : 0;
+    if (need > 0 && (!q.ws || ws_bytes < need)) return DG_ERR_WORKSPACE;
+    if (q.ws && !aligned(q.ws, 16)) return DG_ERR_MISALIGNED;
+    return hip_status(launch_moe(q, (hipStream_t)stream));
+}
+
 }  // namespace
 
 int device_cu_count() {
@@ -507,6 +529,81 @@ dg_status dg_gemv_q8_0_glu(const void* Wg, const void* Wu, const void* Xq, float
 dg_status dg_gemv_q8_0_tiles_glu(const void* Wg, const void* Wu, const void* Xq, float* Y, int64_t N, int64_t K, int M,
                                  int act, dg_stream stream) {
     return gemv_glu_checked(true, true, Wg, Wu, Xq, Y, N, K, M, act, stream);
+}
+
+dg_status dg_adjust_rows(const void* x, void* y, int dtype, int64_t R, int64_t C, int64_t ld, int64_t ldy,
+                         const dg_adjustments* adjustments, dg_stream stream) {
+    dg_adjustments a = {};
+    if (adjustments) a = *adjustments;
+    if (!dtype_ok(dtype) || !a.bias_ids != !a.bias) return DG_ERR_ARG;
+    if (R < 0 || R > kI32Max || C < 0 || C >= kI32Max || ld < C || ld > kI32Max || ldy < C || ldy > kI32Max)
+        return DG_ERR_SHAPE;
+    if (a.tokens && (a.T < 0 || a.ldt < a.T || a.ldt > kI32Max)) return DG_ERR_SHAPE;
+    if (a.bias && (a.B < 0 || a.B > kI32Max)) return DG_ERR_SHAPE;
+    if (a.mask && (a.ldm < (C + 31) / 32 || a.ldm > kI32Max)) return DG_ERR_SHAPE;
+    if (x == y && x && ldy != ld && R > 1) return DG_ERR_SHAPE;   // rows would overlap others
+    if (R == 0 || C == 0) return DG_OK;
+    if (!x || !y) return DG_ERR_NULL;
+    const uintptr_t e = dtype_size(dtype);
+    if (!aligned(x, e) || !aligned(y, e) || !aligned(a.tokens, 4) || !aligned(a.lens, 4) || !aligned(a.prompt_lens, 4) ||
+        !aligned(a.repetition, 4) || !aligned(a.frequency, 4) || !aligned(a.presence, 4) || !aligned(a.bias_ids, 4) ||
+        !aligned(a.bias, 4) || !aligned(a.bias_lens, 4) || !aligned(a.mask, 4))
+        return DG_ERR_MISALIGNED;
+    return hip_status(launch_adjust_rows({x, y, dtype, R, C, ld, ldy, a}, (hipStream_t)stream));
+}
+
+dg_status dg_moe_route(const void* x, int dtype, const float* bias, int32_t* ids, float* weights, int64_t M, int64_t E,
+                       int64_t ld, int k, int score, int renorm, float scale, dg_stream stream) {
+    if (!dtype_ok(dtype) || (score != DG_ROUTE_SOFTMAX && score != DG_ROUTE_SIGMOID) ||
+        !(scale >= -3.4028234e38f && scale <= 3.4028234e38f))
+        return DG_ERR_ARG;
+    if (M < 0 || M > kI32Max || E < 1 || E > 1024 || ld < E || ld > kI32Max || k < 1 || k > 64 || k > E)
+        return DG_ERR_SHAPE;
+    if (M == 0) return DG_OK;
+    if (!x || !ids || !weights) return DG_ERR_NULL;
+    if (!aligned(x, dtype_size(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+        return DG_ERR_MISALIGNED;
+    return hip_status(launch_moe_route({x, dtype, bias, ids, weights, M, E, ld, k, score, renorm != 0, scale},
+                                       (hipStream_t)stream));
+}
+
+size_t dg_moe_workspace_bytes(int64_t N, int64_t K, int64_t M, int k) {
+    return moe_shape_ok(N, K, M, k) ? moe_workspace_bytes(N, K, M, k) : 0;
+}
+
+dg_status dg_moe_q4_0(const void* Wg, const void* Wu, const void* Wd, const void* Xq, const int32_t* ids,
+                      const float* weights, void* Y, int ydtype, int64_t N, int64_t K, int64_t M, int64_t E, int k,
+                      int act, void* ws, size_t ws_bytes, dg_stream stream) {
+    return moe_checked({false, Wg, Wu, Wd, Xq, ids, weights, Y, ydtype, N, K, M, E, k, act, ws}, ws_bytes, stream);
+}
+
+dg_status dg_moe_q8_0(const void* Wg, const void* Wu, const void* Wd, const void* Xq, const int32_t* ids,
+                      const float* weights, void* Y, int ydtype, int64_t N, int64_t K, int64_t M, int64_t E, int k,
+                      int act, void* ws, size_t ws_bytes, dg_stream stream) {
+    return moe_checked({true, Wg, Wu, Wd, Xq, ids, weights, Y, ydtype, N, K, M, E, k, act, ws}, ws_bytes, stream);
+}
+
+size_t dg_lora_workspace_bytes(int64_t M, int64_t K, int64_t R) {
+    return M < 0 || M > kI32Max || K < 0 || K > kI32Max || R < 8 || R > 512 ? 0 : lora_workspace_bytes(M, K, R);
+}
+
+dg_status dg_lora_rows(const void* x, int dtype, const void* A, const void* B, int wdtype, const int32_t* adapter,
+                       const float* scale, const int32_t* ranks, const float* base, float* Y, int64_t M, int64_t N,
+                       int64_t K, int64_t R, int64_t L, int64_t ld, void* ws, size_t ws_bytes, dg_stream stream) {
+    if (!dtype_ok(dtype) || (wdtype != DG_DTYPE_F16 && wdtype != DG_DTYPE_BF16)) return DG_ERR_ARG;
+    if (M < 0 || M > kI32Max || N < 0 || N > kI32Max || K < 0 || K % 8 != 0 || ld < K || ld % 8 != 0 || ld > kI32Max ||
+        R < 8 || R > 512 || R % 8 != 0 || L < 0 || L > kI32Max)
+        return DG_ERR_SHAPE;
+    if (M == 0 || N == 0) return DG_OK;
+    if (!Y || !adapter || (L > 0 && (!B || (K > 0 && (!x || !A))))) return DG_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(adapter, 4) || !aligned(scale, 4) ||
+        !aligned(ranks, 4) || !aligned(base, 4) || !aligned(Y, 4))
+        return DG_ERR_MISALIGNED;
+    const size_t need = lora_workspace_bytes(M, K, R);
+    if (need > 0 && (!ws || ws_bytes < need)) return DG_ERR_WORKSPACE;
+    if (ws && !aligned(ws, 16)) return DG_ERR_MISALIGNED;
+    return hip_status(launch_lora_rows({x, dtype, A, B, wdtype, adapter, scale, ranks, base, Y, M, N, K, R, L, ld, ws},
+                                       (hipStream_t)stream));
 }
 
 }  // extern "C"
