@@ -652,7 +652,7 @@ dg_status dg_sample_rows(const void* x, int dtype, const float* u, const float* 
  *     bias_ids, bias  int32 and float32 [R][B], both or neither.  An entry
  *                  whose token is outside 0..C-1 is ignored.
  *     bias_lens    int32 [R], or NULL for B everywhere; cut to 0..B.
- *     B            0 <= B < 2^31.
+ *     B            0 <= B <= 65535.
  *     mask         uint32 [R][ldm], or NULL: everything allowed.  A row that
  *                  allows nothing is all -infinity.
  *     ldm          >= ceil(C / 32) and < 2^31, with a mask.

@@ -539,7 +539,7 @@ dg_status dg_adjust_rows(const void* x, void* y, int dtype, int64_t R, int64_t C
     if (R < 0 || R > kI32Max || C < 0 || C >= kI32Max || ld < C || ld > kI32Max || ldy < C || ldy > kI32Max)
         return DG_ERR_SHAPE;
     if (a.tokens && (a.T < 0 || a.ldt < a.T || a.ldt > kI32Max)) return DG_ERR_SHAPE;
-    if (a.bias && (a.B < 0 || a.B > kI32Max)) return DG_ERR_SHAPE;
+    if (a.bias && (a.B < 0 || a.B > 65535)) return DG_ERR_SHAPE;
     if (a.mask && (a.ldm < (C + 31) / 32 || a.ldm > kI32Max)) return DG_ERR_SHAPE;
     if (x == y && x && ldy != ld && R > 1) return DG_ERR_SHAPE;   // rows would overlap others
     if (R == 0 || C == 0) return DG_OK;

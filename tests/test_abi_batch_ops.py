@@ -138,7 +138,7 @@ B = P(0x2000)
     ((A, A, F32, 4, 100, 100, 104), {}, SHAPE),          # in place, with other rows
     ((A, B, F32, 4, 100, 100, 100), dict(T=11), SHAPE), ((A, B, F32, 4, 100, 100, 100), dict(T=-1), SHAPE),
     ((A, B, F32, 4, 100, 100, 100), dict(ldt=1 << 31), SHAPE),
-    ((A, B, F32, 4, 100, 100, 100), dict(B=-1), SHAPE), ((A, B, F32, 4, 100, 100, 100), dict(B=1 << 31), SHAPE),
+    ((A, B, F32, 4, 100, 100, 100), dict(B=-1), SHAPE), ((A, B, F32, 4, 100, 100, 100), dict(B=65536), SHAPE),
     ((A, B, F32, 4, 100, 100, 100), dict(ldm=3), SHAPE), ((A, B, F32, 4, 100, 100, 100), dict(ldm=1 << 31), SHAPE),
     ((None, B, F32, 4, 100, 100, 100), {}, NULL), ((A, None, F32, 4, 100, 100, 100), {}, NULL),
     ((P(0x1002), B, F32, 4, 100, 100, 100), {}, MISALIGNED), ((A, P(0x1001), F16, 4, 100, 100, 100), {}, MISALIGNED),
