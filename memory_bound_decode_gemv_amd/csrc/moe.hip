@@ -16,6 +16,7 @@
 // slot leave; otherwise they stand for experts.  No list is built beforehand, so
 // no launch is spent on one.
 #include <algorithm>
+#include <type_traits>
 
 #include "dg_internal.h"
 #include "q81_rules.h"
@@ -31,83 +32,162 @@ constexpr int kTileColumns = 16;
 
 // ---------------------------------------------------------------------------
 // The router: one wave per token, NV experts per lane (e = lane + 64 i).
+//
+// An expert's rank is a whole number that orders as its binary32 logit (softmax
+// without a bias) or its binary64 score does; 0 is none, which no finite number
+// and no infinity but the lowest maps to.  Each of the k choices is a maximum over
+// the wave, then the lowest place that holds it.  Scores of softmax ranked by
+// their logits are made for the chosen alone, in the lanes that store them; the
+// softmax's sum is left out where the weights are divided by their own.
 // ---------------------------------------------------------------------------
-template <class T>
-__device__ __forceinline__ float widen(T v) { return (float)v; }
-
 struct RouteArgs {
     const float* bias;
     int32_t* ids;
     float* weights;
     int64_t M, ld, first;
-    int E, k, score, renorm;
+    int E, k, renorm;
     float scale;
 };
 
 constexpr int kRouteRows = 4;   // waves of a workgroup
 
-template <class T, int NV>
+__device__ __forceinline__ uint32_t rank_bits(float v) {   // -0 as +0
+    const uint32_t u = __builtin_bit_cast(uint32_t, v + 0.0f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t rank_bits(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
+    return u ^ ((uint64_t)((int64_t)u >> 63) | ((uint64_t)1 << 63));
+}
+__device__ __forceinline__ float from_rank(uint32_t r) {
+    return __builtin_bit_cast(float, r ^ ((r >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {   // lanes without a source give 0
+    v = max(v, dpp_mov_u32<kDppRowShr1, 0xF>(v));
+    v = max(v, dpp_mov_u32<kDppRowShr2, 0xF>(v));
+    v = max(v, dpp_mov_u32<kDppRowShr4, 0xF>(v));
+    v = max(v, dpp_mov_u32<kDppRowShr8, 0xF>(v));
+    v = max(v, dpp_mov_u32<kDppRowBcast15, 0xA>(v));
+    v = max(v, dpp_mov_u32<kDppRowBcast31, 0xC>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {   // high words, then the low ones beside the highest
+    const uint32_t hi = wave_max((uint32_t)(v >> 32));
+    const uint32_t lo = wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+    return ((uint64_t)hi << 32) | lo;
+}
+
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_add_f64(double v) {   // lanes without a source add 0
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = dpp_mov_u32<CTRL, ROW_MASK>((uint32_t)u);
+    const uint32_t hi = dpp_mov_u32<CTRL, ROW_MASK>((uint32_t)(u >> 32));
+    return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double readlane_f64(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+    v = dpp_add_f64<kDppRowShr1, 0xF>(v);
+    v = dpp_add_f64<kDppRowShr2, 0xF>(v);
+    v = dpp_add_f64<kDppRowShr4, 0xF>(v);
+    v = dpp_add_f64<kDppRowShr8, 0xF>(v);
+    v = dpp_add_f64<kDppRowBcast15, 0xA>(v);
+    v = dpp_add_f64<kDppRowBcast31, 0xC>(v);
+    return readlane_f64(v, 63);
+}
+
+// exp(v - top), 1 at the top itself (which may be infinite).
+__device__ __forceinline__ double softmax_term(float v, float top) {
+    return v == top ? 1.0 : exp((double)v - (double)top);
+}
+
+// BY_LOGIT: softmax without a bias.  SOFTMAX: softmax with one, else sigmoid.
+template <class T, int NV, bool BY_LOGIT, bool SOFTMAX>
 __global__ void __launch_bounds__(64 * kRouteRows) k_moe_route(const T* __restrict__ x, RouteArgs a) {
+    using Rank = typename std::conditional<BY_LOGIT, uint32_t, uint64_t>::type;
+    constexpr float kNone = -__builtin_huge_valf();
     const int lane = lane_id();
     const int64_t m = a.first + (int64_t)blockIdx.x * kRouteRows + wave_in_block();
     if (m >= a.M) return;
-    const double kNone = -__builtin_huge_val();
-    double key[NV], s[NV];
-    float v[NV];
-    float top = -__builtin_huge_valf();
+    float v[NV], bias[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = lane + 64 * i;
-        v[i] = e < a.E ? widen(x[m * a.ld + e]) : -__builtin_huge_valf();
-        top = v[i] > top ? v[i] : top;
+        v[i] = e < a.E ? (float)x[m * a.ld + e] : kNone;
+        bias[i] = !BY_LOGIT && a.bias && e < a.E ? a.bias[e] : 0.0f;
     }
-    const bool softmax = a.score == DG_ROUTE_SOFTMAX;
-    double sum = 0.0;
-    if (softmax) {
-        for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    Rank key[NV];
+    double s[BY_LOGIT ? 1 : NV];
+    float top = 0.0f;
+    double sum = 1.0;
+    if constexpr (BY_LOGIT || SOFTMAX) {
+        uint32_t r = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) r = max(r, v[i] > kNone ? rank_bits(v[i]) : 0u);
+        r = wave_max(r);
+        top = r ? from_rank(r) : 0.0f;
+        if (SOFTMAX || !a.renorm) {   // wave-uniform
+            sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const double t = v[i] > kNone ? softmax_term(v[i], top) : 0.0;
+                if constexpr (SOFTMAX) s[i] = t;
+                sum += t;
+            }
+            sum = wave_sum_f64(sum);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if constexpr (BY_LOGIT) {
+            key[i] = v[i] > kNone ? rank_bits(v[i]) : 0;
+        } else {
+            if constexpr (SOFTMAX) s[i] = s[i] / sum;
+            else s[i] = 1.0 / (1.0 + exp(-(double)v[i]));
+            const double by = s[i] + (double)bias[i];
+            key[i] = v[i] > kNone && by > -__builtin_huge_val() ? rank_bits(by) : 0;
+        }
+    }
+    // lane j holds the j-th choice
+    int chosen = -1;
+    double mine = 0.0;
+    float logit = 0.0f;
+    for (int j = 0; j < a.k; ++j) {
+        Rank best = key[0];
+#pragma unroll
+        for (int i = 1; i < NV; ++i) best = key[i] > best ? key[i] : best;
+        best = wave_max(best);
+        if (best == 0) break;   // nothing is left
+        bool found = false;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            s[i] = v[i] == top ? 1.0 : v[i] > -__builtin_huge_valf() ? exp((double)v[i] - (double)top) : 0.0;
-            sum += s[i];
+            const uint64_t at = __ballot(key[i] == best);
+            if (found || at == 0) continue;   // wave-uniform
+            found = true;
+            const int l = __builtin_ctzll(at);
+            if (lane == j) chosen = 64 * i + l;
+            if constexpr (!BY_LOGIT) {
+                const double t = readlane_f64(s[i], l);
+                if (lane == j) mine = t;
+            }
+            if (lane == l) key[i] = 0;
         }
-        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] /= sum;
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] = 1.0 / (1.0 + exp(-(double)v[i]));
+        if constexpr (BY_LOGIT)
+            if (lane == j) logit = from_rank(best);
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 64 * i;
-        key[i] = a.bias && e < a.E ? s[i] + (double)a.bias[e] : softmax ? (double)v[i] : s[i];
-        if (!(v[i] > -__builtin_huge_valf()) || !(key[i] > kNone)) key[i] = kNone;
-    }
-    double mine = 0.0, total = 0.0;   // lane j: the j-th chosen expert's score
-    int chosen = -1;
-    for (int j = 0; j < a.k; ++j) {
-        double best = kNone, bs = 0.0;
-        int at = a.E;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (key[i] > best) best = key[i], bs = s[i], at = lane + 64 * i;
-        for (int d = 1; d < 64; d <<= 1) {
-            const double ob = __shfl_xor(best, d), os = __shfl_xor(bs, d);
-            const int oa = __shfl_xor(at, d);
-            if (ob > best || (ob == best && oa < at)) best = ob, bs = os, at = oa;
-        }
-        if (!(best > kNone)) break;   // wave-uniform: nothing is left
-        if (lane == j) mine = bs, chosen = at;
-        total += bs;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (at == lane + 64 * i) key[i] = kNone;
+    if constexpr (BY_LOGIT) mine = chosen >= 0 ? softmax_term(logit, top) / sum : 0.0;
+    if (a.renorm) {
+        const double total = wave_sum_f64(mine);
+        mine = total > 0.0 ? mine / total : 0.0;
     }
     if (lane < a.k) {
-        double w = mine;
-        if (a.renorm) w = total > 0.0 ? w / total : 0.0;
         a.ids[m * a.k + lane] = chosen;
-        a.weights[m * a.k + lane] = chosen < 0 ? 0.0f : (float)(w * (double)a.scale);
+        a.weights[m * a.k + lane] = (float)(mine * (double)a.scale);
     }
 }
 
@@ -421,13 +501,17 @@ k_moe_sum(const float* __restrict__ part, const int32_t* __restrict__ ids, const
 
 template <class T, int NV>
 void route_launch(const MoeRoute& r, const RouteArgs& a, int64_t rows, hipStream_t s) {
-    hipLaunchKernelGGL((k_moe_route<T, NV>), dim3((unsigned)((rows + kRouteRows - 1) / kRouteRows)),
-                       dim3(64 * kRouteRows), 0, s, (const T*)r.x, a);
+    const bool softmax = r.score == DG_ROUTE_SOFTMAX;
+    const auto kernel = softmax && !r.bias ? k_moe_route<T, NV, true, false>
+                        : softmax          ? k_moe_route<T, NV, false, true>
+                                           : k_moe_route<T, NV, false, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((rows + kRouteRows - 1) / kRouteRows)), dim3(64 * kRouteRows), 0, s,
+                       (const T*)r.x, a);
 }
 
 template <class T>
 hipError_t route_dtype(const MoeRoute& r, hipStream_t s) {
-    RouteArgs a{r.bias, r.ids, r.weights, r.M, r.ld, 0, (int)r.E, r.k, r.score, r.renorm, r.scale};
+    RouteArgs a{r.bias, r.ids, r.weights, r.M, r.ld, 0, (int)r.E, r.k, r.renorm, r.scale};
     hipError_t e = hipSuccess;
     for (; a.first < r.M && e == hipSuccess; a.first += kMaxGroupsPerLaunch * kRouteRows) {
         const int64_t rows = std::min<int64_t>(r.M - a.first, kMaxGroupsPerLaunch * kRouteRows);
