@@ -16,6 +16,7 @@
 // slot leave; otherwise they stand for experts.  No list is built beforehand, so
 // no launch is spent on one.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "dg_internal.h"
@@ -27,7 +28,11 @@ namespace {
 
 using namespace tiles;
 
-constexpr int kMaxSlots = 4096;
+// At most 128 registers a wave: 16 waves to a CU.  Left alone the compiler takes a
+// few more for some shapes, and half the waves no longer fit (24 tokens through 64
+// experts of 1536 x 2048: 98 us against 79); held to 96 it spills (32 tokens
+// through 8 of 14336 x 4096, Q8_0: 250 against 230).
+#define MOE_WAVES __attribute__((amdgpu_waves_per_eu(4, 8)))
 constexpr int kTileColumns = 16;
 
 // ---------------------------------------------------------------------------
@@ -200,8 +205,10 @@ struct MoeArgs {
     int by_slot;      // workgroups stand for slots, not experts
     int rows, K;      // rows of one expert's matrix, columns
     int groups;       // row groups of one expert
+    int run, runs;    // row groups of a workgroup, workgroups of an expert
     int64_t first;    // the first workgroup of this launch
     int lds_cols;     // LDS bytes for the columns of a pass
+    int lds_sums;     // and for the sums and hidden values that meet there
 };
 
 // The slots routed to the workgroup's expert, in order, into list (by wave 0);
@@ -222,21 +229,87 @@ __device__ __forceinline__ int claim(const MoeArgs& a, int item, uint16_t* list,
     return cnt;
 }
 
-// The tile sums of this wave (its part of K: kw of KW) over M columns of X,
-// staged in LDS in passes.  Lane i holds the number of column i; the copies take
-// it from there by a shuffle, because the compiler waits for every copy into LDS
-// that is under way before it reads LDS.
-template <class TF, int MP, int W, int KW, int D>
-__device__ __forceinline__ void tile_sums(f32x4 (&acc)[TileSet<MP>::kNA], const uint8_t* tile, const uint8_t* X,
-                                          int column, int S, int M, uint8_t* lds, int lds_cols, int lane, int wave,
-                                          int kw) {
+// Where a lane's A operands lie: M columns in LDS from `column` on, `stride`
+// bytes apart, a column of zeros at `zero`.  Columns past M: the last again, their
+// results dropped.
+template <int MP>
+__device__ __forceinline__ ALanes a_lanes(uint32_t column, uint32_t stride, uint32_t zero, int M, int rn) {
+    ALanes al;
+    al.full = column + (uint32_t)min(rn, M - 1) * stride;
+    const uint32_t pc = column + (uint32_t)min(TileSet<MP>::kC0 + (rn & 7), M - 1) * stride;
+    const bool hi = rn >= 8;
+    al.p01 = hi ? zero : pc;
+    al.p23 = hi ? pc : zero;
+    al.ps = pc + (hi ? (uint32_t)kQ81Bytes : 0u);
+    al.sel = hi ? 0x01000C0Cu : 0x0C0C0100u;
+    return al;
+}
+
+// A wave's groups of a tile, `step` bytes apart, D of them in flight.
+template <class TF, int D>
+struct Stream {
+    u32x4 wb[D][TF::kCodeLoads + 1];
+    const uint8_t* base;
+    int cnt, last, step;
+    __device__ __forceinline__ void load(int d, int i, int lane) {
+        load_group<TF>(base + (size_t)(i < cnt ? i : last) * step, lane, lane & 15, wb[d]);
+    }
+    __device__ __forceinline__ Stream(const uint8_t* b, int n, int st, int lane)
+        : cnt(n), last(n > 0 ? n - 1 : 0), step(st) {
+        start(b, lane);
+    }
+    __device__ __forceinline__ void start(const uint8_t* b, int lane) {
+        base = b;
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(d, d, lane);
+    }
+    // The products, group i against the blocks (first + i every) * 8 of the columns in LDS.
+    template <int MP>
+    __device__ __forceinline__ void products(f32x4 (&acc)[TileSet<MP>::kNA], const uint8_t* lds, const ALanes& al,
+                                             int first, int every, int lane) {
+        const int g = lane >> 4;
+        const int rounds = (cnt + D - 1) / D;
+        for (int rd = 0; rd + 1 < rounds; ++rd) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                const int i = rd * D + d;
+                tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(first + i * every) * kGroupBlocks, g, acc);
+                load(d, i + D, lane);
+                bind_group(wb[(d + 1) % D]);
+            }
+        }
+        if (rounds > 0) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                const int i = (rounds - 1) * D + d;
+                if (d > 0) bind_group(wb[d]);
+                if (i < cnt) tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(first + i * every) * kGroupBlocks, g, acc);
+            }
+        }
+    }
+};
+
+template <int NA>
+__device__ __forceinline__ void clear(f32x4 (&acc)[NA]) {
+#pragma unroll
+    for (int a = 0; a < NA; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+// The sums of this wave (its part of K: kw of KW) of `run` tiles, one after the
+// other, over M columns of X that are staged in LDS: once where whole rows fit, in
+// passes over K for every tile where not.  tile(r): the r-th tile's address;
+// out(r, acc): what is done with its sums (not in the columns' LDS).
+//
+// Lane i holds the number of column i; the copies take it from there by a
+// shuffle, because the compiler waits for every copy into LDS that is under way
+// before it reads LDS.
+template <class TF, int MP, bool RUNS, int W, int KW, int D, class Tile, class Out>
+__device__ __forceinline__ void each_tile(int run, Tile tile, const uint8_t* X, int column, int S, int M, uint8_t* lds,
+                                          int lds_cols, int lane, int wave, int kw, Out out) {
     using TS = TileSet<MP>;
-    constexpr int L = TF::kCodeLoads + 1;
     constexpr int kGroupBytes = TF::kGroupBytes;
-    const int g = lane >> 4, rn = lane & 15;
-    // groups of a pass: whole rounds of every wave where the row does not fit at once
-    int spp = ((lds_cols - 1024) / (16 * (M + 1)) - 1) / kGroupSlots;
-    if (spp < S) {
+    int spp = ((lds_cols - 1024) / (16 * (M + 1)) - 1) / kGroupSlots;   // groups of a pass
+    if (spp < S) {   // whole rounds of every wave
         constexpr int kRound = KW * D;
         const int passes = (S + spp - 1) / spp;
         const int even = (S + passes - 1) / passes;
@@ -248,76 +321,57 @@ __device__ __forceinline__ void tile_sums(f32x4 (&acc)[TileSet<MP>::kNA], const 
     const int cs_slots = kGroupSlots * spp + 1;
     const uint32_t magic = 0xFFFFFFFFu / (uint32_t)cs_slots + 1u;   // ceil(2^32 / stride): the stride is odd
     const int copies = (M * cs_slots + kWave - 1) / kWave;
-    ALanes al;
-    {
-        const uint32_t stride = (uint32_t)cs_slots * 16u;
-        const uint32_t zero = (uint32_t)copies * 1024u;
-        al.full = (uint32_t)(rn < M ? rn : M - 1) * stride;
-        const int c = TS::kC0 + (rn & 7);
-        const uint32_t pc = (uint32_t)(c < M ? c : M - 1) * stride;
-        const bool hi = rn >= 8;
-        al.p01 = hi ? zero : pc;
-        al.p23 = hi ? pc : zero;
-        al.ps = pc + (hi ? (uint32_t)kQ81Bytes : 0u);
-        al.sel = hi ? 0x01000C0Cu : 0x0C0C0100u;
-    }
+    const ALanes al = a_lanes<MP>(0, (uint32_t)cs_slots * 16u, (uint32_t)copies * 1024u, M, lane & 15);
     if constexpr (TS::kPair) {
         u32x4* const z = reinterpret_cast<u32x4*>(lds + copies * 1024);
         for (int e = wave * kWave + lane; e < cs_slots; e += W * kWave) z[e] = u32x4{0u, 0u, 0u, 0u};
     }
-#pragma unroll
-    for (int a = 0; a < TS::kNA; ++a) acc[a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    for (int p0 = 0; p0 < S; p0 += spp) {
-        const int np = min(spp, S - p0);
-        // Wave kw takes the groups kw, kw + KW, ... of the whole row, so that its
-        // order of sums does not depend on where passes end, and so not on M.
-        const int w0 = ((kw - p0) % KW + KW) % KW;   // its first group of the pass
-        const int cnt = max(0, (np - w0 + KW - 1) / KW);
-        const uint8_t* const wbase = tile + (size_t)(p0 + (cnt > 0 ? w0 : 0)) * kGroupBytes;
-        const int last = cnt > 0 ? cnt - 1 : 0;
-        constexpr int kStep = KW * kGroupBytes;
-        if (p0 > 0) lds_barrier();   // every wave is done with the columns of the pass before
-        {
-            const int used = np * kGroupSlots;
-            const uint8_t* const xr = X + (size_t)p0 * kGroupBlocks * kQ81Bytes;
-            for (int j = wave; j < copies; j += W) {
-                const uint32_t q = (uint32_t)(j * kWave + lane);
-                const uint32_t m = __umulhi(q, magic);
-                const uint32_t c = q - m * (uint32_t)cs_slots;
-                const bool ok = m < (uint32_t)M && c < (uint32_t)used;
-                const size_t at = (size_t)__shfl(column, ok ? (int)m : 0) * ((size_t)S * kGroupSlots * 16);
-                const uint8_t* src = xr + at + (ok ? (size_t)c * 16 : 0);
-                __builtin_amdgcn_global_load_lds(src, (lds_void_t*)(lds + j * 1024), 16, 0, 0);
-            }
+    auto stage = [&](int p0, int np) {
+        const int used = np * kGroupSlots;
+        const uint8_t* const xr = X + (size_t)p0 * kGroupBlocks * kQ81Bytes;
+        for (int j = wave; j < copies; j += W) {
+            const uint32_t q = (uint32_t)(j * kWave + lane);
+            const uint32_t m = __umulhi(q, magic);
+            const uint32_t c = q - m * (uint32_t)cs_slots;
+            const bool ok = m < (uint32_t)M && c < (uint32_t)used;
+            const size_t at = (size_t)__shfl(column, ok ? (int)m : 0) * ((size_t)S * kGroupSlots * 16);
+            const uint8_t* src = xr + at + (ok ? (size_t)c * 16 : 0);
+            __builtin_amdgcn_global_load_lds(src, (lds_void_t*)(lds + j * 1024), 16, 0, 0);
         }
-        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the copies only
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
         lds_barrier();                        // every other wave's copies have landed too
-        u32x4 wb[D][L];
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-            load_group<TF>(wbase + (size_t)(d < cnt ? d : last) * kStep, lane, rn, wb[d]);
-        const int rounds = (cnt + D - 1) / D;
-        for (int rd = 0; rd + 1 < rounds; ++rd) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                const int i = rd * D + d;
-                tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(w0 + i * KW) * kGroupBlocks, g, acc);
-                const int nx = i + D;
-                load_group<TF>(wbase + (size_t)(nx < cnt ? nx : last) * kStep, lane, rn, wb[d]);
-                bind_group(wb[(d + 1) % D]);
-            }
+    };
+    f32x4 acc[TS::kNA];
+    // A tile's first weights go out before the copies, which then take no round
+    // trip of their own, or before the epilogue of the tile before it.
+    if (RUNS && spp == S) {
+        const int cnt = max(0, (S - kw + KW - 1) / KW);
+        const int first = cnt > 0 ? kw * kGroupBytes : 0;
+        Stream<TF, D> weights(tile(0) + first, cnt, KW * kGroupBytes, lane);
+        stage(0, S);
+        for (int r = 0; r < run; ++r) {
+            clear(acc);
+            weights.template products<MP>(acc, lds, al, kw, KW, lane);
+            if (r + 1 < run) weights.start(tile(r + 1) + first, lane);
+            out(r, acc);
         }
-        if (rounds > 0) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                const int i = (rounds - 1) * D + d;
-                if (d > 0) bind_group(wb[d]);
-                if (i < cnt) tiles_group<TF, MP>(wb[d], lds, al, (uint32_t)(w0 + i * KW) * kGroupBlocks, g, acc);
-            }
-        }
+        return;
     }
-    lds_barrier();   // every wave is done with the columns
+    for (int r = 0; r < (RUNS ? run : 1); ++r) {
+        clear(acc);
+        for (int p0 = 0; p0 < S; p0 += spp) {
+            const int np = min(spp, S - p0);
+            // Wave kw takes the groups kw, kw + KW, ... of the whole row, so that its
+            // order of sums does not depend on where passes end, and so not on M.
+            const int w0 = ((kw - p0) % KW + KW) % KW;   // its first group of the pass
+            const int cnt = max(0, (np - w0 + KW - 1) / KW);
+            Stream<TF, D> weights(tile(r) + (size_t)(p0 + (cnt > 0 ? w0 : 0)) * kGroupBytes, cnt, KW * kGroupBytes, lane);
+            if (r + p0 > 0) lds_barrier();   // every wave is done with the columns of the pass before
+            stage(p0, np);
+            weights.template products<MP>(acc, lds, al, w0, KW, lane);
+        }
+        out(r, acc);
+    }
 }
 
 // The KW parts of each tile, added in the order 0..KW-1 by the waves with kw = 0.
@@ -355,122 +409,195 @@ __device__ __forceinline__ void each_output(const TileOut<TF, MP>& o, int M, int
     }
 }
 
-// Gate and up products of 32 rows of one expert and M of its columns, then
-// their Q8_1 blocks.
-template <class TF, int MP, int KW, int D>
+// Gate and up products of `run` groups of 8 RT rows of one expert and M of its
+// columns, then their Q8_1 blocks.  Waves: one for each of the RT tiles, the gate's
+// and the up matrix's in turn, with the whole K.
+template <class TF, int MP, bool RUNS, int RT, int D>
 __device__ __forceinline__ void glu_columns(const MoeArgs& a, const uint8_t* Wg, const uint8_t* Wu,
-                                            const uint8_t* Xq, uint8_t* Hq, int act, int e, int grp, int M,
+                                            const uint8_t* Xq, uint8_t* Hq, int act, int e, int grp, int run, int M,
                                             const uint16_t* list, uint8_t* lds, int lane, int wave) {
-    constexpr int RT = 4, W = RT * KW, NA = TileSet<MP>::kNA;
-    const int rt = wave / KW, kw = wave - rt * KW;
-    const bool up = rt & 1;
+    static_assert(RT % 4 == 0, "whole Q8_1 blocks");
+    constexpr int NA = TileSet<MP>::kNA, kRows = RT * 8;
+    const bool up = wave & 1;
     const int S = a.K >> 8;
-    const size_t t = (size_t)e * (a.rows >> 4) + (size_t)grp * 2 + (rt >> 1);
-    const uint8_t* const tile = (up ? Wu : Wg) + t * S * TF::kGroupBytes;
-    f32x4 acc[NA];
+    const uint8_t* const tiles = (up ? Wu : Wg) +
+                                 ((size_t)e * (a.rows >> 4) + (size_t)grp * (RT / 2) + (wave >> 1)) * S * TF::kGroupBytes;
+    f32x4* const red = reinterpret_cast<f32x4*>(lds + a.lds_cols);            // the up sums
+    float* const h = reinterpret_cast<float*>(lds + a.lds_cols + RT / 2 * NA * 1024);   // [column][rows]
     const int slot = list[min(lane, M - 1)];
-    tile_sums<TF, MP, W, KW, D>(acc, tile, Xq, (int)((unsigned)slot / (unsigned)a.k), S, M, lds, a.lds_cols, lane, wave,
-                                kw);
-    f32x4* const red = reinterpret_cast<f32x4*>(lds);
-    join_parts<NA, KW>(acc, red, lane, wave, kw);
-    if (kw == 0 && up) {
+    each_tile<TF, MP, RUNS, RT, 1, D>(
+        run, [&](int r) { return tiles + (size_t)r * (RT / 2) * S * TF::kGroupBytes; }, Xq,
+        (int)((unsigned)slot / (unsigned)a.k), S, M, lds, a.lds_cols, lane, wave, 0, [&](int r, f32x4(&acc)[NA]) {
+            f32x4* const mine = red + (wave >> 1) * NA * kWave + lane;
+            if (up) {
 #pragma unroll
-        for (int i = 0; i < NA; ++i) red[(wave * NA + i) * kWave + lane] = acc[i];
-    }
-    lds_barrier();
-    float* const h = reinterpret_cast<float*>(lds + W * NA * 1024);   // [column][32 rows]
-    if (kw == 0 && !up) {
-        f32x4 us[NA];
+                for (int i = 0; i < NA; ++i) mine[i * kWave] = acc[i];
+            }
+            lds_barrier();
+            if (!up) {
+                f32x4 us[NA];
 #pragma unroll
-        for (int i = 0; i < NA; ++i) us[i] = red[((wave + KW) * NA + i) * kWave + lane];
-        TileOut<TF, MP> out(acc);
-        out.gate(act, TileOut<TF, MP>(us));
-        each_output<TF, MP>(out, M, lane >> 4, [&](int m, float v) { h[m * 32 + (rt >> 1) * 16 + (lane & 15)] = v; });
-    }
-    lds_barrier();
-    // one Q8_1 block per half wave
-    for (int v = wave * kWave + lane; v < M * 32; v += W * kWave) {
-        const int m = v >> 5, j = v & 31;
-        const float f = h[v];
-        float amax = fabsf(f);
+                for (int i = 0; i < NA; ++i) us[i] = mine[i * kWave];
+                TileOut<TF, MP> o(acc);
+                o.gate(act, TileOut<TF, MP>(us));
+                each_output<TF, MP>(o, M, lane >> 4,
+                                    [&](int m, float v) { h[m * kRows + (wave >> 1) * 16 + (lane & 15)] = v; });
+            }
+            lds_barrier();
+            // one Q8_1 block per half wave
+            for (int v = wave * kWave + lane; v < M * kRows; v += RT * kWave) {
+                const int m = v / kRows, b = v % kRows >> 5, j = v & 31;
+                const float f = h[v];
+                float amax = fabsf(f);
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
-        const float d8 = q81_scale(amax);
-        const int c = q81_code(f, d8);
-        int sum = c;
+                for (int d = 1; d < 32; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
+                const float d8 = q81_scale(amax);
+                const int c = q81_code(f, d8);
+                int sum = c;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor(sum, d);
-        uint32_t w = (uint32_t)(uint8_t)(int8_t)c << (8 * (j & 3));
-        w |= __shfl_xor(w, 1);
-        w |= __shfl_xor(w, 2);
-        uint32_t* const block =
-            reinterpret_cast<uint32_t*>(Hq + ((size_t)list[m] * (a.rows >> 5) + (size_t)grp) * kQ81Bytes);
-        if ((j & 3) == 0) block[1 + (j >> 2)] = w;
-        if (j == 0) block[0] = q81_header(d8, sum);
-    }
+                for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor(sum, d);
+                uint32_t w = (uint32_t)(uint8_t)(int8_t)c << (8 * (j & 3));
+                w |= __shfl_xor(w, 1);
+                w |= __shfl_xor(w, 2);
+                uint32_t* const block = reinterpret_cast<uint32_t*>(
+                    Hq + ((size_t)list[m] * (a.rows >> 5) + (size_t)(grp + r) * (RT / 4) + b) * kQ81Bytes);
+                if ((j & 3) == 0) block[1 + (j >> 2)] = w;
+                if (j == 0) block[0] = q81_header(d8, sum);
+            }
+        });
 }
 
-template <class TF, int KW, int D>
-__global__ void __launch_bounds__(64 * 4 * KW)
-k_moe_glu(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ Wu, const uint8_t* __restrict__ Xq,
-          uint8_t* __restrict__ Hq, int act, MoeArgs a) {
-    extern __shared__ u32x4 moe_lds[];
-    uint8_t* const lds = reinterpret_cast<uint8_t*>(moe_lds);
-    uint16_t* const list = reinterpret_cast<uint16_t*>(lds + a.lds_cols);
-    const int lane = lane_id(), wave = wave_in_block();
-    const int64_t b = a.first + blockIdx.x;
-    const int item = (int)(b / a.groups);
-    int e;
-    const int cnt = claim(a, item, list, e, lane, wave);
-    if (cnt == 0) return;   // workgroup-uniform, before any barrier
-    const int grp = (int)(b - (int64_t)item * a.groups);
-    lds_barrier();          // the list is written
-    for (int c0 = 0; c0 < cnt; c0 += kTileColumns) {
-        const int M = min(kTileColumns, cnt - c0);
-        if (c0 > 0) lds_barrier();
-        if (M <= 8) glu_columns<TF, 8, KW, D>(a, Wg, Wu, Xq, Hq, act, e, grp, M, list + c0, lds, lane, wave);
-        else glu_columns<TF, 16, KW, D>(a, Wg, Wu, Xq, Hq, act, e, grp, M, list + c0, lds, lane, wave);
-    }
-}
-
-template <class TF, int MP, int RT, int KW, int D>
+// The down products of `run` groups of RT row tiles of one expert and M of its
+// columns, each in KW parts of K, into the slots' partial columns.
+template <class TF, int MP, bool RUNS, int RT, int KW, int D>
 __device__ __forceinline__ void down_columns(const MoeArgs& a, const uint8_t* Wd, const uint8_t* Hq, float* part,
-                                             int e, int grp, int M, const uint16_t* list, uint8_t* lds, int lane,
-                                             int wave) {
+                                             int e, int grp, int run, int M, const uint16_t* list, uint8_t* lds,
+                                             int lane, int wave) {
+    static_assert(!RUNS || KW == 1, "parts that meet in LDS leave it after one row group");
     constexpr int W = RT * KW, NA = TileSet<MP>::kNA;
     const int rt = wave / KW, kw = wave - rt * KW;
     const int S = a.K >> 8;
     const int t = grp * RT + rt;
-    const uint8_t* const tile = Wd + ((size_t)e * (a.rows >> 4) + t) * S * TF::kGroupBytes;
-    f32x4 acc[NA];
-    tile_sums<TF, MP, W, KW, D>(acc, tile, Hq, list[min(lane, M - 1)], S, M, lds, a.lds_cols, lane, wave, kw);
-    join_parts<NA, KW>(acc, reinterpret_cast<f32x4*>(lds), lane, wave, kw);
-    if (kw == 0) {
-        const TileOut<TF, MP> out(acc);
-        const int n = t * 16 + (lane & 15);
-        each_output<TF, MP>(out, M, lane >> 4, [&](int m, float v) { part[(size_t)list[m] * a.rows + n] = v; });
+    const uint8_t* const tiles = Wd + ((size_t)e * (a.rows >> 4) + t) * S * TF::kGroupBytes;
+    each_tile<TF, MP, RUNS, W, KW, D>(
+        run, [&](int r) { return tiles + (size_t)r * RT * S * TF::kGroupBytes; }, Hq, list[min(lane, M - 1)], S, M, lds,
+        a.lds_cols, lane, wave, kw, [&](int r, f32x4(&acc)[NA]) {
+            join_parts<NA, KW>(acc, reinterpret_cast<f32x4*>(lds + a.lds_cols), lane, wave, kw);
+            if (kw > 0) return;
+            const TileOut<TF, MP> o(acc);
+            const int n = (t + r * RT) * 16 + (lane & 15);
+            each_output<TF, MP>(o, M, lane >> 4, [&](int m, float v) { part[(size_t)list[m] * a.rows + n] = v; });
+        });
+}
+
+// What both kernels do: find the workgroup's expert and columns, and take them
+// 16 (8) at a time.  f(mp, e, first row group, row groups, M, list)
+template <bool MANY, class F>
+__device__ __forceinline__ void each_columns(const MoeArgs& a, uint8_t* lds, F f) {
+    uint16_t* const list = reinterpret_cast<uint16_t*>(lds + a.lds_cols + a.lds_sums);
+    const int64_t b = a.first + blockIdx.x;
+    const int item = (int)(b / a.runs);
+    int e;
+    const int cnt = claim(a, item, list, e, lane_id(), wave_in_block());
+    if (cnt == 0) return;   // workgroup-uniform, before any barrier
+    const int grp = (int)(b - (int64_t)item * a.runs) * a.run;
+    const int run = min(a.run, a.groups - grp);
+    lds_barrier();          // the list is written
+    constexpr int kTile = MANY ? 16 : 8;
+    for (int c0 = 0; c0 < cnt; c0 += kTile) {
+        const int M = min(kTile, cnt - c0);
+        if (c0 > 0) lds_barrier();   // the columns and sums before are done with
+        if (!MANY || M <= 8) f(std::integral_constant<int, 8>(), e, grp, run, M, list + c0);
+        else if constexpr (MANY) f(std::integral_constant<int, 16>(), e, grp, run, M, list + c0);
     }
 }
 
-template <class TF, int RT, int KW, int D>
-__global__ void __launch_bounds__(64 * RT * KW)
+template <class TF, bool MANY, bool RUNS, int RT, int D>
+__global__ void __launch_bounds__(64 * RT) MOE_WAVES
+k_moe_glu(const uint8_t* __restrict__ Wg, const uint8_t* __restrict__ Wu, const uint8_t* __restrict__ Xq,
+          uint8_t* __restrict__ Hq, int act, MoeArgs a) {
+    extern __shared__ u32x4 moe_lds[];
+    uint8_t* const lds = reinterpret_cast<uint8_t*>(moe_lds);
+    each_columns<MANY>(a, lds, [&](auto mp, int e, int grp, int run, int M, const uint16_t* list) {
+        glu_columns<TF, mp.value, RUNS, RT, D>(a, Wg, Wu, Xq, Hq, act, e, grp, run, M, list, lds, lane_id(), wave_in_block());
+    });
+}
+
+template <class TF, bool MANY, bool RUNS, int RT, int KW, int D>
+__global__ void __launch_bounds__(64 * RT * KW) MOE_WAVES
 k_moe_down(const uint8_t* __restrict__ Wd, const uint8_t* __restrict__ Hq, float* __restrict__ part, MoeArgs a) {
     extern __shared__ u32x4 moe_lds[];
     uint8_t* const lds = reinterpret_cast<uint8_t*>(moe_lds);
-    uint16_t* const list = reinterpret_cast<uint16_t*>(lds + a.lds_cols);
+    each_columns<MANY>(a, lds, [&](auto mp, int e, int grp, int run, int M, const uint16_t* list) {
+        down_columns<TF, mp.value, RUNS, RT, KW, D>(a, Wd, Hq, part, e, grp, run, M, list, lds, lane_id(), wave_in_block());
+    });
+}
+
+__device__ __forceinline__ void store_y(void* Y, int ydtype, size_t i, float v) {
+    if (ydtype == DG_DTYPE_F32) ((float*)Y)[i] = v;
+    else if (ydtype == DG_DTYPE_F16) ((_Float16*)Y)[i] = (_Float16)bind_f32(v);
+    else ((__bf16*)Y)[i] = (__bf16)bind_f32(v);
+}
+
+// The down products and their weighted sum for one token at a time: a workgroup
+// has RT row tiles of one token, a wave (j, rt, kw) its j-th expert's products
+// with that expert's hidden column, so nothing is left to a third launch.  Each
+// token reads its experts' weights for itself.  The order of every sum is that of
+// k_moe_down and k_moe_sum.  Waves: k RT KW.
+template <class TF, int RT, int KW, int D>
+__global__ void __launch_bounds__(1024) MOE_WAVES
+k_moe_down_tokens(const uint8_t* __restrict__ Wd, const uint8_t* __restrict__ Hq, const float* __restrict__ weights,
+                  void* __restrict__ Y, int ydtype, MoeArgs a) {
+#pragma clang fp contract(off)
+    constexpr int NA = TileSet<8>::kNA;
+    extern __shared__ u32x4 moe_lds[];
+    uint8_t* const lds = reinterpret_cast<uint8_t*>(moe_lds);
     const int lane = lane_id(), wave = wave_in_block();
+    const int j = wave / (RT * KW), rt = wave / KW % RT, kw = wave % KW;
     const int64_t b = a.first + blockIdx.x;
-    const int item = (int)(b / a.groups);
-    int e;
-    const int cnt = claim(a, item, list, e, lane, wave);
-    if (cnt == 0) return;   // workgroup-uniform, before any barrier
-    const int grp = (int)(b - (int64_t)item * a.groups);
-    lds_barrier();          // the list is written
-    for (int c0 = 0; c0 < cnt; c0 += kTileColumns) {
-        const int M = min(kTileColumns, cnt - c0);
-        if (c0 > 0) lds_barrier();
-        if (M <= 8) down_columns<TF, 8, RT, KW, D>(a, Wd, Hq, part, e, grp, M, list + c0, lds, lane, wave);
-        else down_columns<TF, 16, RT, KW, D>(a, Wd, Hq, part, e, grp, M, list + c0, lds, lane, wave);
+    const int m = (int)(b / a.groups);
+    const int t = (int)(b - (int64_t)m * a.groups) * RT + rt;
+    const int p = m * a.k + j;
+    const int e = a.ids[p];
+    const bool live = e >= 0 && e < a.E;   // wave-uniform
+    const int S = a.K >> 8;
+    const uint32_t stride = (uint32_t)(kGroupSlots * S) * 16u;
+    const uint32_t zero = (uint32_t)a.k * stride;
+    const int cnt = live ? (S - kw + KW - 1) / KW : 0;
+    const uint8_t* const tile = Wd + ((size_t)(live ? e : 0) * (a.rows >> 4) + t) * S * TF::kGroupBytes;
+    Stream<TF, D> stream(tile + (cnt > 0 ? kw : 0) * TF::kGroupBytes, cnt, KW * TF::kGroupBytes, lane);
+    // the k hidden columns lie one after the other; a slot without an expert has none
+    const int waves = a.k * RT * KW, slots = kGroupSlots * S;
+    u32x4* const cols = moe_lds;
+    for (int i = wave * kWave + lane; i < (a.k + 1) * slots; i += waves * kWave) {
+        const int c = i / slots;
+        const bool has = c < a.k && (uint32_t)a.ids[m * a.k + min(c, a.k - 1)] < (uint32_t)a.E;
+        cols[i] = has ? reinterpret_cast<const u32x4*>(Hq + (size_t)m * a.k * stride)[i] : u32x4{0u, 0u, 0u, 0u};
+    }
+    lds_barrier();
+    const ALanes al = a_lanes<8>((uint32_t)j * stride, 0, zero, 1, lane & 15);
+    f32x4 acc[NA];
+#pragma unroll
+    for (int i = 0; i < NA; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    stream.template products<8>(acc, lds, al, kw, KW, lane);
+    lds_barrier();   // every wave is done with the columns
+    join_parts<NA, KW>(acc, reinterpret_cast<f32x4*>(lds), lane, wave, kw);
+    lds_barrier();
+    float* const sums = reinterpret_cast<float*>(lds);   // [j][RT * 16]
+    if (kw == 0) {
+        const TileOut<TF, 8> out(acc);
+        if (lane < 16) sums[(j * RT + rt) * 16 + lane] = out.pair[0];
+    }
+    lds_barrier();
+    const int n = wave * kWave + lane;
+    if (n < RT * 16) {
+        float y = 0.0f;
+        for (int i = 0; i < a.k; ++i) {
+            const int ei = a.ids[m * a.k + i];
+            if (ei < 0 || ei >= a.E) continue;
+            y += weights[m * a.k + i] * sums[i * RT * 16 + n];
+        }
+        store_y(Y, ydtype, (size_t)m * a.rows + (size_t)(t - rt) * 16 + n, y);
     }
 }
 
@@ -525,10 +652,10 @@ hipError_t route_dtype(const MoeRoute& r, hipStream_t s) {
     return e;
 }
 
-// One kernel over (items, row groups), in launches of what one takes.
+// One kernel over (items, workgroups of each), in launches of what one takes.
 template <class F>
 hipError_t over_groups(int64_t items, MoeArgs& a, F launch) {
-    const int64_t all = items * a.groups;
+    const int64_t all = items * a.runs;
     hipError_t e = hipSuccess;
     for (a.first = 0; a.first < all && e == hipSuccess; a.first += kMaxGroupsPerLaunch) {
         launch((unsigned)std::min<int64_t>(all - a.first, kMaxGroupsPerLaunch));
@@ -537,7 +664,107 @@ hipError_t over_groups(int64_t items, MoeArgs& a, F launch) {
     return e;
 }
 
-template <class TF>
+// LDS for the columns of a pass: the whole rows of as many columns as an expert
+// has on the mean, twice over, where that leaves room for two workgroups on a CU.
+int lds_for_columns(const MoeLayer& q, const MoeArgs& a) {
+    const int64_t experts = std::min<int64_t>(a.P, q.E);
+    const int64_t cols = std::min<int64_t>(std::min<int64_t>(kTileColumns, q.M), 2 * ((a.P + experts - 1) / experts));
+    const int64_t want = (cols + 1) * (kGroupSlots * (a.K / 256) + 1) * 16 + 1024;
+    const int64_t room = 80 * 1024 - 256 - a.lds_sums - (a.P * 2 + 15) / 16 * 16;
+    return (int)std::max<int64_t>(8192, std::min<int64_t>(want, room) / 16 * 16);
+}
+
+// Experts that the tokens reach, chosen evenly.
+double live_experts(const MoeLayer& q) {
+    return (double)q.E * (1.0 - std::pow(1.0 - std::min(1.0, (double)q.k / (double)q.E), (double)q.M));
+}
+
+// Row groups of a workgroup.  Over Q4_0 rows of up to 2048 a workgroup's start and
+// end weigh as much as its weights, so it takes as many row groups as make the best
+// use of the workgroups that are resident together: in units of one row group's
+// weights, `start` before each workgroup's first, and a third of a round for the
+// uneven end of more than one round.
+template <class TF, int KW>
+constexpr bool kRuns = std::is_same<TF, TilesQ4_0>::value && KW == 1;
+
+void set_runs(const MoeLayer& q, MoeArgs& a, int waves, bool runs) {
+    a.run = 1;
+    if (runs && a.K <= 2048) {
+        const double live = live_experts(q), resident = device_cu_count() * 16.0 / waves, start = 0.75;
+        double best = 0;
+        for (int r = 1; r <= std::min(8, a.groups); ++r) {
+            const double rounds = live * ((a.groups + r - 1) / r) / resident;
+            const double t = (r + start) * (rounds <= 1.0 ? 1.0 : rounds + 0.35);
+            if (r == 1 || t < best) best = t, a.run = r;
+        }
+    }
+    a.runs = (a.groups + a.run - 1) / a.run;
+}
+
+template <class TF, bool MANY, int RT, int D>
+hipError_t moe_glu(const MoeLayer& q, MoeArgs a, int64_t items, uint8_t* Hq, hipStream_t s) {
+    a.rows = (int)q.N;
+    a.K = (int)q.K;
+    a.groups = (int)(q.N / (8 * RT));
+    a.lds_sums = RT / 2 * (MANY ? 2 : 1) * 1024 + (MANY ? 16 : 8) * 8 * RT * 4;
+    a.lds_cols = lds_for_columns(q, a);
+    set_runs(q, a, RT, kRuns<TF, 1>);
+    return over_groups(items, a, [&](unsigned grid) {
+        const auto kernel = a.run > 1 ? k_moe_glu<TF, MANY, kRuns<TF, 1>, RT, D> : k_moe_glu<TF, MANY, false, RT, D>;
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * RT), a.lds_cols + a.lds_sums + (size_t)a.P * 2, s,
+                           (const uint8_t*)q.Wg, (const uint8_t*)q.Wu, (const uint8_t*)q.Xq, Hq, q.act, a);
+    });
+}
+
+template <class TF, bool MANY, int RT, int KW, int D>
+hipError_t moe_down(const MoeLayer& q, MoeArgs a, int64_t items, const uint8_t* Hq, float* part, hipStream_t s) {
+    a.rows = (int)q.K;
+    a.K = (int)q.N;
+    a.groups = (int)(q.K / 16 / RT);
+    a.lds_sums = KW > 1 ? RT * KW * (MANY ? 2 : 1) * 1024 : 0;
+    a.lds_cols = lds_for_columns(q, a);
+    set_runs(q, a, RT * KW, kRuns<TF, KW>);
+    return over_groups(items, a, [&](unsigned grid) {
+        const auto kernel = a.run > 1 ? k_moe_down<TF, MANY, kRuns<TF, KW>, RT, KW, D> : k_moe_down<TF, MANY, false, RT, KW, D>;
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * RT * KW), a.lds_cols + a.lds_sums + (size_t)a.P * 2, s,
+                           (const uint8_t*)q.Wd, Hq, part, a);
+    });
+}
+
+template <class TF, int RT, int KW, int D>
+hipError_t moe_down_tokens(const MoeLayer& q, MoeArgs a, const uint8_t* Hq, hipStream_t s) {
+    a.rows = (int)q.K;
+    a.K = (int)q.N;
+    a.groups = a.runs = (int)(q.K / 16 / RT);
+    a.run = 1;
+    const int waves = q.k * RT * KW;
+    const size_t lds = std::max<size_t>((size_t)(q.k + 1) * kGroupSlots * (a.K / 256) * 16, (size_t)waves * 1024);
+    return over_groups(q.M, a, [&](unsigned grid) {
+        hipLaunchKernelGGL((k_moe_down_tokens<TF, RT, KW, D>), dim3(grid), dim3(64 * waves), lds, s,
+                           (const uint8_t*)q.Wd, Hq, q.weights, q.Y, q.ydtype, a);
+    });
+}
+
+// Parts of K per row tile of the down products.  It fixes the order of their
+// sums, so it goes by the row's length alone.
+int down_parts(const MoeLayer& q) { return q.N >= 4096 ? 2 : 1; }
+
+// Whether k_moe_down_tokens takes the layer: the weights that tokens of one expert
+// read again (with experts chosen evenly) cost less than the third launch.
+bool by_token(const MoeLayer& q) {
+    const double again = ((double)(q.M * q.k) - live_experts(q)) * (double)q.N * (double)q.K * (q.q8 ? 34.0 / 32 : 18.0 / 32);
+    return again <= 24e6 && q.k * down_parts(q) <= 16 && (size_t)(q.k + 1) * kGroupSlots * (q.N / 256) * 16 <= 80 * 1024;
+}
+
+template <class TF, int KW, int D>
+hipError_t moe_down_tokens_kw(const MoeLayer& q, const MoeArgs& a, const uint8_t* Hq, hipStream_t s) {
+    const int64_t tiles = q.M * (q.K / 16);
+    if (q.k * KW * 4 <= 8 && tiles >= 1024) return moe_down_tokens<TF, 4, KW, D>(q, a, Hq, s);
+    if (q.k * KW * 2 <= 8 && tiles >= 512) return moe_down_tokens<TF, 2, KW, D>(q, a, Hq, s);
+    return moe_down_tokens<TF, 1, KW, D>(q, a, Hq, s);
+}
+
+template <class TF, bool MANY>
 hipError_t moe_layer(const MoeLayer& q, hipStream_t s) {
     const int P = (int)(q.M * q.k);
     uint8_t* const Hq = (uint8_t*)q.ws;
@@ -549,27 +776,18 @@ hipError_t moe_layer(const MoeLayer& q, hipStream_t s) {
     a.k = q.k;
     a.by_slot = P <= q.E;
     const int64_t items = std::min<int64_t>(P, q.E);
-    a.lds_cols = 64 * 1024;
-    const size_t lds = a.lds_cols + (size_t)P * 2;
-
-    constexpr int KW = 2, D = 2;
-    a.rows = (int)q.N;
-    a.K = (int)q.K;
-    a.groups = (int)(q.N / 32);
-    hipError_t e = over_groups(items, a, [&](unsigned grid) {
-        hipLaunchKernelGGL((k_moe_glu<TF, KW, D>), dim3(grid), dim3(64 * 4 * KW), lds, s, (const uint8_t*)q.Wg,
-                           (const uint8_t*)q.Wu, (const uint8_t*)q.Xq, Hq, q.act, a);
-    });
+    const hipError_t e = items * (q.N / 64) >= 256 ? moe_glu<TF, MANY, 8, 2>(q, a, items, Hq, s)
+                                                   : moe_glu<TF, MANY, 4, 2>(q, a, items, Hq, s);
     if (e != hipSuccess) return e;
-    a.rows = (int)q.K;
-    a.K = (int)q.N;
-    constexpr int RT = 4;
-    a.groups = (int)(q.K / 16 / RT);
-    e = over_groups(items, a, [&](unsigned grid) {
-        hipLaunchKernelGGL((k_moe_down<TF, RT, KW, D>), dim3(grid), dim3(64 * RT * KW), lds, s, (const uint8_t*)q.Wd,
-                           Hq, part, a);
-    });
-    return e;
+    const bool two = down_parts(q) == 2;
+    if (by_token(q)) return two ? moe_down_tokens_kw<TF, 2, 4>(q, a, Hq, s) : moe_down_tokens_kw<TF, 1, 2>(q, a, Hq, s);
+    return two ? moe_down<TF, MANY, 4, 2, 2>(q, a, items, Hq, part, s) : moe_down<TF, MANY, 4, 1, 2>(q, a, items, Hq, part, s);
+}
+
+// MANY: an expert can have more than 8 columns.
+template <class TF>
+hipError_t moe_format(const MoeLayer& q, hipStream_t s) {
+    return q.M > 8 ? moe_layer<TF, true>(q, s) : moe_layer<TF, false>(q, s);
 }
 
 template <class T>
@@ -596,8 +814,8 @@ size_t moe_workspace_bytes(int64_t N, int64_t K, int64_t M, int k) {
 hipError_t launch_moe(const MoeLayer& layer, hipStream_t s) {
     MoeLayer q = layer;
     if (q.N == 0) q.k = 0;   // empty products: sums of no slots
-    hipError_t e = q.k == 0 ? hipSuccess : q.q8 ? moe_layer<TilesQ8_0>(q, s) : moe_layer<TilesQ4_0>(q, s);
-    if (e != hipSuccess) return e;
+    hipError_t e = q.k == 0 ? hipSuccess : q.q8 ? moe_format<TilesQ8_0>(q, s) : moe_format<TilesQ4_0>(q, s);
+    if (e != hipSuccess || (q.k > 0 && by_token(q))) return e;
     if (q.ydtype == DG_DTYPE_F32) return moe_sum<float>(q, s);
     if (q.ydtype == DG_DTYPE_F16) return moe_sum<_Float16>(q, s);
     return moe_sum<__bf16>(q, s);

@@ -232,9 +232,10 @@ def distinct(key, E, M, k):
 
 
 # (E, N, K, M, k): workgroups by slot and by expert; one column to several tiles of columns of one expert; rows of one
-# group of 256 columns; columns that fill LDS in one pass and in several
+# group of 256 columns; columns that fill LDS in one pass and in several; enough workgroups for several row groups each
 SHAPES = [(1, 256, 256, 1, 1), (8, 512, 256, 1, 3), (4, 256, 512, 3, 2), (16, 256, 768, 20, 4), (2, 768, 1280, 40, 2),
-          (64, 256, 256, 5, 4), (2, 256, 4352, 24, 1), (2, 4608, 256, 20, 1), (3, 512, 512, 7, 3), (32, 256, 512, 33, 1)]
+          (64, 256, 256, 5, 4), (2, 256, 4352, 24, 1), (2, 4608, 256, 20, 1), (3, 512, 512, 7, 3), (32, 256, 512, 33, 1),
+          (64, 1280, 256, 60, 4), (64, 256, 2560, 60, 4), (16, 256, 256, 200, 4)]
 
 
 @pytest.mark.parametrize("fmt", ["q4_0", "q8_0"])
