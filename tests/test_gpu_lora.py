@@ -82,10 +82,12 @@ class Case:
         return got
 
 
-# one row to many, every kind of rank, odd numbers of outputs, short and long rows of K, strides
+# one row to many, past what is grouped together (1024), every kind of rank, odd numbers of outputs, short and long rows
+# of K
 SHAPES = [(1, 1, 8, 8, 1), (1, 300, 4096, 16, 3), (2, 255, 520, 24, 2), (3, 1001, 8, 8, 2), (5, 257, 1032, 40, 1),
           (7, 64, 2048, 64, 4), (16, 513, 768, 16, 5), (17, 130, 4104, 128, 3), (33, 77, 264, 8, 40), (64, 100, 512, 32, 2),
-          (65, 1030, 256, 16, 9), (130, 45, 1000, 72, 3), (200, 515, 136, 32, 7), (1, 97, 16392, 512, 2), (3, 31, 24, 504, 1)]
+          (65, 1030, 256, 16, 9), (130, 45, 1000, 72, 3), (200, 515, 136, 32, 7), (1, 97, 16392, 512, 2), (3, 31, 24, 504, 1),
+          (1100, 70, 64, 8, 3), (2049, 33, 40, 16, 5), (4, 2101, 1032, 56, 3), (128, 1024, 72, 8, 6), (129, 1024, 72, 8, 6)]
 
 
 @pytest.mark.parametrize("x", TYPES)
@@ -109,15 +111,16 @@ def test_options(dg, dev, M, N, K, R, L):
     assert np.array_equal(c.run(dg, dev), c.base.numpy())
 
 
-def test_ranks(dg, dev):
+@pytest.mark.parametrize("N,R", [(203, 40), (3001, 40), (45, 136)])
+def test_ranks(dg, dev, N, R):
     """Every rank from none to all and beyond; what lies past a rank is not read as a number."""
     ranks = [0, 1, 2, 7, 8, 9, 15, 16, 23, 24, 25, 31, 32, 33, 40, 41, -3, 1 << 30]
     L = len(ranks)
     for x in TYPES:
-        c = Case(11, 3 * L, 203, 392, 40, L, x, ranks=ranks, adapter=np.arange(3 * L) % L)
+        c = Case(11, 3 * L, N, 392, R, L, x, ranks=ranks, adapter=np.arange(3 * L) % L)
         want = c.check(dg, dev)
         for a, r in enumerate(ranks):
-            r = min(max(r, 0), 40)
+            r = min(max(r, 0), R)
             c.A[a, r:] = float("nan")
             c.B[a, :, r:] = float("inf")
         assert np.array_equal(want, c.run(dg, dev, fill=0xFF))   # a workspace of NaN
@@ -130,19 +133,37 @@ def test_no_columns_and_no_adapters(dg, dev):
     assert np.array_equal(c.run(dg, dev), c.base.numpy())
 
 
+@pytest.mark.parametrize("N,K,R", [(333, 1544, 48), (2101, 1544, 16), (2101, 264, 64)])
 @pytest.mark.parametrize("pattern", ["one", "runs", "mixed", "distinct"])
-def test_a_row_does_not_depend_on_the_others(dg, dev, pattern):
+def test_a_row_does_not_depend_on_the_others(dg, dev, pattern, N, K, R):
     """However the adapters of the batch are spread, each row is the row of a call of its own, bit for bit."""
     M, L = 71, 9
     adapter = {"one": np.full(M, 4), "runs": np.arange(M) // 8, "mixed": np.random.default_rng(2).integers(-1, L, M),
                "distinct": np.arange(M) % L}[pattern]
-    c = Case(21, M, 333, 1544, 48, L, "bf16", adapter=adapter)
+    c = Case(21, M, N, K, R, L, "bf16", adapter=adapter)
     got = c.check(dg, dev)
     assert np.array_equal(got, c.run(dg, dev))
     for m in (0, 1, 13, 70):
-        one = Case(21, M, 333, 1544, 48, L, "bf16", adapter=adapter)
+        one = Case(21, M, N, K, R, L, "bf16", adapter=adapter)
         one.M, one.x, one.adapter, one.base = 1, c.x[m:m + 1], c.adapter[m:m + 1], c.base[m:m + 1]
         assert np.array_equal(one.run(dg, dev)[0], got[m])
+
+
+@pytest.mark.parametrize("x", TYPES)
+@pytest.mark.parametrize("w", ["f16", "bf16"])
+def test_subnormal_values(dg, dev, x, w):
+    """Weights and rows below the smallest normal number of their type count for what they are."""
+    import torch
+    c = Case(31, 5, 100, 128, 16, 2, x, w, adapter=[0, 1, 0, 1, 1], base=False, scale=False)
+    tiny = torch.finfo(tdtype(w)).smallest_normal
+    c.A = (c.A.float().sign() * tiny * 0.375).to(tdtype(w))
+    c.x = torch.full_like(c.x, 1.0)
+    c.B = c.B.float().sign().to(tdtype(w)) * (2.0 ** 100 if w == "bf16" else 2.0 ** 10)
+    c.check(dg, dev)
+    assert np.abs(c.definition()[0]).max() > 100 * c.definition()[1].max()
+    if x != "f32":
+        c.A, c.x = c.A.float().sign().to(tdtype(w)), (c.x.float() * torch.finfo(tdtype(x)).smallest_normal / 4).to(tdtype(x))
+        c.check(dg, dev)
 
 
 def test_infinities_stay_in_their_row(dg, dev):
