@@ -249,9 +249,15 @@ def raw():
 # marshalling helpers
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -280,7 +286,7 @@ def _here(t, name):
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a device tensor")
-    cur = _torch().cuda.current_device()
+    cur = _torch()._C._cuda_getDevice()   # a device tensor: the runtime is up
     if dev != cur:
         raise ValueError(f"{name} is on device {dev}, the current device is {cur}")
     return dev
@@ -310,9 +316,10 @@ def _dtype_id(t, name):
     if not _float_ids:
         torch = _torch()
         _float_ids.update({torch.float32: DG_DTYPE_F32, torch.float16: DG_DTYPE_F16, torch.bfloat16: DG_DTYPE_BF16})
-    if t.dtype not in _float_ids:
+    i = _float_ids.get(t.dtype)
+    if i is None:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(_float_ids)}")
-    return _float_ids[t.dtype]
+    return i
 
 
 def _rows(t, name, count):

@@ -14,14 +14,14 @@
 // change it.  Matrix cores with 16 rows of one adapter a product were slower wherever
 // an adapter has few rows, which is what a batch of requests has, and faster past some
 // hundred rows of high rank: 64 x 4096 x 4096, R 16, one adapter 21 us against 7.5;
-// 24 x 14336 x 4096 of binary32, R 64, 20 against 10.6; 200 x 28669 x 8192, R 32,
-// five adapters 49 against 54; 2048 x 4096 x 4096, R 64, four adapters 56 against 111.
+// 24 x 14336 x 4096 of binary32, R 64, 8 adapters 20 against 10.6; 200 x 28669 x 8192,
+// R 32, 64 adapters 49 against 49.5; 2048 x 4096 x 4096, R 64, 4 adapters 56 against 111.
 // Their sums are in another order, so a rule between the two would make a row's
 // results depend on the number of rows; they are not used.
 //
-// What bounds it: few rows, the latency of three to four dependent loads; many, for Y
-// the vector operations, one multiply-add for each row, output and rank and two selects
-// and moves for each output of eight ranks.
+// What bounds it: few rows, the latency of three to four dependent loads; many rows of
+// many adapters, memory (the 200 rows above move 191 MB: h takes 14 us, Y 35); many
+// rows of one adapter, the vector operations.
 #include <algorithm>
 #include <type_traits>
 
@@ -402,8 +402,12 @@ hipError_t lora(const LoraRows& q, hipStream_t s) {
     const int64_t windows = (q.M + a.window - 1) / a.window, rows = std::min<int64_t>(q.M, a.window);
     a.by_row = rows < q.L + 1;
     const int items = (int)std::min<int64_t>(rows, q.L + 1);
-    a.block = 1024;
-    while (a.block > 256 && windows * items * ((q.N + a.block - 1) / a.block) < 1024) a.block /= 2;
+    // Long blocks read h and the adapters less often, short ones fill the machine: 200 x 28669
+    // x 8192, R 32, 64 adapters 49.5 us with 512 or 256, 54 with 1024, 66 with 2048; 200 x
+    // 14336 x 4096, R 16, 4 adapters 17.8 with 512, 19.1 with 256; 96 x 8192 x 1024, R 64, 16
+    // adapters (272 workgroups of 1024) 15.0 with 256, 16.9 with 512.
+    a.block = 512;
+    if (windows * items * ((q.N + a.block - 1) / a.block) < 1024) a.block = 256;
     return lora_expand<EW>(q, a, items, windows, s);
 }
 
