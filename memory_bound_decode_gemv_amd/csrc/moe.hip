@@ -683,7 +683,10 @@ double live_experts(const MoeLayer& q) {
 // end weigh as much as its weights, so it takes as many row groups as make the best
 // use of the workgroups that are resident together: in units of one row group's
 // weights, `start` before each workgroup's first, and a third of a round for the
-// uneven end of more than one round.
+// uneven end of more than one round.  One row group each and as modelled: 24 tokens
+// through 6 of 64 experts of 1536 x 2048 63 and 58 us, 32 through 8 of 128 of 768 x
+// 2048 70 and 63, 16 of the same 57 and 60.  Longer rows and two parts of K: no
+// difference, so their kernels have no such loop.
 template <class TF, int KW>
 constexpr bool kRuns = std::is_same<TF, TilesQ4_0>::value && KW == 1;
 
@@ -746,11 +749,18 @@ hipError_t moe_down_tokens(const MoeLayer& q, MoeArgs a, const uint8_t* Hq, hipS
 }
 
 // Parts of K per row tile of the down products.  It fixes the order of their
-// sums, so it goes by the row's length alone.
+// sums, so it goes by the row's length alone.  With 2, 4 and 8 parts of 14336: one
+// token through 2 of 8 Q4_0 experts 40.6, 39.3, 38.5 us, 16 tokens 123, 125, 135, 32
+// through Q8_0 ones 228, 234, 249.  With 1 and 2 parts of 1536 (64 experts, k 6): one
+// token 16.3, 15.6, 24 tokens 58, 63; of 768 (128 experts, k 8): 14.1, 14.3, 60, 66 (16).
 int down_parts(const MoeLayer& q) { return q.N >= 4096 ? 2 : 1; }
 
 // Whether k_moe_down_tokens takes the layer: the weights that tokens of one expert
-// read again (with experts chosen evenly) cost less than the third launch.
+// read again (with experts chosen evenly) cost less than the third launch.  Without
+// and with it, by the bytes that are read again: 8 experts of 14336 x 4096, one token
+// (none) 43.0 and 40.6 us, three (45e6) 78.8 and 83.0; 64 of 1536 x 2048, k 6, eight
+// tokens (23e6) 44.5 and 41.4, twelve (48e6) 51.6 and 52.2; 128 Q8_0 ones of 768 x
+// 2048, k 8, one token 19 and 16.3, twelve (45e6) 65.8 and 70.3.
 bool by_token(const MoeLayer& q) {
     const double again = ((double)(q.M * q.k) - live_experts(q)) * (double)q.N * (double)q.K * (q.q8 ? 34.0 / 32 : 18.0 / 32);
     return again <= 24e6 && q.k * down_parts(q) <= 16 && (size_t)(q.k + 1) * kGroupSlots * (q.N / 256) * 16 <= 80 * 1024;
@@ -776,8 +786,12 @@ hipError_t moe_layer(const MoeLayer& q, hipStream_t s) {
     a.k = q.k;
     a.by_slot = P <= q.E;
     const int64_t items = std::min<int64_t>(P, q.E);
-    const hipError_t e = items * (q.N / 64) >= 256 ? moe_glu<TF, MANY, 8, 2>(q, a, items, Hq, s)
-                                                   : moe_glu<TF, MANY, 4, 2>(q, a, items, Hq, s);
+    // Eight waves a workgroup share an expert's columns; four leave more workgroups, and shorter
+    // ones, where the row is short.  Eight and four: 32 tokens through 8 Q8_0 experts of 14336 x
+    // 4096 229 and 235 us, one through Q4_0 ones 40.6 and 41.6; 8 tokens through 8 of 128 of 768 x
+    // 2048 35.0 and 33.0, 4 through 6 of 64 of 1536 x 2048 30.4 and 29.4, 24 57.7 and 58.5.
+    const bool eight = q.K > 2048 && items * (q.N / 64) >= 256;
+    const hipError_t e = eight ? moe_glu<TF, MANY, 8, 2>(q, a, items, Hq, s) : moe_glu<TF, MANY, 4, 2>(q, a, items, Hq, s);
     if (e != hipSuccess) return e;
     const bool two = down_parts(q) == 2;
     if (by_token(q)) return two ? moe_down_tokens_kw<TF, 2, 4>(q, a, Hq, s) : moe_down_tokens_kw<TF, 1, 2>(q, a, Hq, s);
