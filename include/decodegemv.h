@@ -645,7 +645,7 @@ dg_status dg_sample_rows(const void* x, int dtype, const float* u, const float* 
  *                  outside 0..C-1 is ignored.
  *     lens         int32 [R], or NULL for T everywhere; cut to 0..T.
  *     prompt_lens  int32 [R], or NULL for 0; cut to 0..lens[r].
- *     T, ldt       0 <= T <= ldt < 2^31.
+ *     T, ldt       0 <= T <= ldt < 2^31, T <= 2^30.
  *     repetition   float32 [R], or NULL: off.  0, a negative number, 1 or NaN:
  *                  off for the row.
  *     frequency, presence  float32 [R], or NULL for 0.
@@ -692,7 +692,8 @@ dg_status dg_adjust_rows(const void* x, void* y, int dtype, int64_t R, int64_t C
  *
  *   x        device [M][ld] of `dtype`, aligned to the element.
  *   bias     device float32 [E], or NULL.
- *   ids      device int32 [M][k].   weights  device float32 [M][k].
+ *   ids      device int32 [M][k].   weights  device float32 [M][k].  They may
+ *            not overlap x, bias or each other.
  *   M        0 <= M < 2^31 (0 launches nothing).  1 <= E <= 1024, E <= ld < 2^31,
  *            1 <= k <= 64, k <= E.   scale finite.
  * Errors: DG_ERR_ARG (dtype, score, scale), DG_ERR_SHAPE, DG_ERR_NULL,
@@ -707,7 +708,8 @@ dg_status dg_adjust_rows(const void* x, void* y, int dtype, int64_t R, int64_t C
  * DG_ACT_*), H is what dg_quantize_q8_1 makes of the fp32 products, and the
  * weighted sum is fp32 in the order of j.  Results are bit-reproducible, and a
  * token's do not depend on the other tokens of the call.  Each chosen expert's
- * weights are read once for every 16 of its tokens.
+ * weights are read once for every 16 of its tokens; the down matrices of a few
+ * tokens once for each of them, where that costs less than another launch.
  *
  *   Wg, Wu   device, the experts' gate and up matrices in 16-row tiles, one
  *            after the other: what dg_repack_q4_0_tiles / dg_repack_q8_0_tiles
@@ -718,7 +720,7 @@ dg_status dg_adjust_rows(const void* x, void* y, int dtype, int64_t R, int64_t C
  *            adds nothing, its weight is not read.  An id may come twice.
  *   weights  device float32 [M][k].
  *   Y        device [M][K] of `ydtype`, aligned to the element; a token
- *            without experts gets zeros.
+ *            without experts gets zeros.  No operand may overlap it or ws.
  *   N, K     multiples of 256, 0 <= N, K <= 2^26; E * N, E * K < 2^31.
  *            K = 0 launches nothing; N = 0 gives Y = 0.
  *   M, E, k  0 <= M <= 4096, 1 <= E <= 1024, k >= 0, M * k <= 4096.  M = 0
@@ -763,9 +765,9 @@ dg_status dg_moe_q8_0(const void* Wg, const void* Wu, const void* Wd, const void
  *   ranks    device int32 [L], or NULL for R; cut to 0..R.  Rows of A and
  *            columns of B from ranks[a] on add nothing, whatever they hold.
  *   base     device float32 [M][N], or NULL for 0.  It may be Y itself.
- *   Y        device float32 [M][N].
+ *   Y        device float32 [M][N].  No other operand may overlap it.
  *   M        0 <= M < 2^31.  N: 0 <= N < 2^31.  M = 0 or N = 0 launches nothing.
- *   K        a multiple of 8, 0 <= K <= ld < 2^31; 0: h = 0.
+ *   K        a multiple of 8, 0 <= K <= 2^30, K <= ld < 2^31; 0: h = 0.
  *   R        a multiple of 8, 8 <= R <= 512.   L  0 <= L < 2^31.
  *   ws       device workspace of dg_lora_workspace_bytes(M, K, R) bytes,
  *            16-byte aligned; contents on entry do not matter; the call owns it

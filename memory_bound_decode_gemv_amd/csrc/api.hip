@@ -14,6 +14,7 @@ namespace {
 thread_local std::string g_last_hip_error;
 
 constexpr int64_t kI32Max = 2147483647;
+constexpr int64_t kAdjustMaxTokens = int64_t(1) << 30, kLoraMaxK = int64_t(1) << 30;   // 32-bit counters in the kernels
 constexpr int64_t kQuantMaxK = int64_t(1) << 26;   // Q4_0 / Q8_0 rows: 32-bit copy offsets in every kernel
 
 dg_status hip_status(hipError_t e) {
@@ -538,7 +539,7 @@ dg_status dg_adjust_rows(const void* x, void* y, int dtype, int64_t R, int64_t C
     if (!dtype_ok(dtype) || !a.bias_ids != !a.bias) return DG_ERR_ARG;
     if (R < 0 || R > kI32Max || C < 0 || C >= kI32Max || ld < C || ld > kI32Max || ldy < C || ldy > kI32Max)
         return DG_ERR_SHAPE;
-    if (a.tokens && (a.T < 0 || a.ldt < a.T || a.ldt > kI32Max)) return DG_ERR_SHAPE;
+    if (a.tokens && (a.T < 0 || a.T > kAdjustMaxTokens || a.ldt < a.T || a.ldt > kI32Max)) return DG_ERR_SHAPE;
     if (a.bias && (a.B < 0 || a.B > 65535)) return DG_ERR_SHAPE;
     if (a.mask && (a.ldm < (C + 31) / 32 || a.ldm > kI32Max)) return DG_ERR_SHAPE;
     if (x == y && x && ldy != ld && R > 1) return DG_ERR_SHAPE;   // rows would overlap others
@@ -584,14 +585,14 @@ dg_status dg_moe_q8_0(const void* Wg, const void* Wu, const void* Wd, const void
 }
 
 size_t dg_lora_workspace_bytes(int64_t M, int64_t K, int64_t R) {
-    return M < 0 || M > kI32Max || K < 0 || K > kI32Max || R < 8 || R > 512 ? 0 : lora_workspace_bytes(M, K, R);
+    return M < 0 || M > kI32Max || K < 0 || K > kLoraMaxK || R < 8 || R > 512 ? 0 : lora_workspace_bytes(M, K, R);
 }
 
 dg_status dg_lora_rows(const void* x, int dtype, const void* A, const void* B, int wdtype, const int32_t* adapter,
                        const float* scale, const int32_t* ranks, const float* base, float* Y, int64_t M, int64_t N,
                        int64_t K, int64_t R, int64_t L, int64_t ld, void* ws, size_t ws_bytes, dg_stream stream) {
     if (!dtype_ok(dtype) || (wdtype != DG_DTYPE_F16 && wdtype != DG_DTYPE_BF16)) return DG_ERR_ARG;
-    if (M < 0 || M > kI32Max || N < 0 || N > kI32Max || K < 0 || K % 8 != 0 || ld < K || ld % 8 != 0 || ld > kI32Max ||
+    if (M < 0 || M > kI32Max || N < 0 || N > kI32Max || K < 0 || K > kLoraMaxK || K % 8 != 0 || ld < K || ld % 8 != 0 || ld > kI32Max ||
         R < 8 || R > 512 || R % 8 != 0 || L < 0 || L > kI32Max)
         return DG_ERR_SHAPE;
     if (M == 0 || N == 0) return DG_OK;

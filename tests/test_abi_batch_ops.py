@@ -89,7 +89,7 @@ def test_workspace_sizes(lib):
     for N, K, M, k in ((255, 256, 1, 1), (256, 256, 4096, 2), (256, 256, -1, 1), (256, 256, 1, -1)):
         assert lib.dg_moe_workspace_bytes(N, K, M, k) == 0
     assert lib.dg_lora_workspace_bytes(3, 64, 8) >= 3 * 8 * 4
-    for M, K, R in ((-1, 64, 8), (3, -8, 8), (3, 64, 0), (3, 64, 520)):
+    for M, K, R in ((-1, 64, 8), (3, -8, 8), (3, (1 << 30) + 8, 8), (3, 64, 0), (3, 64, 520)):
         assert lib.dg_lora_workspace_bytes(M, K, R) == 0
 
 
@@ -103,7 +103,7 @@ def lora(**change):
 @pytest.mark.parametrize("change,expect", [
     (dict(dtype=3), ARG), (dict(wdtype=F32), ARG), (dict(wdtype=-1), ARG),
     (dict(M=-1), SHAPE), (dict(M=1 << 31), SHAPE), (dict(N=-1), SHAPE), (dict(N=1 << 31), SHAPE),
-    (dict(K=60), SHAPE), (dict(K=-8), SHAPE), (dict(ld=56), SHAPE), (dict(ld=68), SHAPE), (dict(ld=1 << 31), SHAPE),
+    (dict(K=60), SHAPE), (dict(K=-8), SHAPE), (dict(K=(1 << 30) + 8, ld=(1 << 31) - 8), SHAPE), (dict(ld=56), SHAPE), (dict(ld=68), SHAPE), (dict(ld=1 << 31), SHAPE),
     (dict(R=0), SHAPE), (dict(R=12), SHAPE), (dict(R=520), SHAPE), (dict(L=-1), SHAPE), (dict(L=1 << 31), SHAPE),
     *((dict([(n, None)]), NULL) for n in ("x", "A", "B", "adapter", "Y")),
     *((dict([(n, P(0x1008))]), MISALIGNED) for n in ("x", "A", "B", "ws")),
@@ -138,6 +138,7 @@ B = P(0x2000)
     ((A, A, F32, 4, 100, 100, 104), {}, SHAPE),          # in place, with other rows
     ((A, B, F32, 4, 100, 100, 100), dict(T=11), SHAPE), ((A, B, F32, 4, 100, 100, 100), dict(T=-1), SHAPE),
     ((A, B, F32, 4, 100, 100, 100), dict(ldt=1 << 31), SHAPE),
+    ((A, B, F32, 4, 100, 100, 100), dict(T=(1 << 30) + 1, ldt=(1 << 31) - 1), SHAPE),
     ((A, B, F32, 4, 100, 100, 100), dict(B=-1), SHAPE), ((A, B, F32, 4, 100, 100, 100), dict(B=65536), SHAPE),
     ((A, B, F32, 4, 100, 100, 100), dict(ldm=3), SHAPE), ((A, B, F32, 4, 100, 100, 100), dict(ldm=1 << 31), SHAPE),
     ((None, B, F32, 4, 100, 100, 100), {}, NULL), ((A, None, F32, 4, 100, 100, 100), {}, NULL),
