@@ -188,7 +188,8 @@ def test_two_streams_with_their_own_workspaces(dg, dev, orc):
 
 
 def test_calls_one_after_another_share_a_workspace(dg, dev, orc):
-    """Two layers on one stream through the same memory: each call is done with it when the next begins."""
+    """Two layers on one stream through the same memory, eager and as two captured graphs in turn: each call is done with it
+    when the next begins."""
     import torch
     s, t = Step(dg, dev, orc, "q4_0", 12, seed=5), Step(dg, dev, orc, "q8_0", 12, seed=6)
     want = []
@@ -200,11 +201,57 @@ def test_calls_one_after_another_share_a_workspace(dg, dev, orc):
         c.set_state(start)
     need = max(c.mws.numel() for c in (s, t))
     s.mws = t.mws = s.lws = t.lws = torch.full((need,), 0x11, dtype=torch.uint8, device=dev)
+    starts = [c.state() for c in (s, t)]
     for c in (s, t):
         c.run()
     torch.cuda.synchronize()
     for c, w in zip((s, t), want):
         for a, b in zip(c.outputs(), w):
+            assert torch.equal(a, b)
+    graphs = []
+    for c in (s, t):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.run()
+    for _ in range(3):
+        for c, start in zip((s, t), starts):
+            c.set_state(start)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for c, w in zip((s, t), want):
+            for a, b in zip(c.outputs(), w):
+                assert torch.equal(a, b)
+
+
+def test_explicit_streams(dg, dev, orc):
+    """stream= as a stream or its handle: the calls run there, behind that stream's own work."""
+    import torch
+    s = Step(dg, dev, orc, "q4_0", 5, seed=9)
+    s.run()
+    torch.cuda.synchronize()
+    x8, n16, logits = s.x8.clone(), s.n16.clone(), s.logits.clone()
+    side = torch.cuda.Stream()
+
+    def calls(stream):
+        y, a, z = torch.zeros_like(s.y), torch.zeros_like(s.a), torch.zeros_like(logits)
+        ids, w = torch.zeros_like(s.ids), torch.zeros_like(s.w)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            late = torch.zeros_like(s.rl)
+            for _ in range(50):   # work that the calls have to come after
+                late.add_(s.rl / 50)
+            late.copy_(s.rl)
+        dg.dg_moe_route(late if stream is not None else s.rl, ids, w, stream=stream)
+        dg.dg_moe_q4_0(*(s.moe.tiles[n] for n in ("Wg", "Wu", "Wd")), x8, ids, w, y, s.F, s.D, s.M, s.E, ws=s.mws, stream=stream)
+        dg.dg_lora_rows(n16, s.A, s.B, s.adapter, a, base=y, scale=s.scale, ws=s.lws, stream=stream)
+        dg.dg_adjust_rows(logits, z, tokens=s.tokens, lens=s.lens, repetition=s.rep, mask=s.mask, stream=stream)
+        torch.cuda.synchronize()
+        return [ids, w, y, a, z]
+    want = calls(None)
+    assert (want[0] >= 0).all()
+    for stream in (side, side.cuda_stream):
+        for a, b in zip(calls(stream), want):
             assert torch.equal(a, b)
 
 
