@@ -215,18 +215,32 @@ struct MoeArgs {
 // their number.  Zero where the workgroup has nothing to do.  Every wave comes
 // to the same result.
 __device__ __forceinline__ int claim(const MoeArgs& a, int item, uint16_t* list, int& e, int lane, int wave) {
+    // Runs of 64 slots on their way together.  1, 2 and 4: 200 tokens through 8 of 128 experts 138.4, 132.6,
+    // 129.9 us, 24 through 6 of 64 56.8, 56.7, 56.6, one through 2 of 8 40.6, 40.8, 41.0.
+    constexpr int U = 2;
+    int id[U];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = a.ids[min(p0 + u * kWave + lane, a.P - 1)];
+    };
+    load(0);
     e = a.by_slot ? a.ids[item] : item;
     if (e < 0 || e >= a.E) return 0;
     int cnt = 0;
-    for (int p0 = 0; p0 < a.P; p0 += kWave) {
-        const int p = p0 + lane;
-        const bool hit = p < a.P && a.ids[p] == e;
-        const uint64_t mask = __ballot(hit);
-        if (a.by_slot && cnt == 0 && mask != 0 && p0 + __builtin_ctzll(mask) < item) return 0;   // an earlier slot's
-        if (wave == 0 && hit) list[cnt + __popcll(mask & (((uint64_t)1 << lane) - 1))] = (uint16_t)p;
-        cnt += __popcll(mask);
+    for (int p0 = 0;;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int p = p0 + u * kWave + lane;
+            const bool hit = p < a.P && id[u] == e;
+            const uint64_t mask = __ballot(hit);
+            if (a.by_slot && cnt == 0 && mask != 0 && p0 + u * kWave + __builtin_ctzll(mask) < item) return 0;   // an earlier slot's
+            if (wave == 0 && hit) list[cnt + __popcll(mask & (((uint64_t)1 << lane) - 1))] = (uint16_t)p;
+            cnt += __popcll(mask);
+        }
+        p0 += U * kWave;
+        if (p0 >= a.P) return cnt;
+        load(p0);
     }
-    return cnt;
 }
 
 // Where a lane's A operands lie: M columns in LDS from `column` on, `stride`
@@ -601,26 +615,35 @@ k_moe_down_tokens(const uint8_t* __restrict__ Wd, const uint8_t* __restrict__ Hq
     }
 }
 
-// Y[m][n] = sum_j w[m][j] part[m k + j][n], in the order of j; four n a thread.
+constexpr int kSumSlots = 8, kSumThreads = 64;
+
+// Y[m][n] = sum_j w[m][j] part[m k + j][n], in the order of j; four n a thread, kSumSlots
+// slots' values on their way together (what a slot without an expert holds is not used).
 template <class T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kSumThreads)
 k_moe_sum(const float* __restrict__ part, const int32_t* __restrict__ ids, const float* __restrict__ weights,
           T* __restrict__ Y, int K, int E, int k) {
 #pragma clang fp contract(off)
     const int n = (int)(blockIdx.x * blockDim.x + threadIdx.x) * 4;
     const int m = blockIdx.y;
     if (n >= K) return;
-    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < k; ++j) {
-        const int p = m * k + j;
-        const int e = ids[p];
-        if (e < 0 || e >= E) continue;
-        const float w = weights[p];
-        const float4 v = *reinterpret_cast<const float4*>(part + (size_t)p * K + n);
-        y[0] += w * v.x;
-        y[1] += w * v.y;
-        y[2] += w * v.z;
-        y[3] += w * v.w;
+    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j0 = 0; j0 < k; j0 += kSumSlots) {
+        f32x4 v[kSumSlots];
+#pragma unroll
+        for (int j = 0; j < kSumSlots; ++j)
+            v[j] = *reinterpret_cast<const f32x4*>(part + (size_t)(m * k + min(j0 + j, k - 1)) * K + n);
+#pragma unroll
+        for (int j = 0; j < kSumSlots; ++j) {
+            const int p = m * k + min(j0 + j, k - 1);
+            const bool has = j0 + j < k && (uint32_t)ids[p] < (uint32_t)E;   // wave-uniform
+            const float w = weights[p];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float next = y[i] + w * v[j][i];
+                y[i] = has ? next : y[i];
+            }
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) Y[(size_t)m * K + n + i] = (T)bind_f32(y[i]);
@@ -808,7 +831,7 @@ template <class T>
 hipError_t moe_sum(const MoeLayer& q, hipStream_t s) {
     const int P = (int)(q.M * q.k);
     const float* const part = (const float*)((const uint8_t*)q.ws + (size_t)P * (q.N / 32) * kQ81Bytes);
-    hipLaunchKernelGGL((k_moe_sum<T>), dim3((unsigned)((q.K / 4 + 255) / 256), (unsigned)q.M), dim3(256), 0, s, part,
+    hipLaunchKernelGGL((k_moe_sum<T>), dim3((unsigned)((q.K / 4 + kSumThreads - 1) / kSumThreads), (unsigned)q.M), dim3(kSumThreads), 0, s, part,
                        q.ids, q.weights, (T*)q.Y, (int)q.K, (int)q.E, q.k);
     return hipGetLastError();
 }
