@@ -110,32 +110,38 @@ __device__ __forceinline__ int rows_of(const LoraArgs& a, int64_t w0, int item, 
 
 constexpr int kDotWaves = 4;
 
-// The dot of one rank's row of A with a row of x, in every lane.  A lane has every
+// The dots of a row of x with TR ranks' rows of A, in every lane.  A lane has every
 // 64th run of eight columns, U of them in flight, and adds them in their order.
-template <class EX, class EW>
-__device__ __forceinline__ float dot_row(const typename EX::raw* xr, const typename EW::raw* Ar, int K, int lane) {
-    constexpr int U = sizeof(typename EX::raw) == 2 ? 8 : 4;
-    float sum = 0.0f;
+template <class EX, class EW, int TR>
+__device__ __forceinline__ void dot_rows(const typename EX::raw* xr, const typename EW::raw* const (&Ar)[TR], int K,
+                                         int lane, float (&sum)[TR]) {
+    constexpr int U = sizeof(typename EX::raw) == 2 && TR == 1 ? 8 : 4;
+#pragma unroll
+    for (int t = 0; t < TR; ++t) sum[t] = 0.0f;
     for (int s = 0; s < K; s += U * 512) {
-        Eight<EW> w[U];
+        Eight<EW> w[TR][U];
         Eight<EX> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = min(s + u * 512 + lane * 8, K - 8);
-            w[u].load(Ar + k);
+#pragma unroll
+            for (int t = 0; t < TR; ++t) w[t][u].load(Ar[t] + k);
             v[u].load(xr + k);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool some = s + u * 512 + lane * 8 < K;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float next = fmaf(EW::widen(w[u].e[e]), EX::widen(v[u].e[e]), sum);
-                sum = some ? next : sum;
-            }
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int t = 0; t < TR; ++t) {
+                    const float next = fmaf(EW::widen(w[t][u].e[e]), EX::widen(v[u].e[e]), sum[t]);
+                    sum[t] = some ? next : sum[t];
+                }
         }
     }
-    return wave_sum_f32(sum);
+#pragma unroll
+    for (int t = 0; t < TR; ++t) sum[t] = wave_sum_f32(sum[t]);
 }
 
 // h of one row and kDotWaves ranks, one a wave: x and A come from L2 but for their first
@@ -152,8 +158,10 @@ k_lora_dots(const typename EX::raw* __restrict__ x, const typename EW::raw* __re
     const int64_t m = a.window0 + blockIdx.y;
     const int ad = valid(a, a.adapter[m]);
     if (ad < 0 || r >= rank_of(a, ad)) return;
-    const float sum = dot_row<EX, EW>(x + m * a.ld, A + ((size_t)ad * a.R + r) * a.K, a.K, lane);
-    if (lane == 0) h[m * a.R + r] = sum;
+    const typename EW::raw* const Ar[1] = {A + ((size_t)ad * a.R + r) * a.K};
+    float sum[1];
+    dot_rows<EX, EW, 1>(x + m * a.ld, Ar, a.K, lane, sum);
+    if (lane == 0) h[m * a.R + r] = sum[0];
 }
 
 // The value of lane i's partner at a level of the sum over 2 D lanes: up to four, the
@@ -291,14 +299,18 @@ constexpr int kOneWaves = 16;
 constexpr int kOneBlock = 1024;   // outputs of a workgroup
 
 // Whether one launch does the whole call: every workgroup of a row makes its h for
-// itself, so A has to be little, and the workgroups few.  Both sides, microseconds on
-// the GPU in one and two launches (the host's second launch comes on top), bfloat16:
-// 1 x 4096 x 4096, R 16: 4.9, 6.0; R 8: 3.9, 5.9; R 32: 7.4, 6.1; 8 x 14336 x 4096,
-// R 16 (112 workgroups): 6.1, 6.4; 8 x 28672 (224): 7.1, 7.1.
+// itself, so A has to be little, and the workgroups few.  Microseconds on the GPU in one
+// and two launches (the host's second launch, about 3, comes on top), bfloat16, rows x
+// outputs x columns, rank: 1 x 4096 x 4096, 8: 3.9, 5.9; 16: 4.9, 6.0; 32: 6.4, 6.0; 4 x
+// 4096 x 8192, 8: 5.5, 8.0; 16 x 4096 x 2048, 32: 4.9, 7.6; 1 x 4096 x 1024, 64 (with four
+// ranks a wave, one after the other) 12.0, 6.0; 8 x 14336 x 4096 (112 workgroups), 16: 6.1,
+// 6.4; 32: 8.1, 6.7.  Binary32 rows of x, 4 x 4096 x 8192, 8: 5.4, 6.6; 16: 8.2, 6.6.
 bool one_launch(const LoraRows& q) {
-    constexpr int64_t kMostA = 65536, kMostGroups = 128;
-    return q.K > 0 && q.R <= 64 && q.R * q.K <= kMostA && q.M <= kMostGroups &&
-           q.M * ((q.N + kOneBlock - 1) / kOneBlock) <= kMostGroups;
+    constexpr int64_t kMostGroups = 128, kMostReads = int64_t(1) << 23;
+    const int64_t most = q.dtype == DG_DTYPE_F32 ? 65536 : 131072, one = q.R * q.K;
+    if (one == 0 || one > most || q.R > 2 * kOneWaves || q.M > kMostGroups) return false;
+    const int64_t groups = q.M * ((q.N + kOneBlock - 1) / kOneBlock);
+    return groups <= kMostGroups && groups * one <= kMostReads;
 }
 
 // The sums are those of the two launches.  Grid: (blocks of outputs, rows).
@@ -319,9 +331,20 @@ k_lora_one(const typename EX::raw* __restrict__ x, const typename EW::raw* __res
         return;
     }
     const int rank = rank_of(a, ad);
-    for (int r = wave; r < rank; r += kOneWaves) {
-        const float sum = dot_row<EX, EW>(x + m * a.ld, A + ((size_t)ad * a.R + r) * a.K, a.K, lane);
-        if (lane == 0) hs[r] = sum;
+    constexpr int TR = LG <= 2 ? 1 : 2;   // ranks of a wave
+    static_assert(8 * LG <= TR * kOneWaves, "every rank");
+    if (wave < rank) {
+        const typename EW::raw* Ar[TR];
+        float sum[TR];
+#pragma unroll
+        for (int t = 0; t < TR; ++t) {   // a rank that there is not: the first again
+            const int r = wave + t * kOneWaves;
+            Ar[t] = A + ((size_t)ad * a.R + (r < rank ? r : wave)) * a.K;
+        }
+        dot_rows<EX, EW, TR>(x + m * a.ld, Ar, a.K, lane, sum);
+#pragma unroll
+        for (int t = 0; t < TR; ++t)
+            if (lane == 0 && wave + t * kOneWaves < rank) hs[wave + t * kOneWaves] = sum[t];
     }
     lds_barrier();
     float h[1][8];
@@ -333,10 +356,7 @@ k_lora_one(const typename EX::raw* __restrict__ x, const typename EW::raw* __res
 
 template <class EX, class EW>
 hipError_t lora_one(const LoraRows& q, const LoraArgs& a, hipStream_t s) {
-    const auto kernel = q.R <= 8    ? k_lora_one<EX, EW, 1>
-                        : q.R <= 16 ? k_lora_one<EX, EW, 2>
-                        : q.R <= 32 ? k_lora_one<EX, EW, 4>
-                                    : k_lora_one<EX, EW, 8>;
+    const auto kernel = q.R <= 8 ? k_lora_one<EX, EW, 1> : q.R <= 16 ? k_lora_one<EX, EW, 2> : k_lora_one<EX, EW, 4>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)((q.N + kOneBlock - 1) / kOneBlock), (unsigned)q.M), dim3(64 * kOneWaves),
                        0, s, (const typename EX::raw*)q.x, (const typename EW::raw*)q.A, (const typename EW::raw*)q.B,
                        q.base ? q.base : q.Y, q.Y, q.base != nullptr, a);

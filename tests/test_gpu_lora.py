@@ -87,7 +87,7 @@ class Case:
 SHAPES = [(1, 1, 8, 8, 1), (1, 300, 4096, 16, 3), (2, 255, 520, 24, 2), (3, 1001, 8, 8, 2), (5, 257, 1032, 40, 1),
           (7, 64, 2048, 64, 4), (16, 513, 768, 16, 5), (17, 130, 4104, 128, 3), (33, 77, 264, 8, 40), (64, 100, 512, 32, 2),
           (65, 1030, 256, 16, 9), (130, 45, 1000, 72, 3), (200, 515, 136, 32, 7), (1, 97, 16392, 512, 2), (3, 31, 24, 504, 1),
-          (1100, 70, 64, 8, 3), (2049, 33, 40, 16, 5), (4, 2101, 1032, 56, 3), (128, 1024, 72, 8, 6), (129, 1024, 72, 8, 6)]
+          (1100, 70, 64, 8, 3), (2049, 33, 40, 16, 5), (4, 2101, 1032, 56, 3), (4, 2101, 1032, 32, 3), (2, 1500, 5000, 24, 2), (6, 1024, 8200, 8, 3), (128, 1024, 72, 8, 6), (129, 1024, 72, 8, 6)]
 
 
 @pytest.mark.parametrize("x", TYPES)
@@ -111,7 +111,7 @@ def test_options(dg, dev, M, N, K, R, L):
     assert np.array_equal(c.run(dg, dev), c.base.numpy())
 
 
-@pytest.mark.parametrize("N,R", [(203, 40), (3001, 40), (45, 136)])
+@pytest.mark.parametrize("N,R", [(203, 40), (3001, 40), (45, 136), (203, 32), (3001, 32), (1200, 16)])
 def test_ranks(dg, dev, N, R):
     """Every rank from none to all and beyond; what lies past a rank is not read as a number."""
     ranks = [0, 1, 2, 7, 8, 9, 15, 16, 23, 24, 25, 31, 32, 33, 40, 41, -3, 1 << 30]
@@ -133,7 +133,7 @@ def test_no_columns_and_no_adapters(dg, dev):
     assert np.array_equal(c.run(dg, dev), c.base.numpy())
 
 
-@pytest.mark.parametrize("N,K,R", [(333, 1544, 48), (2101, 1544, 16), (2101, 264, 64)])
+@pytest.mark.parametrize("N,K,R", [(333, 1544, 48), (2101, 1544, 16), (2101, 264, 64), (2101, 1544, 32)])
 @pytest.mark.parametrize("pattern", ["one", "runs", "mixed", "distinct"])
 def test_a_row_does_not_depend_on_the_others(dg, dev, pattern, N, K, R):
     """However the adapters of the batch are spread, each row is the row of a call of its own, bit for bit."""
