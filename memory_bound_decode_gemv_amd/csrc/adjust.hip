@@ -23,7 +23,7 @@
 // Tokens, logits and mask are on their way before the first wait.
 #include <algorithm>
 
-#include "dg_internal.h"
+#include "dg_batch.h"
 #include "q4_common.h"
 
 #pragma clang fp contract(off)

@@ -5,6 +5,7 @@
 #include <atomic>
 #include <string>
 
+#include "dg_batch.h"
 #include "dg_device.h"
 #include "dg_internal.h"
 

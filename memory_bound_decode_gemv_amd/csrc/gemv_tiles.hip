@@ -67,8 +67,6 @@
 namespace dg {
 namespace {
 
-using namespace tiles;
-
 // ---------------------------------------------------------------------------
 // Rearrangement: one thread per 16-byte slot of the tiled layout (144 per
 // group).  Source reads are 2-byte loads (block fields sit at even offsets).

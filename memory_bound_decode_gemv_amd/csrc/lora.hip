@@ -25,7 +25,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "dg_internal.h"
+#include "dg_batch.h"
 #include "q4_common.h"
 
 namespace dg {

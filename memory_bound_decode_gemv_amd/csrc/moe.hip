@@ -19,14 +19,12 @@
 #include <cmath>
 #include <type_traits>
 
-#include "dg_internal.h"
+#include "dg_batch.h"
 #include "q81_rules.h"
 #include "tiles.h"
 
 namespace dg {
 namespace {
-
-using namespace tiles;
 
 // At most 128 registers a wave: 16 waves to a CU.  Left alone the compiler takes a
 // few more for some shapes, and half the waves no longer fit (24 tokens through 64

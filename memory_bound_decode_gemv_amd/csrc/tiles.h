@@ -8,7 +8,7 @@
 #include "mfma_formats.h"
 
 namespace dg {
-namespace tiles {
+namespace {   // each source that includes this has its own
 
 using namespace q4;
 using namespace mfma;
@@ -206,5 +206,5 @@ struct TileOut {
     }
 };
 
-}  // namespace tiles
+}  // namespace
 }  // namespace dg
