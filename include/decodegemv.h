@@ -717,7 +717,7 @@ dg_status dg_adjust_rows(const void* x, void* y, int dtype, int64_t R, int64_t C
  *   Wd       device, the same of the down matrices, the [E * K][N] stack.
  *   Xq       device, M columns of K/32 Q8_1 blocks, 16-byte aligned.
  *   ids      device int32 [M][k].  An id outside 0..E-1 is no expert: the slot
- *            adds nothing, its weight is not read.  An id may come twice.
+ *            adds nothing, whatever its weight is.  An id may come twice.
  *   weights  device float32 [M][k].
  *   Y        device [M][K] of `ydtype`, aligned to the element; a token
  *            without experts gets zeros.  No operand may overlap it or ws.

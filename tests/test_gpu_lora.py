@@ -175,6 +175,19 @@ def test_infinities_stay_in_their_row(dg, dev):
     assert np.array_equal(got[clean], want[clean]) and not np.isfinite(got[[7, 20]]).any()
 
 
+def test_very_many_rows(dg, dev):
+    """More rows than a launch takes, of the first product and of the windows: one adapter, rows without it among them."""
+    M, N, K, R = 140000, 9, 16, 8
+    c = Case(41, M, N, K, R, 1, "bf16", adapter=np.arange(M) % 5 % 2 - 1)
+    got = c.run(dg, dev)
+    x, A, B = c.x.double().numpy(), c.A[0].double().numpy(), c.B[0].double().numpy()
+    has, s = (c.adapter.numpy() == 0)[:, None], abs(float(c.scale[0]))
+    h, dh = x @ A.T, (K + 1) * STEP * (np.abs(x) @ np.abs(A).T)
+    want = c.base.double().numpy() + np.where(has, float(c.scale[0]) * (h @ B.T), 0.0)
+    tol = np.where(has, s * (dh @ np.abs(B).T + (R + 2) * STEP * ((np.abs(h) + dh) @ np.abs(B).T)), 0.0) + STEP * np.abs(want)
+    assert (np.abs(got - want) <= 1.01 * tol).all()
+
+
 def test_adapters_past_32_bit_offsets(dg, dev):
     """The last of adapters whose weights span more than 2^32 bytes, each."""
     import torch

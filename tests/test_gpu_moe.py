@@ -271,8 +271,14 @@ def test_rows_without_experts_and_odd_ids(dg, dev, orc, fmt):
     c = Layer(dg, dev, orc, fmt, 1500, E, 512, 256, M, ids)
     Y, H = c.check()
     assert not Y[0].any()
+    c.w[(ids < 0) | (ids >= E)] = np.nan      # what slots without an expert hold, in the workspace too, does not count
+    assert np.array_equal(Y, c.run(fill=0xFF)[0])
     one = Layer(dg, dev, orc, fmt, 1500, E, 512, 256, M, np.full((M, 3), 5))   # 27 columns of one expert
     one.check()
+    many = Layer(dg, dev, orc, fmt, 1500, E, 512, 256, 60, np.where(np.arange(180).reshape(60, 3) % 7, ids[np.arange(60) % M], -1))
+    Y, H = many.check()                        # past what one kernel makes of a token
+    many.w[(many.ids < 0) | (many.ids >= E)] = np.inf
+    assert np.array_equal(Y, many.run(fill=0xFF)[0])
     none = Layer(dg, dev, orc, fmt, 1500, E, 512, 256, M, np.full((M, 3), -1))
     Y, H = none.run()
     assert not Y.any() and (H == 0xA5).all()
