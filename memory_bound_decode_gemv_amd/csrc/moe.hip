@@ -8,7 +8,14 @@
 // Three launches: the gated products of every (expert, 32 rows) into Q8_1
 // columns, the down products of every (expert, row group) into one fp32 column
 // per slot (a slot is a token's j-th expert, p = m k + j), and the slots'
-// weighted sum in the order of j.
+// weighted sum in the order of j; for a few tokens the last two are one.
+//
+// The weights of the chosen experts are nearly all that is read, so large experts
+// are bound by HBM: 32 tokens through 2 of 8 Q8_0 experts of 14336 x 4096 (1.5 GB)
+// 150 + 76 + 4 us, 6.7 TB/s; one token through Q4_0 ones 24.2 + 16.5, 5.4 and 4.0
+// TB/s.  Small experts are bound by the dependent steps of each launch (ids, first
+// weights, products, sums): one token through 8 of 128 of 768 x 2048 8.6 + 5.1 us for
+// 21 MB; between them 24 tokens through 6 of 64 of 1536 x 2048 35 + 19 + 4, 5.4 TB/s.
 //
 // A workgroup finds its own work: it reads the ids (at most 4096), and what
 // matches its expert are its columns.  Where there are no more slots than
@@ -41,7 +48,11 @@ constexpr int kTileColumns = 16;
 // and no infinity but the lowest maps to.  Each of the k choices is a maximum over
 // the wave, then the lowest place that holds it.  Scores of softmax ranked by
 // their logits are made for the chosen alone, in the lanes that store them; the
-// softmax's sum is left out where the weights are divided by their own.
+// softmax's sum is left out where the weights are divided by their own.  One token
+// of 64 experts, k 6: 2.6 us, the launch and the choices one after another; 4096 of
+// 256, k 8, with a sigmoid and a bias 8.1, bound by vector instructions: some 600 a
+// wave, issued in half the busy cycles.  Ranks sorted in each lane first, so that a
+// choice looks at one a lane: 8.6, and 78 against 11 for 1024 experts.
 // ---------------------------------------------------------------------------
 struct RouteArgs {
     const float* bias;
