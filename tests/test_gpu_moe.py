@@ -285,6 +285,15 @@ def test_rows_without_experts_and_odd_ids(dg, dev, orc, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["q4_0", "q8_0"])
+@pytest.mark.parametrize("k", [4, 20])
+def test_an_expert_many_times_in_few_tokens(dg, dev, orc, fmt, k):
+    """More columns of one expert than tokens: all slots the same, and two experts in turn; few slots a token and many."""
+    for ids in (np.full((4, k), 2), np.arange(4 * k).reshape(4, k) % 2 * 3):
+        for E in (6, 200):     # workgroups by expert and by slot
+            Layer(dg, dev, orc, fmt, 1800, E, 256, 512, 4, ids).check()
+
+
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0"])
 def test_a_token_does_not_depend_on_the_others(dg, dev, orc, fmt):
     """Alone, in a batch and beside others of its expert in any number: the same bits (columns in one pass and several)."""
     for E, N, K, M, k in ((3, 512, 4608, 45, 1), (3, 4608, 512, 30, 2), (8, 256, 512, 12, 3)):
@@ -300,6 +309,35 @@ def test_most_slots(dg, dev, orc):
     for E, M, k in ((2, 2048, 2), (1024, 64, 64)):
         c = Layer(dg, dev, orc, "q4_0", 1700, E, 256, 256, M, distinct(9, E, M, k))
         c.check()
+
+
+def test_experts_past_32_bit_offsets(dg, dev):
+    """The last of experts whose matrices span more than 2^33 bytes gives what the same weights in the first place give."""
+    import torch
+    E, N, K = 140, 14336, 4096
+    g = torch.Generator(device=dev).manual_seed(4)
+
+    def stack(rows, cols):
+        w = torch.empty(rows * (cols // 32) * 34, dtype=torch.uint8, device=dev)
+        dg.dg_quantize_q8_0(torch.randn(rows, cols, device=dev, generator=g) / math.sqrt(cols), w, rows, cols)
+        one = torch.empty(dg.dg_q8_0_tiles_bytes(rows, cols), dtype=torch.uint8, device=dev)
+        dg.dg_repack_q8_0_tiles(w, one, rows, cols)
+        all_ = torch.zeros(E * one.numel(), dtype=torch.uint8, device=dev)
+        all_[:one.numel()], all_[-one.numel():] = one, one
+        return all_
+    Wg, Wd = stack(N, K), stack(K, N)
+    assert Wg.numel() > 1 << 33
+    for M in (1, 20):      # a token's down products with their sum, and by themselves
+        Xq = torch.empty(M * K // 32 * 36, dtype=torch.uint8, device=dev)
+        dg.dg_quantize_q8_1(torch.randn(M, K, device=dev, generator=g), Xq, M, K)
+        w = torch.ones(M, 1, device=dev)
+        ws = torch.zeros(dg.dg_moe_workspace_bytes(N, K, M, 1), dtype=torch.uint8, device=dev)
+        Y = [torch.zeros(M, K, device=dev) for _ in range(3)]
+        for y, e in zip(Y, (0, E - 1, E // 2)):
+            ids = torch.full((M, 1), e, dtype=torch.int32, device=dev)
+            dg.dg_moe_q8_0(Wg, Wg, Wd, Xq, ids, w, y, N, K, M, E, ws=ws)
+        torch.cuda.synchronize()
+        assert Y[0].abs().max() > 0.1 and torch.equal(Y[0], Y[1]) and not Y[2].any()
 
 
 def test_empty_sizes(dg, dev):
