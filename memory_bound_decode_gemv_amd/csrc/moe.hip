@@ -5,7 +5,7 @@
 //   H[m][j] = Q8_1( act(Wg[e] X[m]) (Wu[e] X[m]) ),  e = ids[m][j]
 //   Y[m]    = sum_j w[m][j] (Wd[e] H[m][j])
 //
-// Three launches: the gated products of every (expert, 32 rows) into Q8_1
+// Three launches: the gated products of every (expert, 32 or 64 rows) into Q8_1
 // columns, the down products of every (expert, row group) into one fp32 column
 // per slot (a slot is a token's j-th expert, p = m k + j), and the slots'
 // weighted sum in the order of j; for a few tokens the last two are one.
@@ -743,9 +743,10 @@ hipError_t moe_glu(const MoeLayer& q, MoeArgs a, int64_t items, uint8_t* Hq, hip
     a.groups = (int)(q.N / (8 * RT));
     a.lds_sums = RT / 2 * (MANY ? 2 : 1) * 1024 + (MANY ? 16 : 8) * 8 * RT * 4;
     a.lds_cols = lds_for_columns(q, a);
-    set_runs(q, a, RT, kRuns<TF, 1>);
+    constexpr bool kLoop = kRuns<TF, 1> && RT == 4;   // eight waves: rows that are too long for it
+    set_runs(q, a, RT, kLoop);
     return over_groups(items, a, [&](unsigned grid) {
-        const auto kernel = a.run > 1 ? k_moe_glu<TF, MANY, kRuns<TF, 1>, RT, D> : k_moe_glu<TF, MANY, false, RT, D>;
+        const auto kernel = a.run > 1 ? k_moe_glu<TF, MANY, kLoop, RT, D> : k_moe_glu<TF, MANY, false, RT, D>;
         hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * RT), a.lds_cols + a.lds_sums + (size_t)a.P * 2, s,
                            (const uint8_t*)q.Wg, (const uint8_t*)q.Wu, (const uint8_t*)q.Xq, Hq, q.act, a);
     });
