@@ -46,7 +46,6 @@ struct AdjustArgs {
     dg_adjustments a;
     int64_t ld, ldy, first;
     int C, chunks;
-    int listed;   // entries of the list: tokens of a history or of a chunk
 };
 
 __device__ __forceinline__ int clampi(int v, int hi) { return min(max(v, 0), hi); }
@@ -245,14 +244,17 @@ __global__ void __launch_bounds__(kThreads) k_adjust(const E* x, E* y, AdjustArg
 template <class E, class W, int G>
 struct Config {
     static constexpr int kChunk = kThreads * (16 / (int)sizeof(E)) * G;
-    static int listed(const AdjustRows& q) { return q.a.tokens ? (int)std::min<int64_t>(q.a.T, kChunk) : 0; }
-    static size_t lds(const AdjustRows& q) {
-        if (!q.a.tokens && !q.a.bias) return 0;
-        return kChunk * sizeof(W) + kChunk / 8 + (q.a.bias ? (size_t)(q.a.B + 63) / 64 * 8 : 0) + (size_t)listed(q) * 2;
+    // The table, the bits, the biases' marks and the list: tokens of a history, at most a chunk's.
+    static constexpr size_t bytes(bool table, int64_t biases, int64_t tokens) {
+        return (table ? kChunk * sizeof(W) + kChunk / 8 : 0) + (size_t)(biases + 63) / 64 * 8 +
+               (size_t)std::min<int64_t>(tokens, kChunk) * 2;
     }
-    static bool fits(const AdjustRows& q) { return lds(q) <= 160 * 1024 - 256; }
+    static_assert(bytes(true, 65535, kChunk) <= 160 * 1024 - 256, "every call fits");
+    static size_t lds(const AdjustRows& q) {
+        return bytes(q.a.tokens || q.a.bias, q.a.bias ? q.a.B : 0, q.a.tokens ? q.a.T : 0);
+    }
     static hipError_t launch(const AdjustRows& q, hipStream_t s) {
-        AdjustArgs p{q.a, q.ld, q.ldy, 0, (int)q.C, (int)((q.C + kChunk - 1) / kChunk), listed(q)};
+        AdjustArgs p{q.a, q.ld, q.ldy, 0, (int)q.C, (int)((q.C + kChunk - 1) / kChunk)};
         const int64_t all = q.R * p.chunks;
         hipError_t e = hipSuccess;
         for (; p.first < all && e == hipSuccess; p.first += kMaxGroupsPerLaunch) {
@@ -268,12 +270,14 @@ struct Config {
 // from 512, else of one (us in graphs, GPU alone, 1 / 2 / 4 groups): 64 rows of
 // 128256 bfloat16 with histories of 4096 to 8192 tokens 16.9 / 13.4 / 12.9; 200 of
 // 32003 binary16 with 500 to 1000 tokens and a mask 13.8 / 11.0 / 11.7; one of
-// 128256 binary32 4.5 / 5.0 / 5.8.  Fewer where LDS would not hold the tables.
+// 128256 binary32 4.5 / 5.0 / 5.8.  Four groups of 16-bit logits and 32-bit words
+// (T > 32767) would need 196 KiB of LDS for the table and the list: two.
 template <class E, class W>
 hipError_t adjust_words(const AdjustRows& q, hipStream_t s) {
     const int64_t groups = q.R * ((q.C + Config<E, W, 1>::kChunk - 1) / Config<E, W, 1>::kChunk);
-    if (groups >= 1024 && Config<E, W, 4>::fits(q)) return Config<E, W, 4>::launch(q, s);
-    if (groups >= 512 && Config<E, W, 2>::fits(q)) return Config<E, W, 2>::launch(q, s);
+    if constexpr (sizeof(E) == sizeof(W))
+        if (groups >= 1024) return Config<E, W, 4>::launch(q, s);
+    if (groups >= 512) return Config<E, W, 2>::launch(q, s);
     return Config<E, W, 1>::launch(q, s);
 }
 

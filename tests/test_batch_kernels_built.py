@@ -18,7 +18,7 @@ def built(tmp_path_factory):
         path = str(d / (source + ".s"))
         _build.device_asm(os.path.join(_build.CSRC, source), path)
         return re.findall(r"^\s*\.amdhsa_kernel (\w+)", open(path).read(), re.M)
-    return {s: names(s) for s in ("moe.hip",)}
+    return {s: names(s) for s in ("moe.hip", "adjust.hip")}
 
 
 def arguments(names, pattern):
@@ -40,3 +40,11 @@ def test_down_products(built):
     got = arguments(built["moe.hip"], r"k_moe_downINS0_9Tiles(Q\d)_0ELb(\d)ELb(\d)ELi4ELi(\d)ELi2E")
     assert got == ({(f, many, 0, parts) for f in ("Q4", "Q8") for many in BOTH for parts in (1, 2)} |
                    {("Q4", many, 1, 1) for many in BOTH})
+
+
+def test_adjustments(built):
+    """Type, the table's words (j: 32 bits, t: 16), groups a thread.  32-bit words beside 16-bit logits stand for histories
+    of more than 32767 tokens, whose list and table of four groups are 196 KiB of the 160 that there are."""
+    got = arguments(built["adjust.hip"], r"k_adjustI(f|DF16_|DF16b)(j|t)Li(\d)E")
+    assert got == ({("f", "j", g) for g in (1, 2, 4)} | {(e, "t", g) for e in ("DF16_", "DF16b") for g in (1, 2, 4)} |
+                   {(e, "j", g) for e in ("DF16_", "DF16b") for g in (1, 2)})
