@@ -645,7 +645,10 @@ dg_status dg_sample_rows(const void* x, int dtype, const float* u, const float* 
  *                  outside 0..C-1 is ignored.
  *     lens         int32 [R], or NULL for T everywhere; cut to 0..T.
  *     prompt_lens  int32 [R], or NULL for 0; cut to 0..lens[r].
- *     T, ldt       0 <= T <= ldt < 2^31, T <= 2^30.
+ *     T, ldt       0 <= T <= ldt < 2^31, T <= 2^30.  T is what the call is
+ *                  built for, whatever the lengths are: pass the most tokens
+ *                  that a row has (in a captured call: will have), not the
+ *                  room that there is for them.
  *     repetition   float32 [R], or NULL: off.  0, a negative number, 1 or NaN:
  *                  off for the row.
  *     frequency, presence  float32 [R], or NULL for 0.

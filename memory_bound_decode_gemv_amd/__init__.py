@@ -877,12 +877,13 @@ def dg_sample_rows(x, u, idx, R=None, C=None, ld=None, temperature=None, top_k=N
 
 def dg_adjust_rows(x, y, tokens=None, lens=None, prompt_lens=None, repetition=None, frequency=None, presence=None,
                    bias_ids=None, bias=None, bias_lens=None, mask=None, R=None, C=None, ld=None, ldy=None,
-                   stream=None):
+                   stream=None, T=None):
     """y [R][ldy] = the logits x [R][ld] (both float32, float16 or bfloat16; y may be x) after the penalties of their
-    histories, biases and masks.  tokens: int32 [R][T], the first lens[r] of a row (int32 [R]; None: T) its prompt of
-    prompt_lens[r] tokens (int32 [R]; None: 0), then its output; repetition, frequency, presence: float32 [R];
-    bias_ids, bias: int32 and float32 [R][B], the first bias_lens[r] of a row (int32 [R]; None: B), the last one of a
-    token counts; mask: int32 [R][words], bit c % 32 of word c / 32 set where token c is allowed.  Each may be None."""
+    histories, biases and masks.  tokens: int32 [R][ldt], the first lens[r] of a row (int32 [R]; None: T) its prompt of
+    prompt_lens[r] tokens (int32 [R]; None: 0), then its output; T: the most tokens that a row has (None: ldt, the whole
+    of its room); repetition, frequency, presence: float32 [R]; bias_ids, bias: int32 and float32 [R][B], the first
+    bias_lens[r] of a row (int32 [R]; None: B), the last one of a token counts; mask: int32 [R][words], bit c % 32 of
+    word c / 32 set where token c is allowed.  Each may be None."""
     torch = _torch()
     i32, f32 = torch.int32, torch.float32
     dev = _here(x, "x")
@@ -900,16 +901,17 @@ def dg_adjust_rows(x, y, tokens=None, lens=None, prompt_lens=None, repetition=No
     live = R > 0 and C > 0
     xa = _arg("x", x, dev, x.dtype, ((R - 1) * ld + C) * e if live and ld >= C else 0)
     ya = _arg("y", y, dev, x.dtype, ((R - 1) * ldy + C) * e if live and ldy >= C else 0)
-    T = B = ldm = 0
+    ldt = B = ldm = 0
     if tokens is not None:
-        T = tokens.shape[-1]
+        ldt = tokens.shape[-1]
+    T = ldt if T is None else int(T)
     if bias_ids is not None:
         B = bias_ids.shape[-1]
     if mask is not None:
         ldm = mask.shape[-1]
     a = dg_adjustments(
-        _arg("tokens", tokens, dev, i32, n * T * 4), _arg("lens", lens, dev, i32, n * 4),
-        _arg("prompt_lens", prompt_lens, dev, i32, n * 4), T, T, _arg("repetition", repetition, dev, f32, n * 4),
+        _arg("tokens", tokens, dev, i32, n * ldt * 4), _arg("lens", lens, dev, i32, n * 4),
+        _arg("prompt_lens", prompt_lens, dev, i32, n * 4), T, ldt, _arg("repetition", repetition, dev, f32, n * 4),
         _arg("frequency", frequency, dev, f32, n * 4), _arg("presence", presence, dev, f32, n * 4),
         _arg("bias_ids", bias_ids, dev, i32, n * B * 4), _arg("bias", bias, dev, f32, n * B * 4),
         _arg("bias_lens", bias_lens, dev, i32, n * 4), B, _arg("mask", mask, dev, i32, n * ldm * 4), ldm)
