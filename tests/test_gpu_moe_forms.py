@@ -74,3 +74,15 @@ def test_slots_without_experts(dg, dev, orc, fmt, E, N, K, M, k):
     assert not Y[0].any()
     c.w[(c.ids < 0) | (c.ids >= E)] = np.nan
     assert np.array_equal(Y, c.run("bf16", fill=0xFF)[0])
+
+
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0"])
+@pytest.mark.parametrize("E,N,K,M,k", [(2, 4608, 768, 18, 2), (20, 256, 4608, 8, 20), (4, 4096, 1024, 8, 1)])
+def test_types_of_the_weighted_sum(dg, dev, orc, fmt, E, N, K, M, k):
+    """16-bit outputs are one rounding of the binary32 sums, made by a launch of their own and beside the down products."""
+    import torch
+    c = Large(dg, dev, orc, fmt, 3500 + E, E, N, K, M, distinct((E, M, 1), E, M, k))
+    Y, H = c.check()
+    for out, t in (("f16", torch.float16), ("bf16", torch.bfloat16)):
+        Y16, H16 = c.run(out)
+        assert np.array_equal(Y16, torch.from_numpy(Y).to(t).float().numpy()) and np.array_equal(H, H16)
