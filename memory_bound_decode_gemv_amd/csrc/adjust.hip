@@ -20,11 +20,13 @@
 // marks which entries are the last of their token, and those tokens, which are
 // worked off by the entries.
 //
-// Tokens, logits and mask are on their way before the first wait.  What is left is
-// bound by the steps that follow one another (tokens, table, list, results, stores;
-// three barriers): one row of 128256 binary32 logits 4.5 us, 64 of bfloat16 with
-// histories of 4096 to 8192 12.9 (34 MB, 2.6 TB/s; the vector unit active in a
-// quarter of the busy cycles).
+// The first tokens and, of a chunk without a mask or a partial group, all logits are
+// on their way before the first wait; a group's word of the mask, and each logit of a
+// row's last, partial group, is waited for by itself.  What bounds it are the steps that
+// follow one another (tokens, table, list, results, stores; three barriers), the stores
+// of unchanged logits behind the counts: one row of 128256 binary32 logits 4.5 us, 64 of
+// bfloat16 with histories of 4096 to 8192 12.9, in place too (34 MB, 2.6 TB/s; the vector
+// unit active in a quarter of the busy cycles).
 #include <algorithm>
 
 #include "dg_batch.h"
@@ -92,9 +94,10 @@ __global__ void __launch_bounds__(kThreads) k_adjust(const E* x, E* y, AdjustArg
     const E* const xr = x + r * p.ld + c0;
     E* const yr = y + r * p.ldy + c0;
 
-    // Everything the workgroup reads is on its way before the first wait: the
-    // first tokens (of the T that a row has room for, before its length is
-    // known), the biased tokens, the logits and the mask.
+    // Asked for before anything is worked off: the first tokens (of the T that a row
+    // may have, before its length is known), the biased tokens, the logits and the
+    // mask.  As compiled, a word of the mask and a logit of a partial group are each
+    // waited for where they are read.
     const int T = a.tokens ? (int)a.T : 0;
     const int32_t* const tok = a.tokens + r * a.ldt;
     u32x4 t[kScan];
@@ -271,7 +274,10 @@ struct Config {
 // 128256 bfloat16 with histories of 4096 to 8192 tokens 16.9 / 13.4 / 12.9; 200 of
 // 32003 binary16 with 500 to 1000 tokens and a mask 13.8 / 11.0 / 11.7; one of
 // 128256 binary32 4.5 / 5.0 / 5.8.  Four groups of 16-bit logits and 32-bit words
-// (T > 32767) would need 196 KiB of LDS for the table and the list: two.
+// (T > 32767) would need 196 KiB of LDS for the table and the list: two.  T counts here
+// and for the words, not the lengths, which the host does not know: the 64 rows above
+// 12.7 with T = 8192 and 32767, 16.8 with 65536; the 200 11.3, 12.5 and 16.0 with 1000,
+// 32767 and 65536.
 template <class E, class W>
 hipError_t adjust_words(const AdjustRows& q, hipStream_t s) {
     const int64_t groups = q.R * ((q.C + Config<E, W, 1>::kChunk - 1) / Config<E, W, 1>::kChunk);

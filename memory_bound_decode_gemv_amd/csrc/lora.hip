@@ -19,9 +19,10 @@
 // Their sums are in another order, so a rule between the two would make a row's
 // results depend on the number of rows; they are not used.
 //
-// What bounds it: few rows, the latency of three to four dependent loads; many rows of
-// many adapters, memory (the 200 rows above move 191 MB: h takes 14 us, Y 35); many
-// rows of one adapter, the vector operations.
+// What bounds it: few rows, the latency of dependent loads (the adapter, the runs of A
+// and x, B behind their sums; dot_rows says how many trips a run is); many rows of many
+// adapters, memory for Y (35 us of the 200 rows above, which move 191 MB) and loads waited
+// for one pair at a time for h (14); many rows of one adapter, the vector operations.
 #include <algorithm>
 #include <type_traits>
 
@@ -111,7 +112,11 @@ __device__ __forceinline__ int rows_of(const LoraArgs& a, int64_t w0, int item, 
 constexpr int kDotWaves = 4;
 
 // The dots of a row of x with TR ranks' rows of A, in every lane.  A lane has every
-// 64th run of eight columns, U of them in flight, and adds them in their order.
+// 64th run of eight columns, U of them a turn, and adds them in their order.  How many of
+// a turn's loads are in flight is the compiler's choice: all or nearly all of them for
+// binary32 rows and for binary16 by binary16; of bfloat16 by bfloat16 it waits for each
+// run's two loads before it asks for the next (eight round trips a turn), and so for
+// most runs of the mixed 16-bit pairs.
 template <class EX, class EW, int TR>
 __device__ __forceinline__ void dot_rows(const typename EX::raw* xr, const typename EW::raw* const (&Ar)[TR], int K,
                                          int lane, float (&sum)[TR]) {
@@ -145,8 +150,9 @@ __device__ __forceinline__ void dot_rows(const typename EX::raw* xr, const typen
 }
 
 // h of one row and kDotWaves ranks, one a wave: x and A come from L2 but for their first
-// readers, and what bounds it is the latency of one run of loads where rows are few, the
-// rate of L2 where they are many.  Two or four ranks a wave, for fewer reads of x, were
+// readers, and what bounds it is the round trips of its loads (dot_rows; 200 bfloat16 rows
+// of 8192 columns and 32 ranks make 16 in each of 6400 waves, 13.9 us).  With the loads
+// as they are, two or four ranks a wave, for fewer reads of x, were
 // no faster (24 rows of binary32, K 4096, R 64, with B: 10.6 us with one, 11.5 with two,
 // 13.9 with four; 200 of bfloat16, K 8192, R 32: 54, 56, 56), nor were four rows of one
 // adapter a wave (13 us, 64 us).  Grid: (runs of ranks, rows).

@@ -13,9 +13,15 @@
 // The weights of the chosen experts are nearly all that is read, so large experts
 // are bound by HBM: 32 tokens through 2 of 8 Q8_0 experts of 14336 x 4096 (1.5 GB)
 // 150 + 76 + 4 us, 6.7 TB/s; one token through Q4_0 ones 24.2 + 16.5, 5.4 and 4.0
-// TB/s.  Small experts are bound by the dependent steps of each launch (ids, first
-// weights, products, sums): one token through 8 of 128 of 768 x 2048 8.6 + 5.1 us for
-// 21 MB; between them 24 tokens through 6 of 64 of 1536 x 2048 35 + 19 + 4, 5.4 TB/s.
+// TB/s, the down products held up by the copies of the hidden columns before them
+// (k_moe_down_tokens).  Small experts are bound by the dependent steps of each launch:
+// one token through 8 of 128 of 768 x 2048 8.6 + 5.1 us for 21 MB, in which a wave has
+// two of its row's eight weight groups in flight, so four round trips to memory beside
+// those of the ids, and two of three in the down products.  Between them 24 tokens
+// through 6 of 64 of 1536 x 2048 35 + 19 + 4, 5.4 TB/s.  Many tokens: a workgroup looks
+// through all slots, 128 a round trip, before its first weights, and an expert's weights
+// are read again for every 16 of its tokens (200 tokens through 8 of 128 of 768 x 2048
+// 132 us, 340 MB).
 //
 // A workgroup finds its own work: it reads the ids (at most 4096), and what
 // matches its expert are its columns.  Where there are no more slots than
@@ -50,8 +56,12 @@ constexpr int kTileColumns = 16;
 // their logits are made for the chosen alone, in the lanes that store them; the
 // softmax's sum is left out where the weights are divided by their own.  One token
 // of 64 experts, k 6: 2.6 us, the launch and the choices one after another; 4096 of
-// 256, k 8, with a sigmoid and a bias 8.1, bound by vector instructions: some 600 a
-// wave, issued in half the busy cycles.  Ranks sorted in each lane first, so that a
+// 256, k 8, with a sigmoid and a bias 8.1, of which some 600 vector instructions a
+// wave are issued in half the busy cycles.  The rest is waiting, for the lane moves of
+// the choices (two whole maxima for a 64-bit rank) and for the loads: as compiled, a
+// 16-bit logit, and a logit with its bias, is waited for before the next is asked for
+// (NV trips, 2 NV for 16 bits with a bias); only binary32 logits of softmax without a
+// bias are on their way together.  Ranks sorted in each lane first, so that a
 // choice looks at one a lane: 8.6, and 78 against 11 for 1024 experts.
 // ---------------------------------------------------------------------------
 struct RouteArgs {
@@ -566,7 +576,10 @@ __device__ __forceinline__ void store_y(void* Y, int ydtype, size_t i, float v) 
 // has RT row tiles of one token, a wave (j, rt, kw) its j-th expert's products
 // with that expert's hidden column, so nothing is left to a third launch.  Each
 // token reads its experts' weights for itself.  The order of every sum is that of
-// k_moe_down and k_moe_sum.  Waves: k RT KW.
+// k_moe_down and k_moe_sum.  The columns go into LDS 16 bytes a lane and turn, each turn
+// behind its slot's id and its own load, and the first of these waits is one for the
+// weights sent ahead too: 12 turns of 256 threads for two columns of 14336 (16.5 us for
+// 66 MB).  Waves: k RT KW.
 template <class TF, int RT, int KW, int D>
 __global__ void __launch_bounds__(1024) MOE_WAVES
 k_moe_down_tokens(const uint8_t* __restrict__ Wd, const uint8_t* __restrict__ Hq, const float* __restrict__ weights,
@@ -716,9 +729,11 @@ double live_experts(const MoeLayer& q) {
 // use of the workgroups that are resident together: in units of one row group's
 // weights, `start` before each workgroup's first, and a third of a round for the
 // uneven end of more than one round.  One row group each and as modelled: 24 tokens
-// through 6 of 64 experts of 1536 x 2048 63 and 58 us, 32 through 8 of 128 of 768 x
-// 2048 70 and 63, 16 of the same 57 and 60.  Longer rows and two parts of K: no
-// difference, so their kernels have no such loop.
+// through 6 of 64 experts of 1536 x 2048 60.3 and 58.0 us, 16 53.1 and 52.6, 32 63.2 and
+// 63.7; 24 through 8 of 128 of 768 x 2048 58.5 and 56.0, 32 62.5 and 59.7, 200 138 and 132;
+// 8 through 8 of 64 of 1280 x 2048 42.2 and 40.6.  It is wrong at 16 through 8 of 128,
+// 49.2 and 54.3.  Longer rows and two parts of K: no difference, so their kernels have no
+// such loop.
 template <class TF, int KW>
 constexpr bool kRuns = std::is_same<TF, TilesQ4_0>::value && KW == 1;
 
