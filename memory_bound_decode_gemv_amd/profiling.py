@@ -561,7 +561,8 @@ def resources_markdown(command=""):
              "(the same build flags as the library).  One line per kernel template: ranges over its "
              "instantiations.  `waves/SIMD` is the occupancy the registers allow (the compiler's "
              "\"Occupancy\"); LDS sized at launch (every staged kernel's buffers) is not part of it and "
-             "lowers it further where a workgroup's LDS is large.  Scratch 0 everywhere means no spills.", "",
+             "lowers it further where a workgroup's LDS is large.  Scratch 0 everywhere means no spills to memory; scalar "
+             "registers that do not fit move to lanes of vector registers, which this report does not count.", "",
              f"{len(rows)} kernels in {len(groups)} templates.", "",
              "| source | kernel template | instantiations | VGPRs | AGPRs | SGPRs | static LDS B | scratch B | waves/SIMD |",
              "|---|---|---|---|---|---|---|---|---|"]
